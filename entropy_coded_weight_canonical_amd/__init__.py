@@ -1,7 +1,7 @@
 """Python binding of ``libentro.so`` (ctypes; argument marshalling only).
 
 The names mirror the C ABI of ``include/entro.h`` and ``include/entro_encode.h``
-without the ``entro_`` prefix.  Every step of the decode path runs in the HIP
+without the ``entro_`` prefix (``include/entro_attn.h``: module ``attn``).  Every step of the decode path runs in the HIP
 kernels of the library; this module only converts arguments.  Device buffers
 are torch tensors on the HIP device (``torch.cuda`` is torch's HIP namespace on
 ROCm); streams are torch streams.  If the library is missing, every call
@@ -23,7 +23,11 @@ __all__ = [
     "quantize", "code_lengths", "encode_layout", "encode",
     "rans_freqs", "rans_table_build", "rans_encode", "rans_decode", "rans_decode_dequant",
     "SCHEME_ASYMMETRIC", "SCHEME_UNSIGNED", "SCHEME_MIXED",
+    "KVCache", "attn_prompt", "kv_store", "kv_load", "attn_cache", "attn_cache_work_bytes",
 ]
+
+from . import attn
+from .attn import KVCache, attn_cache, attn_cache_work_bytes, attn_prompt, kv_load, kv_store
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libentro.so")
@@ -36,6 +40,7 @@ _SCHEME_IDS = {v: k for k, v in _SCHEME_NAMES.items()}
 FLAGS = {
     "overrun": 0x01, "underrun": 0x02, "badcode": 0x04,
     "padding": 0x08, "offsets": 0x10, "lut": 0x20,
+    "length": 0x40, "page": 0x80,
 }
 
 
@@ -131,6 +136,7 @@ def load():
                  "entro_rans_freqs", "entro_rans_table_build", "entro_rans_encode", "entro_rans_decode",
                  "entro_rans_decode_dequant"):
         getattr(lib, name).restype = ctypes.c_int
+    attn._bind(lib)
     _lib = lib
     return lib
 

@@ -1,0 +1,430 @@
+// HIP kernels (gfx950) and entry points of the attention over the 8-bit cache:
+// entro_attn_cache.  Layout and definition are in entro_attn.h.
+#include <algorithm>
+
+#include "entro_attn_device.h"
+#include "entro_internal.h"
+
+namespace entro {
+
+constexpr uint32_t kTile = 64;          // tokens a wavefront takes at a time
+constexpr uint32_t kCacheWaves = 4;     // wavefronts per workgroup, interleaved over a chunk's tiles
+constexpr uint32_t kHeadsPerWg = 16;    // query heads of one key/value head (columns of the matrix products)
+constexpr uint32_t kMinChunkTiles = 8;  // tiles of the smallest chunk of a split sequence
+constexpr uint32_t kChunkTarget = 1024; // chunks x head groups that a call is split into at most (beside one per sequence)
+
+struct CacheArg {
+  const int8_t *k_codes, *v_codes;
+  const float *k_scales, *v_scales;
+  const int32_t *table;
+  uint64_t table_stride;
+  uint32_t table_pages, n_seq, n_pages, n_kv;
+  uint32_t page_log2;
+  const char *q;
+  char *out;
+  int64_t q_t, q_h, o_t, o_h;   // bytes
+  const int32_t *lens;
+  uint32_t n_heads, group;      // group: query heads per key/value head
+  uint32_t parts;               // workgroups (of kHeadsPerWg query heads) per key/value head
+  uint32_t items;               // chunks that the workspace holds
+  float scale;                  // times log2(e)
+  float *part_o;                // [items][n_heads][D]
+  f32x2 *part_ml;               // [items][n_heads]: maximum, sum
+  uint32_t *status;
+};
+
+__device__ __forceinline__ uint32_t cache_len(const CacheArg &a, uint32_t b, bool *ok = nullptr) {
+  const int32_t n = a.lens[b];
+  const bool fine = n >= 0 && (uint64_t)n <= ((uint64_t)a.table_pages << a.page_log2);
+  if (ok) *ok = fine;
+  return fine ? (uint32_t)n : 0u;
+}
+
+// The call's chunk: tiles per chunk, so that all sequences together make about
+// kChunkTarget workgroups whatever their lengths.  Computed alike by every
+// wavefront of both kernels from the lengths alone.
+__device__ __forceinline__ uint32_t chunk_tiles(const CacheArg &a, uint32_t lane) {
+  uint64_t sum = 0;
+  for (uint32_t b0 = 0; b0 < a.n_seq; b0 += 64u) {
+    const uint32_t b = b0 + lane;
+    const uint32_t t = b < a.n_seq ? (cache_len(a, b) + kTile - 1u) / kTile : 0u;
+    // 64 terms below 2^25 each
+    sum += (uint32_t)__shfl((int)wave_scan(t, lane), 63, 64);
+  }
+  const uint64_t per = (uint64_t)a.n_kv * a.parts;
+  const uint64_t c = (rfl64(sum) * per + kChunkTarget - 1u) / kChunkTarget;
+  return (uint32_t)min(max(c, (uint64_t)kMinChunkTiles), (uint64_t)1u << 25);   // a sequence has at most 2^25 tiles
+}
+__device__ __forceinline__ uint32_t chunks_of(const CacheArg &a, uint32_t b, uint32_t c) {
+  return max(1u, ((cache_len(a, b) + kTile - 1u) / kTile + c - 1u) / c);
+}
+
+// Four codes of a word as two pairs of f16: the code plus 128 in the low byte
+// of 1024's bits, less 1152 (exact).
+__device__ __forceinline__ u32x2 half4(uint32_t w) {
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  const uint32_t u = w ^ 0x80808080u;
+  const h2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
+  const uint32_t lo = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u), hi = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
+  return (u32x2){__builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, lo) - off),
+                 __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, hi) - off)};
+}
+__device__ __forceinline__ f16v8 half8(uint32_t w0, uint32_t w1) {
+  const u32x2 a = half4(w0), b = half4(w1);
+  return __builtin_bit_cast(f16v8, (u32x4){a.x, a.y, b.x, b.y});
+}
+
+// Factor of a part with maximum m where the parts' is `all`: parts without
+// tokens (both -inf) count with their zeros, NaN passes through.
+__device__ __forceinline__ float join_factor(float m, float all) { return m == all ? 1.0f : exp2_fast(m - all); }
+
+__device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------
+// One workgroup takes a chunk of one sequence's tokens for one key/value head
+// and up to 16 of its query heads; its four wavefronts take every fourth tile
+// of 64 tokens and join their results in LDS.
+//
+// A tile's scores are K Q^T and its product V^T P^T, both on the matrix cores
+// with the query heads as the 16 columns, so that softmax statistics are per
+// column (a lane and the lanes 16, 32, 48 further hold one head) and the
+// weights leave the first product in the lanes where the second wants them:
+// the first product's row 4 g + r of its i-th part is made token
+// 16 g + 4 i + r, and lane group g then holds 16 consecutive tokens, just the
+// 16 bytes of value codes it reads for one dimension.  Nothing of the cache
+// passes through LDS; each code is read once, 16 bytes a lane.
+//
+// Codes become f16 exactly; q is brought to f16 by a power of two (exact but
+// for values 2^-24 below the row's largest).  With t = s + log2(value scale)
+// and M its running maximum, weights are held as 2^(t - M + 15): the scale of
+// a page's values rides in the exponent, and f16 covers weights down to 2^-29
+// of the largest with 11 bits.  The sum of the softmax is of the same numbers
+// before rounding, divided by the value scale, in 32 bits.
+// ---------------------------------------------------------------------------
+template <entro_dtype T, int D>
+__global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
+  constexpr int S64 = D / 64;            // 64-dimension parts of a key row read as 16 bytes a lane
+  constexpr bool S32 = (D % 64) != 0;    // and one of 32 read as 8
+  constexpr int KS = D / 32;             // matrix products over the dimensions
+  constexpr int DT = D / 16;             // 16-dimension parts of the output
+  __shared__ float red_o[kCacheWaves][kHeadsPerWg][D + 4];
+  __shared__ f32x2 red_ml[kCacheWaves][kHeadsPerWg];
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+  const uint32_t n = lane & 15u, g = lane >> 4;
+  const uint32_t kvh = blockIdx.y / a.parts, h0 = (blockIdx.y % a.parts) * kHeadsPerWg;
+  const uint32_t heads = min(kHeadsPerWg, a.group - h0);
+  const uint32_t head0 = kvh * a.group + h0;
+  const uint32_t page = 1u << a.page_log2;
+  if (blockIdx.x == 0u && blockIdx.y == 0u)
+    for (uint32_t b = tid; b < a.n_seq; b += 256u) {
+      bool ok;
+      cache_len(a, b, &ok);
+      if (!ok) atomicOr(a.status + b, ENTRO_F_LENGTH);
+    }
+  const uint32_t ct = chunk_tiles(a, lane);
+  for (uint32_t item = blockIdx.x;; item += gridDim.x) {
+    const Found f = find_item(item, a.n_seq, lane, [&](uint32_t b) { return chunks_of(a, b, ct); });
+    if (f.seq == a.n_seq) break;
+    const uint32_t len = cache_len(a, f.seq);
+    const uint32_t tile_end = min((f.local + 1u) * ct, (len + kTile - 1u) / kTile);
+    const int32_t *row = a.table + (uint64_t)f.seq * a.table_stride;
+
+    // the query head of this lane's column, as f16 times 2^-e
+    f16v8 qf[KS];
+    float c;                               // score = c * key scale * product
+    {
+      u32x4 raw[KS];
+      const char *q = a.q + f.seq * a.q_t + (int64_t)(head0 + min(n, heads - 1u)) * a.q_h;
+#pragma unroll
+      for (int s = 0; s < S64; ++s) {
+        raw[2 * s] = *reinterpret_cast<const u32x4 *>(q + (64 * s + 16 * g) * 2);
+        raw[2 * s + 1] = *reinterpret_cast<const u32x4 *>(q + (64 * s + 16 * g + 8) * 2);
+      }
+      if (S32) raw[KS - 1] = *reinterpret_cast<const u32x4 *>(q + (64 * S64 + 8 * g) * 2);
+      float top = 0.0f;
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(Elem<T>::lo(raw[s][e])), fabsf(Elem<T>::hi(raw[s][e]))));
+      top = max32(max16(top));
+      int e2 = 0;
+      if (T == ENTRO_BF16) e2 = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;   // bf16 denormals: -127
+      c = ldexpf(a.scale, e2);
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        if (T == ENTRO_F16) {
+          qf[s] = __builtin_bit_cast(f16v8, raw[s]);
+        } else {
+          u32x4 w;
+          for (int e = 0; e < 4; ++e)
+            w[e] = Elem<ENTRO_F16>::pack2(ldexpf(Elem<T>::lo(raw[s][e]), -e2), ldexpf(Elem<T>::hi(raw[s][e]), -e2));
+          qf[s] = __builtin_bit_cast(f16v8, w);
+        }
+      }
+    }
+
+    f32x4 o[DT];
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    float m = -INFINITY, l = 0.0f;   // l: this lane's tokens only
+    bool bad = false;
+
+    for (uint32_t tile = f.local * ct + wave; tile < tile_end; tile += kCacheWaves) {
+      // pages of the 16-token blocks that this lane reads keys of (n / 4) and
+      // values of (g); a block past the end, or of a page that does not exist,
+      // reads page 0 and counts as hidden
+      const uint32_t bk = tile * 4u + (n >> 2), bv = tile * 4u + g;
+      const uint32_t tk = bk * 16u, tv = bv * 16u;
+      int32_t pk = tk < len ? row[tk >> a.page_log2] : 0, pv = tv < len ? row[tv >> a.page_log2] : 0;
+      const bool v_bad = pv < 0 || (uint32_t)pv >= a.n_pages;
+      if (pk < 0 || (uint32_t)pk >= a.n_pages) pk = 0;
+      if (v_bad) pv = 0;
+      bad |= v_bad;
+      const uint32_t rk = (tk & (page - 1u)) + (n & 3u), rv = tv & (page - 1u);
+      const uint64_t ak = (uint64_t)(uint32_t)pk * a.n_kv + kvh, av = (uint64_t)(uint32_t)pv * a.n_kv + kvh;
+      const int8_t *kp = a.k_codes + ((ak << a.page_log2) + rk) * D;
+      const int8_t *vp = a.v_codes + ((av * D + n) << a.page_log2) + rv;
+      u32x4 kq[4][S64];
+      u32x2 kq2[4];
+      u32x4 vq[DT];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int s = 0; s < S64; ++s) kq[i][s] = *reinterpret_cast<const u32x4 *>(kp + 4 * i * D + 64 * s + 16 * g);
+        if (S32) kq2[i] = *reinterpret_cast<const u32x2 *>(kp + 4 * i * D + 64 * S64 + 8 * g);
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) vq[d] = *reinterpret_cast<const u32x4 *>(vp + ((uint64_t)(16 * d) << a.page_log2));
+      const float ks = a.k_scales[av] * c;   // rows 4 g + r of the products are tokens of block g
+      const float vs = fmaxf(a.v_scales[av], 1.17549435e-38f);
+
+      f32x4 s4[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s4[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int s = 0; s < S64; ++s) {
+          s4[i] = mfma16(half8(kq[i][s].x, kq[i][s].y), qf[2 * s], s4[i]);
+          s4[i] = mfma16(half8(kq[i][s].z, kq[i][s].w), qf[2 * s + 1], s4[i]);
+        }
+        if (S32) s4[i] = mfma16(half8(kq2[i].x, kq2[i].y), qf[KS - 1], s4[i]);
+      }
+      // scores in powers of two, with the value scale's logarithm
+      const float lv = __log2f(vs), iv = 1.0f / vs;
+      const uint32_t seen = v_bad || tv >= len ? 0u : min(16u, len - tv);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        for (int r = 0; r < 4; ++r) {
+          const float t = (uint32_t)(4 * i + r) < seen ? s4[i][r] * ks + lv : -INFINITY;
+          s4[i][r] = t;
+          mx = fmaxf(mx, t);
+        }
+      mx = max32(max16(mx));
+      if (__any(mx > m)) {
+        const float mn = fmaxf(m, mx);
+        const float k = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+        m = mn;
+        l *= k;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] *= k;
+      }
+      const float off = m == -INFINITY ? 0.0f : m - 15.0f;
+      float sum = 0.0f;
+      u32x4 pw[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float p[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          p[r] = exp2_fast(s4[i][r] - off);
+          sum += p[r];
+        }
+        pw[i >> 1][2 * (i & 1)] = Elem<ENTRO_F16>::pack2(p[0], p[1]);
+        pw[i >> 1][2 * (i & 1) + 1] = Elem<ENTRO_F16>::pack2(p[2], p[3]);
+      }
+      l += seen ? sum * iv : 0.0f;
+      const f16v8 p0 = __builtin_bit_cast(f16v8, pw[0]), p1 = __builtin_bit_cast(f16v8, pw[1]);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        o[d] = mfma16(half8(vq[d].x, vq[d].y), p0, o[d]);
+        o[d] = mfma16(half8(vq[d].z, vq[d].w), p1, o[d]);
+      }
+    }
+    if (bad) atomicOr(a.status + f.seq, ENTRO_F_PAGE);
+    l = add32(add16(l));
+
+    // join the wavefronts
+    if (g == 0u) red_ml[wave][n] = (f32x2){m, l};
+#pragma unroll
+    for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(&red_o[wave][n][16 * d + 4 * g]) = o[d];
+    __syncthreads();
+    const bool whole = chunks_of(a, f.seq, ct) == 1u;
+    for (uint32_t i = tid; i < heads * (D / 2u); i += 256u) {
+      const uint32_t h = i / (D / 2u), d = i % (D / 2u) * 2u;
+      float mm = -INFINITY;
+#pragma unroll
+      for (uint32_t w = 0; w < kCacheWaves; ++w) mm = fmaxf(mm, red_ml[w][h].x);
+      float x = 0.0f, y = 0.0f, ll = 0.0f;
+#pragma unroll
+      for (uint32_t w = 0; w < kCacheWaves; ++w) {
+        const float k = join_factor(red_ml[w][h].x, mm);
+        x += k * red_o[w][h][d];
+        y += k * red_o[w][h][d + 1u];
+        ll += k * red_ml[w][h].y;
+      }
+      if (whole) {
+        const float r = ll > 0.0f ? 1.0f / ll : ll == 0.0f ? 0.0f : ll;   // NaN stays
+        *reinterpret_cast<uint32_t *>(a.out + f.seq * a.o_t + (int64_t)(head0 + h) * a.o_h + d * 2u) =
+            Elem<T>::pack2(x * r, y * r);
+      } else {
+        const uint64_t at = (uint64_t)item * a.n_heads + head0 + h;
+        *reinterpret_cast<f32x2 *>(a.part_o + at * D + d) = (f32x2){x, y};
+        if (d == 0u) a.part_ml[at] = (f32x2){mm, ll};
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Joins the chunks of a split sequence in their order: one workgroup per
+// sequence and query head; four groups of 64 threads take every fourth chunk
+// (two dimensions a thread), then the groups are joined.
+template <entro_dtype T, int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(CacheArg a) {
+  __shared__ float red[4][D + 2];
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, group = tid >> 6;
+  const uint32_t b = blockIdx.x, head = blockIdx.y;
+  const uint32_t ct = chunk_tiles(a, lane);
+  const uint32_t n = chunks_of(a, b, ct);
+  if (n == 1u) return;
+  uint32_t first = 0;
+  for (uint32_t b0 = 0; b0 < b; b0 += 64u) {
+    const uint32_t own = b0 + lane < b ? chunks_of(a, b0 + lane, ct) : 0u;
+    first += (uint32_t)__shfl((int)wave_scan(own, lane), 63, 64);
+  }
+  const f32x2 *ml = a.part_ml + (uint64_t)first * a.n_heads + head;
+  const float *po = a.part_o + ((uint64_t)first * a.n_heads + head) * D;
+  float m = -INFINITY;
+  for (uint32_t i = lane; i < n; i += 64u) m = fmaxf(m, ml[(uint64_t)i * a.n_heads].x);
+  for (int s = 32; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
+  const uint32_t d = lane * 2u;
+  float x = 0.0f, y = 0.0f, l = 0.0f;
+#pragma unroll 4
+  for (uint32_t i = group; i < n; i += 4u) {
+    const f32x2 v = ml[(uint64_t)i * a.n_heads];
+    const float k = join_factor(v.x, m);
+    l += k * v.y;
+    if (d < D) {
+      const f32x2 p = *reinterpret_cast<const f32x2 *>(po + (uint64_t)i * a.n_heads * D + d);
+      x += k * p.x;
+      y += k * p.y;
+    }
+  }
+  if (d < D) {
+    red[group][d] = x;
+    red[group][d + 1u] = y;
+  }
+  if (lane == 0u) red[group][D] = l;
+  __syncthreads();
+  if (group == 0u && d < D) {
+    for (int w = 1; w < 4; ++w) {
+      x += red[w][d];
+      y += red[w][d + 1u];
+      l += red[w][D];
+    }
+    const float r = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+    *reinterpret_cast<uint32_t *>(a.out + b * a.o_t + head * a.o_h + d * 2u) = Elem<T>::pack2(x * r, y * r);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+
+static uint64_t cache_items(uint64_t n_seq, uint64_t n_kv, uint64_t parts) {
+  // every sequence has at most one chunk more than its tiles / chunk
+  return n_seq + kChunkTarget / (n_kv * parts) + 1u;
+}
+
+template <entro_dtype T, int D>
+static entro_status launch_cache(CacheArg &a, hipStream_t s) {
+  a.part_ml = reinterpret_cast<f32x2 *>(a.part_o + (uint64_t)a.items * a.n_heads * D);
+  const uint32_t y = a.n_kv * a.parts;
+  // no sequence can have a second chunk: no second launch, no idle workgroups
+  const uint64_t tiles = (((uint64_t)a.table_pages << a.page_log2) + kTile - 1u) / kTile;
+  const bool split = tiles > kMinChunkTiles;
+  uint64_t grid = split ? a.items : a.n_seq;
+  grid = std::max<uint64_t>(1, cap_grid(grid * y) / y);
+  (void)hipGetLastError();
+  hipLaunchKernelGGL((attn_cache_kernel<T, D>), dim3((uint32_t)grid, y), dim3(256), 0, s, a);
+  if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
+  if (split) {
+    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(a.n_seq, a.n_heads), dim3(256), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
+  }
+  return ENTRO_OK;
+}
+
+}  // namespace entro
+
+using namespace entro;
+
+extern "C" uint64_t entro_attn_cache_work_bytes(uint32_t n_seq, uint32_t n_heads, uint32_t n_kv_heads, uint32_t head_dim) {
+  if (n_seq == 0 || check_heads(n_heads, n_kv_heads, head_dim, ENTRO_BF16) != ENTRO_OK) return 0;
+  const uint64_t parts = (n_heads / n_kv_heads + kHeadsPerWg - 1u) / kHeadsPerWg;
+  return cache_items(n_seq, n_kv_heads, parts) * n_heads * (head_dim + 2ull) * 4ull;
+}
+
+extern "C" entro_status entro_attn_cache(const entro_kv_cache *c, const entro_kv_table *t, const entro_attn_cache_args *a,
+                                         uint32_t *d_status, hipStream_t stream) {
+  if (!a) return ENTRO_E_INVAL;
+  entro_status st = check_cache(c, t);
+  if (st != ENTRO_OK) return st;
+  st = check_heads(a->n_heads, c->n_kv_heads, c->head_dim, a->dtype);
+  if (st != ENTRO_OK) return st;
+  if (!std::isfinite(a->scale)) return ENTRO_E_INVAL;
+  if (t->n_seq == 0) return ENTRO_OK;
+  if (!a->d_lens || !d_status || !a->d_work || (reinterpret_cast<uintptr_t>(a->d_work) & 15u)) return ENTRO_E_INVAL;
+  for (const entro_rows *r : {&a->q, &a->out}) {
+    st = check_rows(*r, t->n_seq);
+    if (st != ENTRO_OK) return st;
+  }
+  if (a->work_bytes < entro_attn_cache_work_bytes(t->n_seq, a->n_heads, c->n_kv_heads, c->head_dim)) return ENTRO_E_INVAL;
+  CacheArg k{};
+  k.k_codes = c->d_k_codes;
+  k.v_codes = c->d_v_codes;
+  k.k_scales = c->d_k_scales;
+  k.v_scales = c->d_v_scales;
+  k.table = t->d_table;
+  k.table_stride = t->table_stride;
+  k.table_pages = t->table_pages;
+  k.n_seq = t->n_seq;
+  k.n_pages = c->n_pages;
+  k.n_kv = c->n_kv_heads;
+  k.page_log2 = c->page_tokens == 16u ? 4u : c->page_tokens == 32u ? 5u : c->page_tokens == 64u ? 6u : 7u;
+  k.q = static_cast<const char *>(a->q.d);
+  k.out = static_cast<char *>(a->out.d);
+  k.q_t = 2 * a->q.stride_t;
+  k.q_h = 2 * a->q.stride_h;
+  k.o_t = 2 * a->out.stride_t;
+  k.o_h = 2 * a->out.stride_h;
+  k.lens = a->d_lens;
+  k.n_heads = a->n_heads;
+  k.group = a->n_heads / c->n_kv_heads;
+  k.parts = (k.group + kHeadsPerWg - 1u) / kHeadsPerWg;
+  const uint64_t items = cache_items(t->n_seq, k.n_kv, k.parts);
+  if (items > 0x7FFFFFFFull) return ENTRO_E_UNSUPPORTED;
+  k.items = (uint32_t)items;
+  k.scale = a->scale * kLog2e;
+  k.part_o = static_cast<float *>(a->d_work);
+  k.status = d_status;
+  if (a->dtype == ENTRO_BF16)
+    return c->head_dim == 64u   ? launch_cache<ENTRO_BF16, 64>(k, stream)
+           : c->head_dim == 96u ? launch_cache<ENTRO_BF16, 96>(k, stream)
+                                : launch_cache<ENTRO_BF16, 128>(k, stream);
+  return c->head_dim == 64u   ? launch_cache<ENTRO_F16, 64>(k, stream)
+         : c->head_dim == 96u ? launch_cache<ENTRO_F16, 96>(k, stream)
+                              : launch_cache<ENTRO_F16, 128>(k, stream);
+}

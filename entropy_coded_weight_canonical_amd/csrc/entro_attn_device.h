@@ -1,0 +1,165 @@
+// Device and host helpers shared by the attention and cache kernels
+// (entro_attn_prompt.hip, entro_kv.hip, entro_attn_cache.hip): element types,
+// matrix-core fragments, reductions, and the search that turns a workgroup's
+// number into a place in one of the call's sequences.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "entro_attn.h"
+#include "entro_device.h"
+
+namespace entro {
+
+typedef __bf16 bf16v8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16v8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// The two 16-bit element types.  pack2 rounds two floats to nearest even into
+// one word, the first in the low half.  kInf: the magnitude bits from which a
+// value is infinite or NaN.
+template <entro_dtype T>
+struct Elem;
+template <>
+struct Elem<ENTRO_BF16> {
+  typedef __bf16 type;
+  typedef bf16v8 v8;
+  static constexpr uint32_t kInf = 0x7F80u;
+  __device__ static float lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
+  __device__ static float hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xFFFF0000u); }
+  __device__ static uint32_t pack2(float a, float b) {
+    typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, v2));
+  }
+  __device__ static f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+};
+template <>
+struct Elem<ENTRO_F16> {
+  typedef _Float16 type;
+  typedef f16v8 v8;
+  typedef _Float16 v2 __attribute__((ext_vector_type(2)));
+  static constexpr uint32_t kInf = 0x7C00u;
+  __device__ static float lo(uint32_t w) { return (float)__builtin_bit_cast(v2, w).x; }
+  __device__ static float hi(uint32_t w) { return (float)__builtin_bit_cast(v2, w).y; }
+  __device__ static uint32_t pack2(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, v2));
+  }
+  __device__ static f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
+  }
+};
+
+// 2^x in one instruction (x below -126 gives a denormal or 0)
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Maximum or sum over the lane pairs 32 (16) apart, in both lanes.
+__device__ __forceinline__ float max32(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float add32(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+__device__ __forceinline__ float max16(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+__device__ __forceinline__ float add16(float v) {
+  const uint32_t u = __builtin_bit_cast(uint32_t, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+// Inclusive running sum over the wavefront's lanes.
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t lane) {
+  for (uint32_t s = 1; s < 64u; s <<= 1) {
+    const uint32_t o = (uint32_t)__shfl_up((int)v, s, 64);
+    if (lane >= s) v += o;
+  }
+  return v;
+}
+
+// The sequence whose items include number `item` when the sequences' items
+// (count(b) of them) are numbered one after another, and the item's number
+// within it.  Every lane of the wavefront returns the same; seq = n_seq where
+// there are fewer items.  64 sequences a step.
+struct Found {
+  uint32_t seq, local;
+};
+template <typename Count>
+__device__ __forceinline__ Found find_item(uint32_t item, uint32_t n_seq, uint32_t lane, Count count) {
+  uint32_t before = 0;
+  for (uint32_t b0 = 0; b0 < n_seq; b0 += 64u) {
+    const uint32_t b = b0 + lane;
+    const uint32_t own = b < n_seq ? count(b) : 0u;
+    const uint32_t run = wave_scan(own, lane);
+    const uint64_t past = __ballot(before + run > item);
+    if (past) {
+      const uint32_t at = (uint32_t)__builtin_ctzll(past);
+      const uint32_t begin = before + (uint32_t)__shfl((int)(run - own), (int)at, 64);
+      return {rfl(b0 + at), rfl(item - begin)};
+    }
+    before += (uint32_t)__shfl((int)run, 63, 64);
+  }
+  return {n_seq, 0u};
+}
+
+// Rows of sequence b from its running sums, with what is wrong with them.
+struct Span {
+  uint32_t begin, count;
+  bool ok;
+};
+__device__ __forceinline__ Span span_of(const int32_t *cu, uint32_t b, uint32_t total) {
+  const int32_t lo = cu[b], hi = cu[b + 1];
+  const bool ok = lo >= 0 && hi >= lo && (uint32_t)hi <= total;
+  return {ok ? (uint32_t)lo : 0u, ok ? (uint32_t)(hi - lo) : 0u, ok};
+}
+
+// host side: one 16-bit operand
+inline entro_status check_rows(const entro_rows &r, uint32_t rows) {
+  if (rows == 0) return ENTRO_OK;
+  if (!r.d || (reinterpret_cast<uintptr_t>(r.d) & 15u)) return ENTRO_E_INVAL;
+  if ((r.stride_t & 7) || (r.stride_h & 7)) return ENTRO_E_INVAL;
+  if (r.stride_t < 0 || r.stride_h < 0) return ENTRO_E_INVAL;
+  return ENTRO_OK;
+}
+
+inline bool head_dim_ok(uint32_t d) { return d == 64u || d == 96u || d == 128u; }
+
+inline entro_status check_heads(uint32_t n_heads, uint32_t n_kv, uint32_t dim, int dtype) {
+  if (n_heads == 0 || n_kv == 0 || n_heads % n_kv) return ENTRO_E_INVAL;
+  if (dtype != ENTRO_BF16 && dtype != ENTRO_F16) return ENTRO_E_INVAL;
+  if (!head_dim_ok(dim) || n_heads > 65535u) return ENTRO_E_UNSUPPORTED;
+  return ENTRO_OK;
+}
+
+inline entro_status check_cache(const entro_kv_cache *c, const entro_kv_table *t) {
+  if (!c || !t) return ENTRO_E_INVAL;
+  if (t->n_seq == 0) return ENTRO_OK;
+  if (c->page_tokens != 16u && c->page_tokens != 32u && c->page_tokens != 64u && c->page_tokens != 128u)
+    return ENTRO_E_FORMAT;
+  if (!head_dim_ok(c->head_dim) || c->n_kv_heads > 65535u) return ENTRO_E_UNSUPPORTED;
+  if (c->n_kv_heads == 0 || c->n_pages == 0 || c->n_pages > 0x7FFFFFFFu) return ENTRO_E_INVAL;
+  if (!c->d_k_codes || !c->d_v_codes || !c->d_k_scales || !c->d_v_scales || !t->d_table) return ENTRO_E_INVAL;
+  if ((reinterpret_cast<uintptr_t>(c->d_k_codes) | reinterpret_cast<uintptr_t>(c->d_v_codes)) & 15u)
+    return ENTRO_E_INVAL;
+  if (t->table_pages == 0 || t->table_pages > t->table_stride) return ENTRO_E_INVAL;
+  // positions are 31-bit numbers
+  if ((uint64_t)t->table_pages * c->page_tokens > 0x7FFFFFFFull || t->n_seq > 0x7FFFFFFFu) return ENTRO_E_UNSUPPORTED;
+  return ENTRO_OK;
+}
+
+}  // namespace entro
