@@ -32,37 +32,19 @@ constexpr float kLift = T == ENTRO_F16 ? 12.0f : 0.0f;
 template <entro_dtype T>
 constexpr float kLag = T == ENTRO_F16 ? 3.0f : 8.0f;
 
-// Whether one of the eight 16-bit values is infinite or NaN.
+// The 16-bit values of w that are infinite or NaN: 0x8000 in their places.
 template <entro_dtype T>
-__device__ __forceinline__ bool special(u32x4 w) {
+__device__ __forceinline__ uint32_t special(uint32_t w) {
   constexpr uint32_t exps = Elem<T>::kInf * 0x10001u, one = (0x8000u - Elem<T>::kInf) * 0x10001u;
-  uint32_t any = 0;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) any |= (w[e] & exps) + one;   // a full exponent carries into bit 15
-  return (any & 0x80008000u) != 0u;
+  return ((w & exps) + one) & 0x80008000u;   // a full exponent carries into bit 15
 }
 
-// acc + w p for 16 tokens (token 8 (j / 4) + 4 half + j % 4 is element j of a
-// half) that hold infinities or NaN, where some queries must not see some of
-// the tokens: 0 * inf would reach them.  One product a token, added where the
-// lane's query sees it (`seen`: its tokens here, from the first on).
+// w with zeros in the place of infinities and NaN.
 template <entro_dtype T>
-__device__ __forceinline__ f32x16 mfma_seen(u32x4 w, u32x4 p, f32x16 acc, uint32_t half, int seen) {
-#pragma unroll 1
-  for (uint32_t t = 0; t < 16u; ++t) {
-    const uint32_t j = (t & 3u) + 4u * (t >> 3);
-    const bool mine = half == ((t >> 2) & 1u);
-    u32x4 x;
+__device__ __forceinline__ u32x4 without_special(u32x4 w) {
 #pragma unroll
-    for (uint32_t e = 0; e < 4; ++e) x[e] = mine && e == j / 2u ? w[e] & (0xFFFFu << (16u * (j & 1u))) : 0u;
-    f32x16 add;
-#pragma unroll
-    for (int r = 0; r < 16; ++r) add[r] = 0.0f;
-    add = Elem<T>::mfma32(x, p, add);
-#pragma unroll
-    for (int r = 0; r < 16; ++r) acc[r] += (int)t < seen ? add[r] : 0.0f;
-  }
-  return acc;
+  for (int e = 0; e < 4; ++e) w[e] &= ~((special<T>(w[e]) >> 15) * 0xFFFFu);
+  return w;
 }
 
 // LDS place (16-byte piece) of piece c of row r of a tile of keys or values.
@@ -80,22 +62,36 @@ __device__ __forceinline__ uint32_t value_piece(uint32_t r, uint32_t c) {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
+
+// o *= k in the registers that hold o: written as a product, the two ways
+// through the (rare) branch around it get registers of their own, and the
+// common way copies all outputs every tile.
+__device__ __forceinline__ void scale_in_place(f32x16 &o, float k) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    float x = o[r];
+    asm volatile("v_mul_f32 %0, %1, %0" : "+v"(x) : "v"(k));
+    o[r] = x;
+  }
+}
+
+// Instructions stay on their side of this place.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
 // Four rows (tokens) of 16 columns turned: a lane of a group of 16 gives the
 // address of row lane / 4, columns 4 (lane % 4) on, and receives the four rows
 // of column lane % 16.
-__device__ __forceinline__ u32x2 read_turned(uint32_t at) {
-  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(uintptr_t)at));
+__device__ __forceinline__ u32x2 read_turned(const void *at) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)at));
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup takes 128 QB queries of one sequence and head, a wavefront 32 QB
-// of them; the keys come in tiles of 64 that all four wavefronts read from
-// LDS, two tiles in turn: the next one's copies (global memory to LDS, 16
-// bytes a lane) are in flight while one is computed, one barrier a tile.
-// Copies go through a buffer resource that ends with the sequence's last row,
-// so rows past it arrive as zeros.
+// One workgroup takes 128 queries of one sequence and head, a wavefront 32 of
+// them; the keys come in tiles of 64 that all four wavefronts read from LDS,
+// two tiles in turn: the next one's copies (global memory to LDS, 16 bytes a
+// lane) are in flight while one is computed, one barrier a tile.  Copies go
+// through a buffer resource that ends with the sequence's last row, so rows
+// past it arrive as zeros.
 //
 // Scores are K Q^T and outputs V^T P^T with the queries as columns: a lane and
 // the one 32 further hold one query's softmax, whose statistics need one
@@ -103,12 +99,21 @@ __device__ __forceinline__ u32x2 read_turned(uint32_t at) {
 // the order in which the second takes them (row 8 (r / 4) + 4 half + r % 4 of a
 // product is element r of a half; the values' tokens are read in that order).
 // Values are turned on the way from LDS to registers.
+//
+// Values that a query must not see have weight 0, and 0 times an infinity
+// would reach it: a tile that some queries see in part is looked over by the
+// wavefronts that copied it, and where it holds infinities or NaN these are
+// left out of the product and added at the end, to the queries that see them.
 // ---------------------------------------------------------------------------
-template <entro_dtype T, int D, int QB>
-__global__ __launch_bounds__(256, QB == 1 ? 2 : 1) void attn_prompt_kernel(PromptArg a) {
+template <entro_dtype T, int D>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_prompt_kernel(PromptArg a) {
   constexpr int KS = D / 16, DT = D / 32, N = D / 32;
   constexpr uint32_t kBytes = kTile * D * 2u, kPieces = D / 8u;   // of a tile, of a row
-  constexpr uint32_t kQueries = 32u * QB, kRows = kQueries * kWaves4;
+  constexpr uint32_t kQueries = 32u, kRows = kQueries * kWaves4;
+  // four arrays: the compiler then knows that copies into one tile's need not
+  // be waited for before the other's are read
+  __shared__ u32x4 lds_k0[kBytes / 16u], lds_k1[kBytes / 16u], lds_v0[kBytes / 16u], lds_v1[kBytes / 16u];
+  __shared__ uint32_t lds_special[2];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = rfl(tid >> 6), n = lane & 31u, half = lane >> 5;
   if (blockIdx.x == 0u)
     for (uint32_t b = tid; b < a.n_seq; b += 256u)
@@ -122,10 +127,6 @@ __global__ __launch_bounds__(256, QB == 1 ? 2 : 1) void attn_prompt_kernel(Promp
     k_off[s] = r * (uint32_t)a.k_t + key_piece<D>(r, c) * 16u;
     v_off[s] = r * (uint32_t)a.v_t + value_piece<D>(r, c) * 16u;
   }
-  // and of its reads: keys of row n, values of rows 4 half + (lane / 4) % 4
-  const uint32_t k_row = n * (2u * D);
-  const uint32_t v_r = 4u * half + ((lane >> 2) & 3u), v_c = 2u * ((lane >> 4) & 1u) + ((lane >> 1) & 1u);
-  const uint32_t v_row = v_r * (2u * D) + (lane & 1u) * 8u;
 
   for (uint64_t id = blockIdx.x;; id += gridDim.x) {
     // a key/value head's query heads and tiles stay on one XCD (workgroups go
@@ -140,174 +141,222 @@ __global__ __launch_bounds__(256, QB == 1 ? 2 : 1) void attn_prompt_kernel(Promp
     const uint32_t count_q = rfl(sq.count), count_k = rfl(sk.count), begin_q = rfl(sq.begin), begin_k = rfl(sk.begin);
     // the last queries first: they have the most keys
     const uint32_t wg0 = ((count_q + kRows - 1u) / kRows - 1u - f.local) * kRows;
-    const uint32_t q0 = wg0 + wave * kQueries;
+    const uint32_t q0 = wg0 + wave * kQueries, qi = q0 + n;
     const int64_t shift = (int64_t)count_k - count_q;       // query i sees keys up to i + shift
     const char *kb = a.k + begin_k * a.k_t + kvh * a.k_h, *vb = a.v + begin_k * a.v_t + kvh * a.v_h;
 
-    u32x4 qf[QB][KS];
-#pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      const char *qp = a.q + (int64_t)(begin_q + min(q0 + 32u * b + n, count_q - 1u)) * a.q_t + head * a.q_h;
+    u32x4 qf[KS];
+    {
+      const char *qp = a.q + (int64_t)(begin_q + min(qi, count_q - 1u)) * a.q_t + head * a.q_h;
 #pragma unroll
       for (int s = 0; s < KS; ++s)
-        qf[b][s] = (*reinterpret_cast<const u32x4 *>(qp + s * 32 + half * 16) & a.q_and) ^ a.q_xor;
+        qf[s] = (*reinterpret_cast<const u32x4 *>(qp + s * 32 + half * 16) & a.q_and) ^ a.q_xor;
     }
-    f32x16 o[QB][DT];
-    float m[QB], l[QB];
+    f32x16 o[DT];
+    float m = -INFINITY, l = 0.0f;   // l: this lane's keys only
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      m[b] = -INFINITY;
-      l[b] = 0.0f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-        for (int r = 0; r < 16; ++r) o[b][d][r] = 0.0f;
-    }
+    for (int d = 0; d < DT; ++d)
+      for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
     // keys that the workgroup, and this wavefront, see
     const int64_t wg_end = max((int64_t)0, (int64_t)min(wg0 + kRows, count_q) + shift);
     const int64_t my_end = q0 < count_q ? max((int64_t)0, (int64_t)min(q0 + kQueries, count_q) + shift) : 0;
-    const int64_t full_end = (int64_t)q0 + shift + 1;       // keys that every query of the wavefront sees
     const uint32_t tiles = (uint32_t)((wg_end + kTile - 1) / kTile);
+    const uint32_t mine = (uint32_t)((my_end + kTile - 1) / kTile);
+    // tiles that every query of the workgroup sees whole, an even number
+    const uint32_t full = (uint32_t)min((int64_t)tiles, max((int64_t)0, (int64_t)wg0 + shift + 1) / kTile) & ~1u;
 
-    auto copy = [&](uint32_t tile, uint32_t buf) {
+    auto copy = [&](uint32_t tile, u32x4 *to_k, u32x4 *to_v) {
       const uint32_t rows = min(kTile, count_k - tile * kTile);
       const __amdgpu_buffer_rsrc_t rk = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<char *>(kb + (int64_t)(tile * kTile) * a.k_t), 0, (int)((rows - 1u) * (uint32_t)a.k_t + 2u * D), 0x00020000);
       const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<char *>(vb + (int64_t)(tile * kTile) * a.v_t), 0, (int)((rows - 1u) * (uint32_t)a.v_t + 2u * D), 0x00020000);
-      const uint32_t to = buf * (2u * kBytes) + wave * N * 1024u;
 #pragma unroll
       for (uint32_t s = 0; s < (uint32_t)N; ++s)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_void *)(uintptr_t)(to + s * 1024u), 16, (int)k_off[s], 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_void *)(to_k + (wave * N + s) * 64u), 16, (int)k_off[s], 0, 0, 0);
 #pragma unroll
       for (uint32_t s = 0; s < (uint32_t)N; ++s)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void *)(uintptr_t)(to + kBytes + s * 1024u), 16, (int)v_off[s], 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void *)(to_v + (wave * N + s) * 64u), 16, (int)v_off[s], 0, 0, 0);
     };
-    __syncthreads();   // the last item's tiles have been read
-    if (tiles) copy(0, 0);
+    __syncthreads();   // the last item's tiles and marks have been read
+    if (tid < 2u) lds_special[tid] = 0u;
+    __syncthreads();   // no mark is set before
+    if (tiles) copy(0, lds_k0, lds_v0);
 
-    // keys of a tile that the lane's query of block b sees
-    auto sees = [&](int b, uint32_t tile) {
-      const int64_t k = (int64_t)(q0 + 32u * b + n) + shift + 1 - (int64_t)tile * kTile;
-      return (int)min(max(k, (int64_t)0), (int64_t)kTile);
+    // The two products are written in the order in which their instructions
+    // should run, which the barriers keep the compiler to: LDS reads several
+    // products ahead of their use, and the exponentials of the next 16 keys
+    // between the products of the last.  (Its own order waited for each read.)
+    auto key = [&](const u32x4 *kt, uint32_t ln, int i) {   // keys 32 (i / KS) on, dimensions 16 (i % KS) on
+      const uint32_t r = ln & 31u;
+      const uint32_t at = r * (2u * D) + (uint32_t)(i / KS * 64 * D) + key_piece<D>(r, 2 * (i % KS) + (ln >> 5)) * 16u;
+      return *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(kt) + at);
     };
-    auto compute = [&](uint32_t tile, uint32_t buf, auto masked) {
-      constexpr bool MASKED = decltype(masked)::value;
-      const uint32_t kt = buf * (2u * kBytes), vt = kt + kBytes;
-      f32x16 s[QB][2];
+    auto scores = [&](f32x16 (&s)[2], const u32x4 *kt, uint32_t ln) {
+      constexpr int AHEAD = 6;
+      u32x4 w[AHEAD];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < AHEAD; ++i) w[i] = key(kt, ln, i);
+      in_order();
 #pragma unroll
-        for (int b = 0; b < QB; ++b)
-          for (int r = 0; r < 16; ++r) s[b][i][r] = 0.0f;
+      for (int i = 0; i < 2 * KS; ++i) {
+        if (i % KS == 0)
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          const u32x4 w = *(lds_u32x4 *)(uintptr_t)(kt + i * 64u * D + k_row + key_piece<D>(n, 2 * k + half) * 16u);
-#pragma unroll
-          for (int b = 0; b < QB; ++b) s[b][i] = Elem<T>::mfma32(w, qf[b][k], s[b][i]);
-        }
+          for (int r = 0; r < 16; ++r) s[i / KS][r] = 0.0f;
+        s[i / KS] = Elem<T>::mfma32(w[i % AHEAD], qf[i % KS], s[i / KS]);
+        if (i + AHEAD < 2 * KS) w[i % AHEAD] = key(kt, ln, i + AHEAD);
+        in_order();
       }
-      u32x4 p[QB][4];
+    };
+    // Maximum of the lane's query up to this tile.
+    auto raise_to = [&](const f32x16 (&s)[2]) {
+      float mx = -INFINITY;
 #pragma unroll
-      for (int b = 0; b < QB; ++b) {
-        if (MASKED) {
-          const int seen = sees(b, tile) - 4 * (int)half;
+      for (int i = 0; i < 2; ++i)
+        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[i][r]);
+      mx = max32(mx);
+      const bool raise = mx * a.scale > m * a.scale + kLag<T>;
+      if (__any(raise)) {
+        const float mn = raise ? mx : m;
+        const float k = mn == -INFINITY ? 1.0f : exp2_fast((m - mn) * a.scale);
+        m = mn;
+        l *= k;
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-            for (int r = 0; r < 16; ++r) s[b][i][r] = 32 * i + 8 * (r / 4) + r % 4 < seen ? s[b][i][r] : -INFINITY;
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[b][i][r]);
-        mx = max32(mx);
-        const bool raise = mx * a.scale > m[b] * a.scale + kLag<T>;
-        if (__any(raise)) {
-          const float mn = raise ? mx : m[b];
-          const float k = mn == -INFINITY ? 1.0f : exp2_fast((m[b] - mn) * a.scale);
-          m[b] = mn;
-          l[b] *= k;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[b][d] *= k;
-        }
-        const float off = m[b] == -INFINITY ? 0.0f : kLift<T> - m[b] * a.scale;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          for (int r = 0; r < 16; r += 2) {
-            const float x = exp2_fast(__builtin_fmaf(s[b][i][r], a.scale, off));
-            const float y = exp2_fast(__builtin_fmaf(s[b][i][r + 1], a.scale, off));
-            l[b] += x + y;
-            p[b][2 * i + r / 8][r % 8 / 2] = Elem<T>::pack2(x, y);
-          }
+        for (int d = 0; d < DT; ++d) scale_in_place(o[d], k);
       }
-      auto value = [&](uint32_t c, int d) {
-        const uint32_t at = vt + c * 32u * D + v_row + value_piece<D>(v_r, 4 * d + v_c) * 16u;
-        const u32x2 lo = read_turned(at), hi = read_turned(at + 16u * D);
-        return (u32x4){lo.x, lo.y, hi.x, hi.y};
+    };
+    // Values of 16 tokens from 16 c on, of dimensions 32 d on: the lane gives
+    // the place of row 4 half + (lane / 4) % 4 and the one 8 further.
+    auto value = [&](const u32x4 *vt, uint32_t ln, int c, int d) {
+      const uint32_t r = 4u * (ln >> 5) + ((ln >> 2) & 3u), piece = 2u * ((ln >> 4) & 1u) + ((ln >> 1) & 1u);
+      // (one step from the array: further ones, and the compiler loses track
+      // of which it is)
+      const uint32_t at = (uint32_t)(c * 32 * D) + r * (2u * D) + (ln & 1u) * 8u + value_piece<D>(r, 4 * d + piece) * 16u;
+      const u32x2 lo = read_turned(reinterpret_cast<const char *>(vt) + at),
+                  hi = read_turned(reinterpret_cast<const char *>(vt) + (at + 16u * D));
+      return (u32x4){lo.x, lo.y, hi.x, hi.y};
+    };
+    // Outputs of a tile; kept(w): w, or what is left of it.
+    auto outputs = [&](const f32x16 (&s)[2], const u32x4 *vt, uint32_t ln, auto kept) {
+      const float off = m == -INFINITY ? 0.0f : kLift<T> - m * a.scale;
+      u32x4 p[2], w[DT];
+      auto pair = [&](int c, int e) {   // weights of keys 16 c + 2 e, 2 e + 1 (in the products' order)
+        const float x = exp2_fast(__builtin_fmaf(s[c / 2][c % 2 * 8 + 2 * e], a.scale, off));
+        const float y = exp2_fast(__builtin_fmaf(s[c / 2][c % 2 * 8 + 2 * e + 1], a.scale, off));
+        l += x + y;
+        p[c % 2][e] = Elem<T>::pack2(x, y);
       };
-      if (MASKED) {
-        bool any = false;
-#pragma unroll 1
-        for (uint32_t c = 0; c < 4; ++c)
 #pragma unroll
-          for (int d = 0; d < DT; ++d) any |= special<T>(value(c, d));
-        if (__any(any)) {
-#pragma unroll 1
-          for (uint32_t c = 0; c < 4; ++c)
+      for (int d = 0; d < DT; ++d) w[d] = value(vt, ln, 0, d);
+      in_order();
 #pragma unroll
-            for (int b = 0; b < QB; ++b) {
-              const int seen = sees(b, tile) - 16 * (int)c;
-              const u32x4 w = c == 0u ? p[b][0] : c == 1u ? p[b][1] : c == 2u ? p[b][2] : p[b][3];
+      for (int e = 0; e < 4; ++e) pair(0, e);
 #pragma unroll
-              for (int d = 0; d < DT; ++d) o[b][d] = mfma_seen<T>(value(c, d), w, o[b][d], half, seen);
-            }
-          return;
-        }
-      }
-#pragma unroll
-      for (uint32_t c = 0; c < 4; ++c)
+      for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          const u32x4 w = value(c, d);
+          o[d] = Elem<T>::mfma32(kept(w[d]), p[c % 2], o[d]);
+          if (c < 3) {
+            w[d] = value(vt, ln, c + 1, d);
 #pragma unroll
-          for (int b = 0; b < QB; ++b) o[b][d] = Elem<T>::mfma32(w, p[b][c], o[b][d]);
+            for (int e = 4 * d / DT; e < 4 * (d + 1) / DT; ++e) pair(c + 1, e);
+          }
+          in_order();
         }
     };
-    for (uint32_t t = 0; t < tiles; ++t) {
+
+    auto whole = [&](uint32_t t, const u32x4 *kt, const u32x4 *vt, u32x4 *next_k, u32x4 *next_v) {
       wait_lds_copy();
-      __syncthreads();   // tile t is there; the buffer of tile t - 1 is free
-      if (t + 1u < tiles) copy(t + 1u, (t + 1u) & 1u);
-      const int64_t k0 = (int64_t)t * kTile;
-      if (k0 + kTile <= full_end) compute(t, t & 1u, std::false_type{});
-      else if (k0 < my_end) compute(t, t & 1u, std::true_type{});
-    }
+      __syncthreads();   // tile t is there; the other buffer has been read
+      if (t + 1u < tiles) copy(t + 1u, next_k, next_v);
+      f32x16 s[2];
+      scores(s, kt, lane);
+      raise_to(s);
+      outputs(s, vt, lane, [](u32x4 w) { return w; });
+    };
+    bool left_out = false;   // infinities or NaN among the values of a tile seen in part
+    auto part = [&](uint32_t t, const u32x4 *kt, const u32x4 *vt, u32x4 *next_k, u32x4 *next_v) {
+      wait_lds_copy();
+      uint32_t any = 0;
 #pragma unroll
-    for (int b = 0; b < QB; ++b) {
-      const uint32_t qi = q0 + 32u * b + n;
-      const float sum = add32(l[b]);
-      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;   // NaN stays
-      if (qi < count_q) {
-        char *op = a.out + (int64_t)(begin_q + qi) * a.o_t + head * a.o_h;
+      for (uint32_t i = 0; i < (uint32_t)N; ++i) {
+        const u32x4 w = vt[(wave * N + i) * 64u + lane];
+        for (int e = 0; e < 4; ++e) any |= special<T>(w[e]);
+      }
+      if (any) lds_special[t & 1u] = 1u;
+      __syncthreads();
+      if (t + 1u < tiles) copy(t + 1u, next_k, next_v);
+      // (a mark stays for the tiles after: they take the longer way for nothing)
+      const bool special_here = lds_special[t & 1u] != 0u;
+      if (t >= mine) return;
+      // what follows from the lane's number is worked out again here, or it
+      // would take registers from the loop over whole tiles
+      uint32_t ln = lane;
+      asm volatile("" : "+v"(ln));
+      f32x16 s[2];
+      scores(s, kt, ln);
+      const int seen = (int)min(max((int64_t)(q0 + (ln & 31u)) + shift + 1 - (int64_t)t * kTile, (int64_t)0), (int64_t)kTile) - 4 * (int)(ln >> 5);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        for (int r = 0; r < 16; ++r) s[i][r] = 32 * i + 8 * (r / 4) + r % 4 < seen ? s[i][r] : -INFINITY;
+      raise_to(s);
+      if (special_here) {
+        left_out = true;
+        outputs(s, vt, ln, [](u32x4 w) { return without_special<T>(w); });
+      } else {
+        outputs(s, vt, ln, [](u32x4 w) { return w; });
+      }
+    };
+    uint32_t t = 0;
+    for (; t < full; t += 2u) {
+      whole(t, lds_k0, lds_v0, lds_k1, lds_v1);
+      whole(t + 1u, lds_k1, lds_v1, lds_k0, lds_v0);
+    }
+    for (; t < tiles; ++t) {
+      const bool odd = t & 1u;
+      part(t, odd ? lds_k1 : lds_k0, odd ? lds_v1 : lds_v0, odd ? lds_k0 : lds_k1, odd ? lds_v0 : lds_v1);
+    }
+
+    const float sum = add32(l);
+    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;   // NaN stays
+#pragma unroll
+    for (int d = 0; d < DT; ++d) o[d] *= inv;
+    if (left_out)
+      for (int64_t j = (int64_t)full * kTile; j < my_end; ++j) {
+        const char *vp = vb + j * a.v_t + half * 8u;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int r = 0; r < 16; r += 4)
-            *reinterpret_cast<u32x2 *>(op + (32 * d + 8 * (r / 4) + 4 * half) * 2) =
-                (u32x2){Elem<T>::pack2(o[b][d][r] * inv, o[b][d][r + 1] * inv),
-                        Elem<T>::pack2(o[b][d][r + 2] * inv, o[b][d][r + 3] * inv)};
+          for (int r = 0; r < 16; r += 4) {
+            const u32x2 w = *reinterpret_cast<const u32x2 *>(vp + (32 * d + 2 * r) * 2);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t x = e & 1 ? w[e / 2] >> 16 : w[e / 2];
+              const bool add = j <= (int64_t)qi + shift && (x & Elem<T>::kInf) == Elem<T>::kInf;
+              o[d][r + e] += add ? Elem<T>::lo(x) : 0.0f;
+            }
+          }
       }
+    if (qi < count_q) {
+      char *op = a.out + (int64_t)(begin_q + qi) * a.o_t + head * a.o_h;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; r += 4)
+          *reinterpret_cast<u32x2 *>(op + (32 * d + 2 * r + 4 * half) * 2) =
+              (u32x2){Elem<T>::pack2(o[d][r], o[d][r + 1]), Elem<T>::pack2(o[d][r + 2], o[d][r + 3])};
     }
   }
 }
 
 template <entro_dtype T, int D>
 static entro_status launch_prompt(const PromptArg &a, hipStream_t s) {
-  constexpr int QB = 1;
-  constexpr uint32_t rows = 32u * QB * kWaves4;
+  constexpr uint32_t rows = 32u * kWaves4;
   uint64_t grid = std::min<uint64_t>(a.total_q, (uint64_t)a.total_q / rows + a.n_seq);
   grid = std::min<uint64_t>(grid * a.n_heads, 1u << 30);
   grid = std::max<uint64_t>(1, cap_grid(grid));
   (void)hipGetLastError();
-  hipLaunchKernelGGL((attn_prompt_kernel<T, D, QB>), dim3((uint32_t)grid), dim3(256), 2u * 2u * kTile * D * 2u, s, a);
+  hipLaunchKernelGGL((attn_prompt_kernel<T, D>), dim3((uint32_t)grid), dim3(256), 0, s, a);
   return hipGetLastError() == hipSuccess ? ENTRO_OK : ENTRO_E_HIP;
 }
 
