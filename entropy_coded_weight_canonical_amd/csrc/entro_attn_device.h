@@ -23,7 +23,8 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 constexpr float kLog2e = 1.4426950408889634f;
 
 // The two 16-bit element types.  pack2 rounds two floats to nearest even into
-// one word, the first in the low half.  kInf: the magnitude bits from which a
+// one word, the first in the low half; add2 adds both values of a word to a
+// float, in 32 bits.  kInf: the magnitude bits from which a
 // value is infinite or NaN.
 template <entro_dtype T>
 struct Elem;
@@ -37,6 +38,10 @@ struct Elem<ENTRO_BF16> {
   __device__ static uint32_t pack2(float a, float b) {
     typedef __bf16 v2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, v2));
+  }
+  __device__ static float add2(uint32_t w, float c) {
+    typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(v2, w), __builtin_bit_cast(v2, 0x3F803F80u), c, false);
   }
   __device__ static f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);
@@ -52,6 +57,9 @@ struct Elem<ENTRO_F16> {
   __device__ static float hi(uint32_t w) { return (float)__builtin_bit_cast(v2, w).y; }
   __device__ static uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, v2));
+  }
+  __device__ static float add2(uint32_t w, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(v2, w), __builtin_bit_cast(v2, 0x3C003C00u), c, false);
   }
   __device__ static f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(v8, a), __builtin_bit_cast(v8, b), c, 0, 0, 0);

@@ -48,16 +48,16 @@ __device__ __forceinline__ u32x4 without_special(u32x4 w) {
 }
 
 // LDS place (16-byte piece) of piece c of row r of a tile of keys or values.
-// Rows are 2 D bytes, and a wavefront reads one piece of 32 rows (keys), or two
-// neighbouring pieces of 8 rows (values), at once: the pieces' order within a
-// row varies with the row so that these spread over all banks.
+// Rows are 2 D bytes, and 256 bytes are read at once: one piece of 16 rows
+// (keys), or four neighbouring pieces of 4 rows (values).  The pieces' order
+// within a row varies with the row so that these lie in different banks.
 template <int D>
 __device__ __forceinline__ uint32_t key_piece(uint32_t r, uint32_t c) {
   return D == 128 ? c ^ (r & 15u) : D == 64 ? c ^ ((r >> 1) & 7u) : c ^ ((r >> 2) & 3u);
 }
 template <int D>
 __device__ __forceinline__ uint32_t value_piece(uint32_t r, uint32_t c) {
-  return D == 128 ? c ^ (2u * (r & 7u)) : D == 64 ? c ^ (2u * ((r >> 1) & 3u)) : c;
+  return D == 128 ? c ^ (4u * (r & 3u)) : D == 64 ? c ^ (4u * ((r >> 1) & 1u)) : c;
 }
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -243,8 +243,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       auto pair = [&](int c, int e) {   // weights of keys 16 c + 2 e, 2 e + 1 (in the products' order)
         const float x = exp2_fast(__builtin_fmaf(s[c / 2][c % 2 * 8 + 2 * e], a.scale, off));
         const float y = exp2_fast(__builtin_fmaf(s[c / 2][c % 2 * 8 + 2 * e + 1], a.scale, off));
-        l += x + y;
         p[c % 2][e] = Elem<T>::pack2(x, y);
+        l = Elem<T>::add2(p[c % 2][e], l);
       };
 #pragma unroll
       for (int d = 0; d < DT; ++d) w[d] = value(vt, ln, 0, d);
