@@ -5,9 +5,10 @@ attention of packed prompts), ``kv_store`` and ``kv_load`` (keys and values
 into the paged 8-bit cache and back), ``attn_cache`` (one new token per
 sequence over the cache).  Operands are torch tensors on the HIP device; the
 functions check shapes and types, pass pointers and strides on, and return
-without waiting.  Work goes to ``stream`` (default: the current stream); a
-caller that uses another stream than the one its tensors were made on orders
-the two itself.  ``status`` is an int32 tensor with one entry per sequence,
+without waiting.  Work goes to ``stream`` (a torch stream or a raw handle;
+default: the current stream).  The caller orders it after the work that made
+its tensors; their memory is kept until a torch stream has used them (on a raw
+handle that, too, is the caller's).  ``status`` is an int32 tensor with one entry per sequence,
 zeroed by the caller, in which faults found in the data are OR-ed
 (``FLAGS["length"]``, ``FLAGS["page"]``).
 """
@@ -15,11 +16,16 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 __all__ = ["KVCache", "attn_prompt", "kv_store", "kv_load", "attn_cache", "attn_cache_work_bytes"]
 
 _P, _U32, _I64 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_int64
 
+
+# The structures of the C ABI.  The functions below pack the same bytes
+# themselves (a tenth of the time of filling a structure by its fields: a
+# call's work in Python is of the order of a small call's time on the GPU).
 
 class Rows(ctypes.Structure):
     _fields_ = [("d", _P), ("stride_t", _I64), ("stride_h", _I64)]
@@ -59,36 +65,50 @@ def _bind(lib):
     lib.entro_attn_cache_work_bytes.restype = ctypes.c_uint64
 
 
-_dtypes = None
+_PROMPT = struct.Struct("@PqqPqqPqqPqqPPIIIIIIif")
+_STORE = struct.Struct("@PqqPqqPPIi")
+_CACHE = struct.Struct("@PqqPqqPIifPQ")
+_TABLE = struct.Struct("@PIIIi")
+
+# torch and what of it the calls use, from the first call on (the package's
+# host side works without)
+torch = None
+_DTYPES: dict = {}
+_raw_stream = None
+
+
+def _torch_once() -> None:
+    global torch, _raw_stream
+    if torch is None:
+        import torch as t
+
+        _DTYPES.update({t.bfloat16: 0, t.float16: 1})
+        _raw_stream = t._C._cuda_getCurrentRawStream
+        torch = t
 
 
 def _dtype_id(dtype) -> int:
-    global _dtypes
-    if _dtypes is None:
-        import torch
-
-        _dtypes = {torch.bfloat16: 0, torch.float16: 1}
-    try:
-        return _dtypes[dtype]
-    except KeyError:
-        raise ValueError(f"element type {dtype}: bfloat16 or float16 expected") from None
+    i = _DTYPES.get(dtype)
+    if i is None:
+        raise ValueError(f"element type {dtype}: bfloat16 or float16 expected")
+    return i
 
 
-def _rows(x, what: str, dtype, heads: int, dim: int) -> Rows:
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != dim:
-        raise ValueError(f"{what}: shape {tuple(x.shape)}, expected [rows, {heads}, {dim}]")
-    if x.dtype != dtype or not x.is_cuda:
+def _rows(x, what: str, dtype, heads: int, dim: int):
+    """(pointer, row stride, head stride) of a 16-bit operand."""
+    shape = x.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{what}: shape {tuple(shape)}, expected [rows, {heads}, {dim}]")
+    if x.dtype is not dtype or not x.is_cuda:
         raise ValueError(f"{what}: a {dtype} tensor on the GPU expected, got {x.dtype} on {x.device}")
     st, sh, sd = x.stride()
     if sd != 1:
         raise ValueError(f"{what}: the head dimension has to be contiguous")
-    return Rows(x.data_ptr(), st if x.shape[0] > 1 else heads * dim, sh if heads > 1 else dim)
+    return x.data_ptr(), st if shape[0] > 1 else heads * dim, sh if heads > 1 else dim
 
 
-def _ints(x, what: str, n: int):
-    import torch
-
-    if x.dtype != torch.int32 or x.dim() != 1 or x.shape[0] != n or not x.is_cuda or (n > 1 and x.stride(0) != 1):
+def _ints(x, what: str, n: int) -> int:
+    if x.dtype is not torch.int32 or x.shape != (n,) or not x.is_cuda or (n > 1 and not x.is_contiguous()):
         raise ValueError(f"{what}: {n} contiguous int32 values on the GPU expected, got {x.dtype} {tuple(x.shape)} on {x.device}")
     return x.data_ptr()
 
@@ -99,67 +119,83 @@ class KVCache:
     ``k_scales`` / ``v_scales`` float32 [pages][kv heads].  Holds the tensors,
     so that the device memory outlives the calls."""
 
-    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "desc")
+    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "tensors", "desc")
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
-        import torch
-
+        _torch_once()
         if k_codes.dim() != 4 or v_codes.dim() != 4:
             raise ValueError("k_codes and v_codes have four dimensions")
         pages, kv, page, dim = k_codes.shape
         if v_codes.shape != (pages, kv, dim, page) or k_scales.shape != (pages, kv) or v_scales.shape != (pages, kv):
             raise ValueError("the shapes of codes and scales do not belong together")
-        for x, t in ((k_codes, torch.int8), (v_codes, torch.int8), (k_scales, torch.float32), (v_scales, torch.float32)):
-            if x.dtype != t or not x.is_cuda or not x.is_contiguous():
-                raise ValueError("int8 codes and float32 scales, contiguous and on the GPU, expected")
+        i8, f32 = torch.int8, torch.float32
+        if not (k_codes.dtype is i8 and v_codes.dtype is i8 and k_scales.dtype is f32 and v_scales.dtype is f32
+                and k_codes.is_cuda and v_codes.is_cuda and k_scales.is_cuda and v_scales.is_cuda
+                and k_codes.is_contiguous() and v_codes.is_contiguous() and k_scales.is_contiguous()
+                and v_scales.is_contiguous()):
+            raise ValueError("int8 codes and float32 scales, contiguous and on the GPU, expected")
         self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.tensors = (k_codes, v_codes, k_scales, v_scales)
         self.desc = Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), pages, page, kv,
                           dim)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
         """A cache of ``n_pages`` unused pages (16, 32, 64 or 128 tokens each)."""
-        import torch
-
+        _torch_once()
         codes = lambda *s: torch.zeros(n_pages, n_kv_heads, *s, dtype=torch.int8, device=device)  # noqa: E731
         scales = lambda: torch.zeros(n_pages, n_kv_heads, dtype=torch.float32, device=device)  # noqa: E731
         return cls(codes(page_tokens, head_dim), codes(head_dim, page_tokens), scales(), scales())
 
 
-def _table(table, n: int) -> Table:
-    import torch
-
-    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != n or not table.is_cuda:
+def _table(table, n: int) -> bytes:
+    if table.dtype is not torch.int32 or table.dim() != 2 or table.shape[0] != n or not table.is_cuda:
         raise ValueError(f"table: int32 [{n}][pages] on the GPU expected, got {table.dtype} {tuple(table.shape)} on {table.device}")
     pages = table.shape[1]
-    if pages > 1 and table.stride(1) != 1:
+    sn, sp = table.stride()
+    if pages > 1 and sp != 1:
         raise ValueError("table: the pages of a sequence have to lie side by side")
-    return Table(table.data_ptr(), table.stride(0) if n > 1 else pages, pages, n)
+    return _TABLE.pack(table.data_ptr(), sn if n > 1 else pages, pages, n, 0)
 
 
-def _on(stream) -> int:
-    from . import _stream_handle
+def _on(stream, *used) -> int:
+    """The stream's handle.  Tensors that a torch stream other than their own
+    uses are noted with torch, which then keeps their memory until that stream
+    is through with them, however early the caller drops them."""
+    if stream is None:
+        return _raw_stream(used[0].get_device())
+    if hasattr(stream, "cuda_stream"):
+        for x in used:
+            x.record_stream(stream)
+        return stream.cuda_stream
+    return int(stream)
 
-    return _stream_handle(stream)
+
+_fns: dict = {}
 
 
 def _call(name: str, *args) -> None:
-    from . import _check, load
+    fn = _fns.get(name)
+    if fn is None:
+        from . import load
 
-    _check(getattr(load(), name)(*args), name)
+        fn = _fns[name] = getattr(load(), name)
+    status = fn(*args)
+    if status:
+        from . import _check
+
+        _check(status, name)
 
 
 def _empty(shape, dtype, like, stream):
     """Memory of a result: from the stream that writes it, so that torch does
     not hand it out again before."""
-    import torch
-
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            raise ValueError("on a raw stream handle the caller gives the memory of results and workspace")
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=like.device)
-    return torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not hasattr(stream, "cuda_stream"):
+        raise ValueError("on a raw stream handle the caller gives the memory of results and workspace")
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def attn_prompt(q, k, v, cu_q, cu_k, status, scale=None, out=None, stream=None):
@@ -169,6 +205,7 @@ def attn_prompt(q, k, v, cu_q, cu_k, status, scale=None, out=None, stream=None):
     sums (n + 1).  A sequence's last keys are its queries' own; more keys than
     queries are tokens in front of them.  Returns ``out`` [rows][heads][dim]
     (rows of no sequence are left as they are)."""
+    _torch_once()
     n = cu_q.shape[0] - 1
     if n < 0 or q.dim() != 3 or k.dim() != 3:
         raise ValueError("q, k, v are [rows][heads][dim], cu_q and cu_k hold n + 1 sums")
@@ -176,28 +213,34 @@ def attn_prompt(q, k, v, cu_q, cu_k, status, scale=None, out=None, stream=None):
     kv = k.shape[1]
     if v.shape[0] != k.shape[0]:
         raise ValueError("k and v have the same rows")
+    t = q.dtype
     if out is None:
-        out = _empty((rows, heads, dim), q.dtype, q, stream)
-    elif out.shape[0] != rows:
-        raise ValueError("out has the rows of q")
-    a = PromptArgs(_rows(q, "q", q.dtype, heads, dim), _rows(k, "k", q.dtype, kv, dim), _rows(v, "v", q.dtype, kv, dim),
-                   _rows(out, "out", q.dtype, heads, dim), _ints(cu_q, "cu_q", n + 1), _ints(cu_k, "cu_k", n + 1), n, rows,
-                   k.shape[0], heads, kv, dim, _dtype_id(q.dtype), 1.0 / math.sqrt(dim) if scale is None else scale)
-    _call("entro_attn_prompt", ctypes.byref(a), _ints(status, "status", n), _on(stream))
+        out = _empty((rows, heads, dim), t, q, stream)
+        ro = out.data_ptr(), heads * dim, dim
+    else:
+        ro = _rows(out, "out", t, heads, dim)
+        if out.shape[0] != rows:
+            raise ValueError("out has the rows of q")
+    a = _PROMPT.pack(*_rows(q, "q", t, heads, dim), *_rows(k, "k", t, kv, dim), *_rows(v, "v", t, kv, dim), *ro,
+                     _ints(cu_q, "cu_q", n + 1), _ints(cu_k, "cu_k", n + 1), n, rows,
+                     k.shape[0], heads, kv, dim, _dtype_id(t), 1.0 / math.sqrt(dim) if scale is None else scale)
+    _call("entro_attn_prompt", a, _ints(status, "status", n), _on(stream, q, k, v, cu_q, cu_k, status, out))
     return out
 
 
 def kv_store(cache: KVCache, k, v, table, held, cu_new, status, stream=None) -> None:
     """Write packed new keys and values behind the ``held`` tokens of each
     sequence (``entro_kv_store``)."""
+    _torch_once()
     n = table.shape[0]
     kv, dim = cache.k_codes.shape[1], cache.k_codes.shape[3]
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v have the same rows")
-    a = StoreArgs(_rows(k, "k", k.dtype, kv, dim), _rows(v, "v", k.dtype, kv, dim), _ints(held, "held", n),
-                  _ints(cu_new, "cu_new", n + 1), k.shape[0], _dtype_id(k.dtype))
-    t = _table(table, n)
-    _call("entro_kv_store", ctypes.byref(cache.desc), ctypes.byref(t), ctypes.byref(a), _ints(status, "status", n), _on(stream))
+    t = k.dtype
+    a = _STORE.pack(*_rows(k, "k", t, kv, dim), *_rows(v, "v", t, kv, dim), _ints(held, "held", n),
+                    _ints(cu_new, "cu_new", n + 1), k.shape[0], _dtype_id(t))
+    _call("entro_kv_store", ctypes.byref(cache.desc), _table(table, n), a, _ints(status, "status", n),
+          _on(stream, k, v, *cache.tensors, table, held, cu_new, status))
 
 
 def kv_load(cache: KVCache, table, first, cu_out, total: int, status, dtype=None, out=None, stream=None):
@@ -205,8 +248,7 @@ def kv_load(cache: KVCache, table, first, cu_out, total: int, status, dtype=None
     the ``cu_out[b + 1] - cu_out[b]`` tokens from position ``first[b]`` on.
     Returns ``(k, v)``, each [total][kv heads][dim], of ``dtype`` (default
     bfloat16) or the pair ``out``."""
-    import torch
-
+    _torch_once()
     n = table.shape[0]
     kv, dim = cache.k_codes.shape[1], cache.k_codes.shape[3]
     if out is None:
@@ -215,10 +257,11 @@ def kv_load(cache: KVCache, table, first, cu_out, total: int, status, dtype=None
     k, v = out
     if k.shape[0] != total or v.shape[0] != total:
         raise ValueError("the outputs have `total` rows")
-    a = StoreArgs(_rows(k, "k", k.dtype, kv, dim), _rows(v, "v", k.dtype, kv, dim), _ints(first, "first", n),
-                  _ints(cu_out, "cu_out", n + 1), total, _dtype_id(k.dtype))
-    t = _table(table, n)
-    _call("entro_kv_load", ctypes.byref(cache.desc), ctypes.byref(t), ctypes.byref(a), _ints(status, "status", n), _on(stream))
+    t = k.dtype
+    a = _STORE.pack(*_rows(k, "k", t, kv, dim), *_rows(v, "v", t, kv, dim), _ints(first, "first", n),
+                    _ints(cu_out, "cu_out", n + 1), total, _dtype_id(t))
+    _call("entro_kv_load", ctypes.byref(cache.desc), _table(table, n), a, _ints(status, "status", n),
+          _on(stream, k, v, *cache.tensors, table, first, cu_out, status))
     return k, v
 
 
@@ -229,6 +272,9 @@ def attn_cache_work_bytes(n_seq: int, n_heads: int, n_kv_heads: int, head_dim: i
     return int(load().entro_attn_cache_work_bytes(n_seq, n_heads, n_kv_heads, head_dim))
 
 
+_work_sizes: dict = {}   # workspace by the call's sizes
+
+
 def attn_cache(q, cache: KVCache, table, lens, status, scale=None, out=None, work=None, stream=None):
     """Attention of one new token per sequence over the cache
     (``entro_attn_cache``): ``q`` [n][heads][dim], ``lens`` the tokens of each
@@ -236,26 +282,32 @@ def attn_cache(q, cache: KVCache, table, lens, status, scale=None, out=None, wor
     tensor of at least ``attn_cache_work_bytes`` bytes that no call on another
     stream uses meanwhile (made for the call by default).  Returns ``out``
     [n][heads][dim]."""
-    import torch
-
+    _torch_once()
     if q.dim() != 3:
         raise ValueError("q is [sequences][heads][dim]")
     n, heads, dim = q.shape
-    kv = cache.k_codes.shape[1]
-    need = attn_cache_work_bytes(n, heads, kv, dim)
+    kv = cache.desc.n_kv_heads
+    if dim != cache.desc.head_dim:
+        raise ValueError(f"q has head dimension {dim}, the cache {cache.desc.head_dim}")
+    t = q.dtype
     if out is None:
-        out = _empty((n, heads, dim), q.dtype, q, stream)
-    elif out.shape[0] != n:
-        raise ValueError("out has the rows of q")
+        out = _empty((n, heads, dim), t, q, stream)
+        ro = out.data_ptr(), heads * dim, dim
+    else:
+        ro = _rows(out, "out", t, heads, dim)
+        if out.shape[0] != n:
+            raise ValueError("out has the rows of q")
     if work is None:
+        need = _work_sizes.get((n, heads, kv, dim))
+        if need is None:
+            if len(_work_sizes) >= 4096:
+                _work_sizes.clear()
+            need = _work_sizes[n, heads, kv, dim] = attn_cache_work_bytes(n, heads, kv, dim)
         work = _empty((max(need, 16),), torch.uint8, q, stream)
     elif not work.is_cuda or not work.is_contiguous():
         raise ValueError("work: a contiguous tensor on the GPU expected")
-    a = CacheArgs(_rows(q, "q", q.dtype, heads, dim), _rows(out, "out", q.dtype, heads, dim), _ints(lens, "lens", n), heads,
-                  _dtype_id(q.dtype), 1.0 / math.sqrt(dim) if scale is None else scale, work.data_ptr(),
-                  work.numel() * work.element_size())
-    if dim != cache.desc.head_dim:
-        raise ValueError(f"q has head dimension {dim}, the cache {cache.desc.head_dim}")
-    t = _table(table, n)
-    _call("entro_attn_cache", ctypes.byref(cache.desc), ctypes.byref(t), ctypes.byref(a), _ints(status, "status", n), _on(stream))
+    a = _CACHE.pack(*_rows(q, "q", t, heads, dim), *ro, _ints(lens, "lens", n), heads, _dtype_id(t),
+                    1.0 / math.sqrt(dim) if scale is None else scale, work.data_ptr(), work.numel() * work.element_size())
+    _call("entro_attn_cache", ctypes.byref(cache.desc), _table(table, n), a, _ints(status, "status", n),
+          _on(stream, q, *cache.tensors, table, lens, status, out, work))
     return out
