@@ -8,10 +8,10 @@
 namespace entro {
 
 constexpr uint32_t kTile = 64;          // tokens a wavefront takes at a time
-constexpr uint32_t kCacheWaves = 4;     // wavefronts per workgroup, interleaved over a chunk's tiles
+constexpr uint32_t kCacheWaves = 4;     // wavefronts per workgroup, interleaved over its tiles
 constexpr uint32_t kHeadsPerWg = 16;    // query heads of one key/value head (columns of the matrix products)
-constexpr uint32_t kMinChunkTiles = 8;  // tiles of the smallest chunk of a split sequence
-constexpr uint32_t kChunkTarget = 1024; // chunks x head groups that a call is split into at most (beside one per sequence)
+constexpr uint32_t kShareTiles = 4;     // least tiles of a workgroup's share
+constexpr uint32_t kShares = 512;       // shares of a call, all heads together: two workgroups on each of 256 CUs
 
 struct CacheArg {
   const int8_t *k_codes, *v_codes;
@@ -26,10 +26,10 @@ struct CacheArg {
   const int32_t *lens;
   uint32_t n_heads, group;      // group: query heads per key/value head
   uint32_t parts;               // workgroups (of kHeadsPerWg query heads) per key/value head
-  uint32_t items;               // chunks that the workspace holds
+  uint32_t shares;              // that the tokens of a key/value head are split into at most; 0: one sequence each
   float scale;                  // times log2(e)
-  float *part_o;                // [items][n_heads][D]
-  f32x2 *part_ml;               // [items][n_heads]: maximum, sum
+  float *part_o;                // [n_seq + shares][n_heads][D]
+  f32x2 *part_ml;               // [n_seq + shares][n_heads]: maximum, sum
   uint32_t *status;
 };
 
@@ -40,23 +40,39 @@ __device__ __forceinline__ uint32_t cache_len(const CacheArg &a, uint32_t b, boo
   return fine ? (uint32_t)n : 0u;
 }
 
-// The call's chunk: tiles per chunk, so that all sequences together make about
-// kChunkTarget workgroups whatever their lengths.  Computed alike by every
-// wavefront of both kernels from the lengths alone.
-__device__ __forceinline__ uint32_t chunk_tiles(const CacheArg &a, uint32_t lane) {
-  uint64_t sum = 0;
-  for (uint32_t b0 = 0; b0 < a.n_seq; b0 += 64u) {
-    const uint32_t b = b0 + lane;
-    const uint32_t t = b < a.n_seq ? (cache_len(a, b) + kTile - 1u) / kTile : 0u;
-    // 64 terms below 2^25 each
-    sum += (uint32_t)__shfl((int)wave_scan(t, lane), 63, 64);
-  }
-  const uint64_t per = (uint64_t)a.n_kv * a.parts;
-  const uint64_t c = (rfl64(sum) * per + kChunkTarget - 1u) / kChunkTarget;
-  return (uint32_t)min(max(c, (uint64_t)kMinChunkTiles), (uint64_t)1u << 25);   // a sequence has at most 2^25 tiles
+__device__ __forceinline__ uint32_t tiles_of(const CacheArg &a, uint32_t b) {
+  return (cache_len(a, b) + kTile - 1u) / kTile;
 }
-__device__ __forceinline__ uint32_t chunks_of(const CacheArg &a, uint32_t b, uint32_t c) {
-  return max(1u, ((cache_len(a, b) + kTile - 1u) / kTile + c - 1u) / c);
+
+// Tiles of the sequences before b, one after another.
+__device__ __forceinline__ uint64_t tiles_before(const CacheArg &a, uint32_t b, uint32_t lane) {
+  uint64_t sum = 0;
+  for (uint32_t b0 = 0; b0 < b; b0 += 64u) {
+    const uint32_t t = b0 + lane < b ? tiles_of(a, b0 + lane) : 0u;
+    sum += __builtin_amdgcn_readlane(wave_scan(t), 63);   // 64 terms of at most 2^25
+  }
+  return rfl64(sum);
+}
+
+// The tiles of all sequences, one after another, in equal shares (to one tile)
+// whatever the sequences' lengths, one workgroup each and as many as the GPU
+// holds at once: share w has tiles begin(w) .. begin(w + 1) - 1.  A share's part
+// of one sequence is a piece; a sequence in one piece is finished by its
+// workgroup, the others' pieces are joined by the second kernel.  Piece (w, b)
+// of share w and sequence b has the workspace's place w + b: going along the
+// tiles, one of the two grows at each end of a piece.
+struct Shares {
+  uint64_t tiles;
+  uint32_t n;
+  __device__ uint64_t begin(uint32_t w) const { return w * tiles / n; }
+  // the share of tile t: the last w with begin(w) <= t, i.e. w tiles < (t + 1) n
+  __device__ uint32_t of(uint64_t t) const { return (uint32_t)(((t + 1u) * n + tiles - 1u) / tiles) - 1u; }
+};
+__device__ __forceinline__ Shares shares_of(const CacheArg &a, uint32_t lane) {
+  Shares s;
+  s.tiles = tiles_before(a, a.n_seq, lane);
+  s.n = (uint32_t)min((uint64_t)a.shares, max((uint64_t)1, s.tiles / kShareTiles));
+  return s;
 }
 
 // Four codes of a word as two pairs of f16: the code plus 128 in the low byte
@@ -83,9 +99,9 @@ __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup takes a chunk of one sequence's tokens for one key/value head
-// and up to 16 of its query heads; its four wavefronts take every fourth tile
-// of 64 tokens and join their results in LDS.
+// One workgroup takes pieces of sequences for one key/value head and up to 16
+// of its query heads; its four wavefronts take every fourth tile of 64 tokens
+// and join their results in LDS.
 //
 // A tile's scores are K Q^T and its product V^T P^T, both on the matrix cores
 // with the query heads as the 16 columns, so that softmax statistics are per
@@ -94,7 +110,9 @@ __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
 // the first product's row 4 g + r of its i-th part is made token
 // 16 g + 4 i + r, and lane group g then holds 16 consecutive tokens, just the
 // 16 bytes of value codes it reads for one dimension.  Nothing of the cache
-// passes through LDS; each code is read once, 16 bytes a lane.
+// passes through LDS; each code is read once, 16 bytes a lane.  The next tile's
+// keys are on their way from where this tile's scores are done, a tile's values
+// from its start.
 //
 // Codes become f16 exactly; q is brought to f16 by a power of two (exact but
 // for values 2^-24 below the row's largest).  With t = s + log2(value scale)
@@ -123,20 +141,55 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
       cache_len(a, b, &ok);
       if (!ok) atomicOr(a.status + b, ENTRO_F_LENGTH);
     }
-  const uint32_t ct = chunk_tiles(a, lane);
-  for (uint32_t item = blockIdx.x;; item += gridDim.x) {
-    const Found f = find_item(item, a.n_seq, lane, [&](uint32_t b) { return chunks_of(a, b, ct); });
-    if (f.seq == a.n_seq) break;
-    const uint32_t len = cache_len(a, f.seq);
-    const uint32_t tile_end = min((f.local + 1u) * ct, (len + kTile - 1u) / kTile);
-    const int32_t *row = a.table + (uint64_t)f.seq * a.table_stride;
+  // empty sequences have no piece
+  if (blockIdx.x == 0u)
+    for (uint32_t b = wave; b < a.n_seq; b += kCacheWaves)
+      if (cache_len(a, b) == 0u)
+        for (uint32_t i = lane; i < heads * (D / 2u); i += 64u)
+          *reinterpret_cast<uint32_t *>(a.out + b * a.o_t + (int64_t)(head0 + i / (D / 2u)) * a.o_h + i % (D / 2u) * 4u) = 0u;
+  Shares sh{};
+  if (a.shares) sh = shares_of(a, lane);
+  const uint32_t units = a.shares ? sh.n : a.n_seq;
+  for (uint32_t w = blockIdx.x; w < units; w += gridDim.x) {
+  // the tiles t0 .. t1 - 1 of sequence `seq` that come next, of the `left` that the share still has
+  uint32_t seq, t0;
+  uint64_t left;
+  if (a.shares) {
+    const uint64_t begin = sh.begin(w);
+    left = sh.begin(w + 1u) - begin;
+    uint64_t before = 0;
+    seq = 0u;
+    t0 = 0u;
+    for (uint32_t b0 = 0; b0 < a.n_seq; b0 += 64u) {
+      const uint32_t own = b0 + lane < a.n_seq ? tiles_of(a, b0 + lane) : 0u;
+      const uint32_t run = wave_scan(own);
+      const uint64_t past = __ballot(before + run > begin);
+      if (past) {
+        const uint32_t at = (uint32_t)__builtin_ctzll(past);
+        seq = rfl(b0 + at);
+        t0 = rfl((uint32_t)(begin - before - __builtin_amdgcn_readlane(run - own, at)));
+        break;
+      }
+      before += __builtin_amdgcn_readlane(run, 63);
+    }
+  } else {
+    seq = w;
+    t0 = 0u;
+    left = tiles_of(a, w);
+  }
+  for (; left; ++seq, t0 = 0u) {
+    const uint32_t len = cache_len(a, seq), all_tiles = (len + kTile - 1u) / kTile;
+    const uint32_t t1 = (uint32_t)min((uint64_t)all_tiles, t0 + left);
+    if (t1 == t0) continue;   // an empty sequence
+    left -= t1 - t0;
+    const int32_t *row = a.table + (uint64_t)seq * a.table_stride;
 
     // the query head of this lane's column, as f16 times 2^-e
     f16v8 qf[KS];
     float c;                               // score = c * key scale * product
     {
       u32x4 raw[KS];
-      const char *q = a.q + f.seq * a.q_t + (int64_t)(head0 + min(n, heads - 1u)) * a.q_h;
+      const char *q = a.q + seq * a.q_t + (int64_t)(head0 + min(n, heads - 1u)) * a.q_h;
 #pragma unroll
       for (int s = 0; s < S64; ++s) {
         raw[2 * s] = *reinterpret_cast<const u32x4 *>(q + (64 * s + 16 * g) * 2);
@@ -170,34 +223,47 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
     float m = -INFINITY, l = 0.0f;   // l: this lane's tokens only
     bool bad = false;
 
-    for (uint32_t tile = f.local * ct + wave; tile < tile_end; tile += kCacheWaves) {
-      // pages of the 16-token blocks that this lane reads keys of (n / 4) and
-      // values of (g); a block past the end, or of a page that does not exist,
-      // reads page 0 and counts as hidden
-      const uint32_t bk = tile * 4u + (n >> 2), bv = tile * 4u + g;
-      const uint32_t tk = bk * 16u, tv = bv * 16u;
-      int32_t pk = tk < len ? row[tk >> a.page_log2] : 0, pv = tv < len ? row[tv >> a.page_log2] : 0;
-      const bool v_bad = pv < 0 || (uint32_t)pv >= a.n_pages;
-      if (pk < 0 || (uint32_t)pk >= a.n_pages) pk = 0;
-      if (v_bad) pv = 0;
-      bad |= v_bad;
-      const uint32_t rk = (tk & (page - 1u)) + (n & 3u), rv = tv & (page - 1u);
-      const uint64_t ak = (uint64_t)(uint32_t)pk * a.n_kv + kvh, av = (uint64_t)(uint32_t)pv * a.n_kv + kvh;
-      const int8_t *kp = a.k_codes + ((ak << a.page_log2) + rk) * D;
-      const int8_t *vp = a.v_codes + ((av * D + n) << a.page_log2) + rv;
-      u32x4 kq[4][S64];
-      u32x2 kq2[4];
-      u32x4 vq[DT];
+    // Pages of the 16-token blocks that this lane reads keys of (n / 4) and
+    // values of (g).  A block past the end, or of a page that does not exist,
+    // reads page 0 and counts as hidden.
+    struct Pages {
+      int32_t k, v;
+    };
+    auto pages = [&](uint32_t tile) {
+      const uint32_t tk = tile * kTile + (n >> 2) * 16u, tv = tile * kTile + g * 16u;
+      return (Pages){tk < len ? row[tk >> a.page_log2] : 0, tv < len ? row[tv >> a.page_log2] : 0};
+    };
+    u32x4 kq[4][S64], vq[DT];
+    u32x2 kq2[4];
+    auto keys = [&](uint32_t tile, int32_t p) {
+      const uint32_t tk = tile * kTile + (n >> 2) * 16u;
+      const uint64_t at = (uint64_t)((uint32_t)p < a.n_pages ? (uint32_t)p : 0u) * a.n_kv + kvh;
+      const int8_t *kp = a.k_codes + ((at << a.page_log2) + (tk & (page - 1u)) + (n & 3u)) * D;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int s = 0; s < S64; ++s) kq[i][s] = *reinterpret_cast<const u32x4 *>(kp + 4 * i * D + 64 * s + 16 * g);
         if (S32) kq2[i] = *reinterpret_cast<const u32x2 *>(kp + 4 * i * D + 64 * S64 + 8 * g);
       }
-#pragma unroll
-      for (int d = 0; d < DT; ++d) vq[d] = *reinterpret_cast<const u32x4 *>(vp + ((uint64_t)(16 * d) << a.page_log2));
+    };
+    const uint32_t first = t0 + wave;
+    Pages now{}, next{};
+    if (first < t1) {
+      now = pages(first);
+      keys(first, now.k);
+    }
+    for (uint32_t tile = first; tile < t1; tile += kCacheWaves) {
+      const bool more = tile + kCacheWaves < t1;
+      if (more) next = pages(tile + kCacheWaves);
+      const uint32_t tv = tile * kTile + g * 16u;
+      const bool v_bad = (uint32_t)now.v >= a.n_pages;
+      bad |= v_bad;
+      const uint64_t av = (uint64_t)(v_bad ? 0u : (uint32_t)now.v) * a.n_kv + kvh;
+      const int8_t *vp = a.v_codes + ((av * D + n) << a.page_log2) + (tv & (page - 1u));
       const float ks = a.k_scales[av] * c;   // rows 4 g + r of the products are tokens of block g
       const float vs = fmaxf(a.v_scales[av], 1.17549435e-38f);
+#pragma unroll
+      for (int d = 0; d < DT; ++d) vq[d] = *reinterpret_cast<const u32x4 *>(vp + ((uint64_t)(16 * d) << a.page_log2));
 
       f32x4 s4[4];
 #pragma unroll
@@ -210,6 +276,8 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
         }
         if (S32) s4[i] = mfma16(half8(kq2[i].x, kq2[i].y), qf[KS - 1], s4[i]);
       }
+      if (more) keys(tile + kCacheWaves, next.k);
+      now = next;
       // scores in powers of two, with the value scale's logarithm
       const float lv = __log2f(vs), iv = 1.0f / vs;
       const uint32_t seen = v_bad || tv >= len ? 0u : min(16u, len - tv);
@@ -252,7 +320,7 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
         o[d] = mfma16(half8(vq[d].z, vq[d].w), p1, o[d]);
       }
     }
-    if (bad) atomicOr(a.status + f.seq, ENTRO_F_PAGE);
+    if (bad) atomicOr(a.status + seq, ENTRO_F_PAGE);
     l = add32(add16(l));
 
     // join the wavefronts
@@ -260,79 +328,93 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(&red_o[wave][n][16 * d + 4 * g]) = o[d];
     __syncthreads();
-    const bool whole = chunks_of(a, f.seq, ct) == 1u;
+    const bool whole = t1 - t0 == all_tiles;
     for (uint32_t i = tid; i < heads * (D / 2u); i += 256u) {
       const uint32_t h = i / (D / 2u), d = i % (D / 2u) * 2u;
       float mm = -INFINITY;
 #pragma unroll
-      for (uint32_t w = 0; w < kCacheWaves; ++w) mm = fmaxf(mm, red_ml[w][h].x);
+      for (uint32_t v = 0; v < kCacheWaves; ++v) mm = fmaxf(mm, red_ml[v][h].x);
       float x = 0.0f, y = 0.0f, ll = 0.0f;
 #pragma unroll
-      for (uint32_t w = 0; w < kCacheWaves; ++w) {
-        const float k = join_factor(red_ml[w][h].x, mm);
-        x += k * red_o[w][h][d];
-        y += k * red_o[w][h][d + 1u];
-        ll += k * red_ml[w][h].y;
+      for (uint32_t v = 0; v < kCacheWaves; ++v) {
+        const float k = join_factor(red_ml[v][h].x, mm);
+        x += k * red_o[v][h][d];
+        y += k * red_o[v][h][d + 1u];
+        ll += k * red_ml[v][h].y;
       }
       if (whole) {
         const float r = ll > 0.0f ? 1.0f / ll : ll == 0.0f ? 0.0f : ll;   // NaN stays
-        *reinterpret_cast<uint32_t *>(a.out + f.seq * a.o_t + (int64_t)(head0 + h) * a.o_h + d * 2u) =
+        *reinterpret_cast<uint32_t *>(a.out + seq * a.o_t + (int64_t)(head0 + h) * a.o_h + d * 2u) =
             Elem<T>::pack2(x * r, y * r);
       } else {
-        const uint64_t at = (uint64_t)item * a.n_heads + head0 + h;
+        const uint64_t at = ((uint64_t)w + seq) * a.n_heads + head0 + h;
         *reinterpret_cast<f32x2 *>(a.part_o + at * D + d) = (f32x2){x, y};
         if (d == 0u) a.part_ml[at] = (f32x2){mm, ll};
       }
     }
     __syncthreads();
   }
+  }
 }
 
-// Joins the chunks of a split sequence in their order: one workgroup per
-// sequence and query head; four groups of 64 threads take every fourth chunk
-// (two dimensions a thread), then the groups are joined.
+// Joins the pieces of a split sequence: one workgroup per sequence and query
+// head.  Four groups of 64 threads (two dimensions each) take every fourth
+// piece, eight at a time, then the groups are joined; the order is the same in
+// every call.
 template <entro_dtype T, int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(CacheArg a) {
-  __shared__ float red[4][D + 2];
+  __shared__ float red_o[4][D];
+  __shared__ f32x2 red_ml[4];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, group = tid >> 6;
   const uint32_t b = blockIdx.x, head = blockIdx.y;
-  const uint32_t ct = chunk_tiles(a, lane);
-  const uint32_t n = chunks_of(a, b, ct);
+  const Shares sh = shares_of(a, lane);
+  const uint32_t tiles = rfl(tiles_of(a, b));
+  if (tiles == 0u) return;
+  const uint64_t begin = tiles_before(a, b, lane);
+  const uint32_t w0 = sh.of(begin), n = sh.of(begin + tiles - 1u) - w0 + 1u;
   if (n == 1u) return;
-  uint32_t first = 0;
-  for (uint32_t b0 = 0; b0 < b; b0 += 64u) {
-    const uint32_t own = b0 + lane < b ? chunks_of(a, b0 + lane, ct) : 0u;
-    first += (uint32_t)__shfl((int)wave_scan(own, lane), 63, 64);
-  }
-  const f32x2 *ml = a.part_ml + (uint64_t)first * a.n_heads + head;
-  const float *po = a.part_o + ((uint64_t)first * a.n_heads + head) * D;
-  float m = -INFINITY;
-  for (uint32_t i = lane; i < n; i += 64u) m = fmaxf(m, ml[(uint64_t)i * a.n_heads].x);
-  for (int s = 32; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor(m, s, 64));
-  const uint32_t d = lane * 2u;
-  float x = 0.0f, y = 0.0f, l = 0.0f;
-#pragma unroll 4
-  for (uint32_t i = group; i < n; i += 4u) {
-    const f32x2 v = ml[(uint64_t)i * a.n_heads];
-    const float k = join_factor(v.x, m);
-    l += k * v.y;
-    if (d < D) {
-      const f32x2 p = *reinterpret_cast<const f32x2 *>(po + (uint64_t)i * a.n_heads * D + d);
-      x += k * p.x;
-      y += k * p.y;
+  const uint64_t at = ((uint64_t)w0 + b) * a.n_heads + head;
+  const f32x2 *ml = a.part_ml + at;
+  const float *po = a.part_o + at * D;
+  const uint32_t d = min(lane * 2u, D - 2u);
+  float m = -INFINITY, x = 0.0f, y = 0.0f, l = 0.0f;
+  for (uint32_t i0 = group; i0 < n; i0 += 32u) {
+    f32x2 v[8], p[8];
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) {
+      const uint64_t i = min(i0 + 4u * j, n - 1u);
+      v[j] = ml[i * a.n_heads];
+      p[j] = *reinterpret_cast<const f32x2 *>(po + i * a.n_heads * D + d);
+    }
+    float mn = m;
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) mn = fmaxf(mn, v[j].x);
+    float k = join_factor(m, mn);
+    x *= k;
+    y *= k;
+    l *= k;
+    m = mn;
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) {
+      if (i0 + 4u * j >= n) break;
+      k = join_factor(v[j].x, m);
+      x += k * p[j].x;
+      y += k * p[j].y;
+      l += k * v[j].y;
     }
   }
-  if (d < D) {
-    red[group][d] = x;
-    red[group][d + 1u] = y;
-  }
-  if (lane == 0u) red[group][D] = l;
+  if (lane * 2u < D) *reinterpret_cast<f32x2 *>(&red_o[group][d]) = (f32x2){x, y};
+  if (lane == 0u) red_ml[group] = (f32x2){m, l};
   __syncthreads();
-  if (group == 0u && d < D) {
-    for (int w = 1; w < 4; ++w) {
-      x += red[w][d];
-      y += red[w][d + 1u];
-      l += red[w][D];
+  if (group == 0u && lane * 2u < D) {
+    m = -INFINITY;
+    x = y = l = 0.0f;
+    for (int g = 0; g < 4; ++g) m = fmaxf(m, red_ml[g].x);
+    for (int g = 0; g < 4; ++g) {
+      const float k = join_factor(red_ml[g].x, m);
+      x += k * red_o[g][d];
+      y += k * red_o[g][d + 1u];
+      l += k * red_ml[g].y;
     }
     const float r = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
     *reinterpret_cast<uint32_t *>(a.out + b * a.o_t + head * a.o_h + d * 2u) = Elem<T>::pack2(x * r, y * r);
@@ -343,19 +425,18 @@ __global__ __launch_bounds__(256) void attn_join_kernel(CacheArg a) {
 // host side
 // ---------------------------------------------------------------------------
 
-static uint64_t cache_items(uint64_t n_seq, uint64_t n_kv, uint64_t parts) {
-  // every sequence has at most one chunk more than its tiles / chunk
-  return n_seq + kChunkTarget / (n_kv * parts) + 1u;
-}
+// Shares of one key/value head's tokens.
+static uint32_t cache_shares(uint32_t n_kv, uint32_t parts) { return std::max(1u, kShares / (n_kv * parts)); }
 
 template <entro_dtype T, int D>
 static entro_status launch_cache(CacheArg &a, hipStream_t s) {
-  a.part_ml = reinterpret_cast<f32x2 *>(a.part_o + (uint64_t)a.items * a.n_heads * D);
   const uint32_t y = a.n_kv * a.parts;
-  // no sequence can have a second chunk: no second launch, no idle workgroups
+  // where no sequence is longer than the least share: a workgroup each, nothing to join
   const uint64_t tiles = (((uint64_t)a.table_pages << a.page_log2) + kTile - 1u) / kTile;
-  const bool split = tiles > kMinChunkTiles;
-  uint64_t grid = split ? a.items : a.n_seq;
+  const bool split = tiles > kShareTiles;
+  a.part_ml = reinterpret_cast<f32x2 *>(a.part_o + ((uint64_t)a.n_seq + a.shares) * a.n_heads * D);
+  uint64_t grid = split ? a.shares : a.n_seq;
+  if (!split) a.shares = 0;
   grid = std::max<uint64_t>(1, cap_grid(grid * y) / y);
   (void)hipGetLastError();
   hipLaunchKernelGGL((attn_cache_kernel<T, D>), dim3((uint32_t)grid, y), dim3(256), 0, s, a);
@@ -373,8 +454,8 @@ using namespace entro;
 
 extern "C" uint64_t entro_attn_cache_work_bytes(uint32_t n_seq, uint32_t n_heads, uint32_t n_kv_heads, uint32_t head_dim) {
   if (n_seq == 0 || check_heads(n_heads, n_kv_heads, head_dim, ENTRO_BF16) != ENTRO_OK) return 0;
-  const uint64_t parts = (n_heads / n_kv_heads + kHeadsPerWg - 1u) / kHeadsPerWg;
-  return cache_items(n_seq, n_kv_heads, parts) * n_heads * (head_dim + 2ull) * 4ull;
+  const uint32_t parts = (n_heads / n_kv_heads + kHeadsPerWg - 1u) / kHeadsPerWg;
+  return ((uint64_t)n_seq + cache_shares(n_kv_heads, parts)) * n_heads * (head_dim + 2ull) * 4ull;
 }
 
 extern "C" entro_status entro_attn_cache(const entro_kv_cache *c, const entro_kv_table *t, const entro_attn_cache_args *a,
@@ -414,9 +495,7 @@ extern "C" entro_status entro_attn_cache(const entro_kv_cache *c, const entro_kv
   k.n_heads = a->n_heads;
   k.group = a->n_heads / c->n_kv_heads;
   k.parts = (k.group + kHeadsPerWg - 1u) / kHeadsPerWg;
-  const uint64_t items = cache_items(t->n_seq, k.n_kv, k.parts);
-  if (items > 0x7FFFFFFFull) return ENTRO_E_UNSUPPORTED;
-  k.items = (uint32_t)items;
+  k.shares = cache_shares(k.n_kv, k.parts);
   k.scale = a->scale * kLog2e;
   k.part_o = static_cast<float *>(a->d_work);
   k.status = d_status;

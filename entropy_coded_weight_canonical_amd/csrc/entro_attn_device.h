@@ -91,13 +91,30 @@ __device__ __forceinline__ float add16(float v) {
   return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
-// Inclusive running sum over the wavefront's lanes.
-__device__ __forceinline__ uint32_t wave_scan(uint32_t v, uint32_t lane) {
-  for (uint32_t s = 1; s < 64u; s <<= 1) {
-    const uint32_t o = (uint32_t)__shfl_up((int)v, s, 64);
-    if (lane >= s) v += o;
-  }
+// Inclusive running sum (maximum) over the wavefront's lanes: within rows of 16
+// by shifts, then the rows' ends to the rows after (vector instructions only;
+// all lanes active).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp0(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += dpp0<0x111, 0xF>(v);   // row_shr:1, 2, 4, 8
+  v += dpp0<0x112, 0xF>(v);
+  v += dpp0<0x114, 0xF>(v);
+  v += dpp0<0x118, 0xF>(v);
+  v += dpp0<0x142, 0xA>(v);   // row_bcast:15 into rows 1 and 3
+  v += dpp0<0x143, 0xC>(v);   // row_bcast:31 into rows 2 and 3
   return v;
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp0<0x111, 0xF>(v));
+  v = max(v, dpp0<0x112, 0xF>(v));
+  v = max(v, dpp0<0x114, 0xF>(v));
+  v = max(v, dpp0<0x118, 0xF>(v));
+  v = max(v, dpp0<0x142, 0xA>(v));
+  v = max(v, dpp0<0x143, 0xC>(v));
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
 // The sequence whose items include number `item` when the sequences' items
@@ -113,14 +130,13 @@ __device__ __forceinline__ Found find_item(uint32_t item, uint32_t n_seq, uint32
   for (uint32_t b0 = 0; b0 < n_seq; b0 += 64u) {
     const uint32_t b = b0 + lane;
     const uint32_t own = b < n_seq ? count(b) : 0u;
-    const uint32_t run = wave_scan(own, lane);
+    const uint32_t run = wave_scan(own);
     const uint64_t past = __ballot(before + run > item);
     if (past) {
       const uint32_t at = (uint32_t)__builtin_ctzll(past);
-      const uint32_t begin = before + (uint32_t)__shfl((int)(run - own), (int)at, 64);
-      return {rfl(b0 + at), rfl(item - begin)};
+      return {rfl(b0 + at), rfl(item - before - __builtin_amdgcn_readlane(run - own, at))};
     }
-    before += (uint32_t)__shfl((int)run, 63, 64);
+    before += __builtin_amdgcn_readlane(run, 63);
   }
   return {n_seq, 0u};
 }

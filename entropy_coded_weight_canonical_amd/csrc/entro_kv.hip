@@ -116,7 +116,7 @@ __device__ __forceinline__ uint32_t top_of(uint32_t w, uint32_t top) {
 
 // Largest of v over the workgroup.
 __device__ __forceinline__ uint32_t wg_max(uint32_t v, uint32_t *red) {
-  for (int s = 32; s >= 1; s >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, s, 64));
+  v = wave_max(v);
   const uint32_t waves = blockDim.x >> 6;
   if (waves > 1u) {
     __syncthreads();
