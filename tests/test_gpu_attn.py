@@ -687,3 +687,23 @@ def test_prompt_piece_by_piece(ent):
         bb = bound(e[None, None], m[None, None], np.array([[tp]]), np64(q)[199:, i: i + 1], np.abs(ks).max(), np.abs(vs).max(), 200,
                    "bf16", "cache", 1 / 8)[0, 0]
         assert (np.abs(np64(one)[0, i] - e) <= bb).all()
+
+
+@pytest.mark.parametrize("shape", [(512, 8, 2, 64), (768, 8, 8, 96), (1024, 8, 2, 128)], ids=str)
+def test_attention_block_example(ent, shape):
+    """Coded q, k, v, o products around the cache and attention, against the
+    float32 block.  A cached value is off by up to half a step of its page's
+    range (its largest of 64 x dim values, about 4 sigma, by 127: 1.6% of
+    sigma, uniform: 0.9% rms), keys twice rounded at most; bf16 operands add
+    0.2% each: within 2% of the norm altogether."""
+    say(f"attention block {shape}")
+    import importlib.util
+    import os
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    spec = importlib.util.spec_from_file_location("attention_block", os.path.join(root, "examples", "attention_block.py"))
+    block = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(block)
+    hidden, heads, kv, dim = shape
+    err, _, _ = block.run(hidden, heads, kv, dim, prompt=150, new=9)
+    assert err <= 0.02
