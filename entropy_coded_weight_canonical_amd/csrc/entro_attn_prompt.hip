@@ -14,6 +14,7 @@ struct PromptArg {
   int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;   // bytes
   const int32_t *cu_q, *cu_k;
   uint32_t n_seq, total_q, total_k, n_heads, n_kv;
+  uint32_t heads;                                   // query heads of a workgroup: 1, 2 or 4 of one key/value head
   float scale;                                      // magnitude, times log2(e); 1 where the scale is 0
   uint32_t q_and, q_xor;                            // on a pair of q: the scale's sign, and 0 where the scale is 0
   uint32_t *status;
@@ -75,6 +76,13 @@ __device__ __forceinline__ void scale_in_place(f32x16 &o, float k) {
   }
 }
 
+// The lane's number, not known to be the one it was: what follows from it is
+// worked out at its use, or it would take registers from the loop over tiles.
+__device__ __forceinline__ uint32_t fresh(uint32_t lane) {
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 // Instructions stay on their side of this place.
 __device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
 
@@ -86,8 +94,9 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 }
 
 // ---------------------------------------------------------------------------
-// One workgroup takes 128 queries of one sequence and head, a wavefront 32 of
-// them; the keys come in tiles of 64 that all four wavefronts read from LDS,
+// One workgroup takes 128 rows of one sequence and key/value head, a wavefront
+// 32 of them: 128 queries of one query head or, for short prompts that would
+// leave wavefronts empty, 32 (64) queries of four (two).  The keys come in tiles of 64 that all four wavefronts read from LDS,
 // two tiles in turn: the next one's copies (global memory to LDS, 16 bytes a
 // lane) are in flight while one is computed, one barrier a tile.  Copies go
 // through a buffer resource that ends with the sequence's last row, so rows
@@ -106,15 +115,16 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 // left out of the product and added at the end, to the queries that see them.
 // ---------------------------------------------------------------------------
 template <entro_dtype T, int D>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void attn_prompt_kernel(PromptArg a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3 : 2, D == 64 ? 3 : 2))) void attn_prompt_kernel(PromptArg a) {
   constexpr int KS = D / 16, DT = D / 32, N = D / 32;
   constexpr uint32_t kBytes = kTile * D * 2u, kPieces = D / 8u;   // of a tile, of a row
-  constexpr uint32_t kQueries = 32u, kRows = kQueries * kWaves4;
+  constexpr uint32_t kQueries = 32u;
   // four arrays: the compiler then knows that copies into one tile's need not
   // be waited for before the other's are read
   __shared__ u32x4 lds_k0[kBytes / 16u], lds_k1[kBytes / 16u], lds_v0[kBytes / 16u], lds_v1[kBytes / 16u];
   __shared__ uint32_t lds_special[2];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = rfl(tid >> 6), n = lane & 31u, half = lane >> 5;
+  const uint32_t rows = kQueries * kWaves4 / a.heads;   // queries of a workgroup
   if (blockIdx.x == 0u)
     for (uint32_t b = tid; b < a.n_seq; b += 256u)
       if (!span_of(a.cu_q, b, a.total_q).ok || !span_of(a.cu_k, b, a.total_k).ok) atomicOr(a.status + b, ENTRO_F_LENGTH);
@@ -131,46 +141,41 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   for (uint64_t id = blockIdx.x;; id += gridDim.x) {
     // a key/value head's query heads and tiles stay on one XCD (workgroups go
     // around the 8 in turn) where n_kv is a multiple of 8
-    const uint32_t slot = (uint32_t)(id % a.n_heads);
-    const uint32_t kvh = slot % a.n_kv, head = kvh * (a.n_heads / a.n_kv) + slot / a.n_kv;
-    const Found f = find_item((uint32_t)(id / a.n_heads), a.n_seq, lane, [&](uint32_t b) {
-      return span_of(a.cu_k, b, a.total_k).ok ? (span_of(a.cu_q, b, a.total_q).count + kRows - 1u) / kRows : 0u;
+    const uint32_t slots = a.n_heads / a.heads, slot = (uint32_t)(id % slots);
+    const uint32_t kvh = slot % a.n_kv, head = kvh * (a.n_heads / a.n_kv) + slot / a.n_kv * a.heads + wave % a.heads;
+    const Found f = find_item((uint32_t)(id / slots), a.n_seq, lane, [&](uint32_t b) {
+      return span_of(a.cu_k, b, a.total_k).ok ? (span_of(a.cu_q, b, a.total_q).count + rows - 1u) / rows : 0u;
     });
     if (f.seq == a.n_seq) break;
     const Span sq = span_of(a.cu_q, f.seq, a.total_q), sk = span_of(a.cu_k, f.seq, a.total_k);
     const uint32_t count_q = rfl(sq.count), count_k = rfl(sk.count), begin_q = rfl(sq.begin), begin_k = rfl(sk.begin);
     // the last queries first: they have the most keys
-    const uint32_t wg0 = ((count_q + kRows - 1u) / kRows - 1u - f.local) * kRows;
-    const uint32_t q0 = wg0 + wave * kQueries, qi = q0 + n;
+    const uint32_t wg0 = ((count_q + rows - 1u) / rows - 1u - f.local) * rows;
+    const uint32_t q0 = wg0 + wave / a.heads * kQueries, qi = q0 + n;
     const int64_t shift = (int64_t)count_k - count_q;       // query i sees keys up to i + shift
     const char *kb = a.k + begin_k * a.k_t + kvh * a.k_h, *vb = a.v + begin_k * a.v_t + kvh * a.v_h;
 
-    u32x4 qf[KS];
-    {
-      const char *qp = a.q + (int64_t)(begin_q + min(qi, count_q - 1u)) * a.q_t + head * a.q_h;
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-        qf[s] = (*reinterpret_cast<const u32x4 *>(qp + s * 32 + half * 16) & a.q_and) ^ a.q_xor;
-    }
     f32x16 o[DT];
     float m = -INFINITY, l = 0.0f;   // l: this lane's keys only
 #pragma unroll
     for (int d = 0; d < DT; ++d)
       for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
     // keys that the workgroup, and this wavefront, see
-    const int64_t wg_end = max((int64_t)0, (int64_t)min(wg0 + kRows, count_q) + shift);
+    const int64_t wg_end = max((int64_t)0, (int64_t)min(wg0 + rows, count_q) + shift);
     const int64_t my_end = q0 < count_q ? max((int64_t)0, (int64_t)min(q0 + kQueries, count_q) + shift) : 0;
     const uint32_t tiles = (uint32_t)((wg_end + kTile - 1) / kTile);
     const uint32_t mine = (uint32_t)((my_end + kTile - 1) / kTile);
     // tiles that every query of the workgroup sees whole, an even number
     const uint32_t full = (uint32_t)min((int64_t)tiles, max((int64_t)0, (int64_t)wg0 + shift + 1) / kTile) & ~1u;
 
+    // 32 rows for this wavefront in a tile's place
+    auto quarter = [&](u32x4 *k, u32x4 *v) { return (wave < 2u ? k : v) + (wave & 1u) * (kBytes / 32u); };
     auto copy = [&](uint32_t tile, u32x4 *to_k, u32x4 *to_v) {
-      const uint32_t rows = min(kTile, count_k - tile * kTile);
+      const uint32_t n_rows = min(kTile, count_k - tile * kTile);
       const __amdgpu_buffer_rsrc_t rk = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<char *>(kb + (int64_t)(tile * kTile) * a.k_t), 0, (int)((rows - 1u) * (uint32_t)a.k_t + 2u * D), 0x00020000);
+          const_cast<char *>(kb + (int64_t)(tile * kTile) * a.k_t), 0, (int)((n_rows - 1u) * (uint32_t)a.k_t + 2u * D), 0x00020000);
       const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<char *>(vb + (int64_t)(tile * kTile) * a.v_t), 0, (int)((rows - 1u) * (uint32_t)a.v_t + 2u * D), 0x00020000);
+          const_cast<char *>(vb + (int64_t)(tile * kTile) * a.v_t), 0, (int)((n_rows - 1u) * (uint32_t)a.v_t + 2u * D), 0x00020000);
 #pragma unroll
       for (uint32_t s = 0; s < (uint32_t)N; ++s)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_void *)(to_k + (wave * N + s) * 64u), 16, (int)k_off[s], 0, 0, 0);
@@ -182,6 +187,27 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     if (tid < 2u) lds_special[tid] = 0u;
     __syncthreads();   // no mark is set before
     if (tiles) copy(0, lds_k0, lds_v0);
+    // the wavefront's queries, by way of its quarter of the other tile's place
+    // (whole rows a copy; rows past the end are zeros)
+    u32x4 qf[KS];
+    {
+      const uint32_t ln = fresh(lane);
+      u32x4 *at = quarter(lds_k1, lds_v1);
+      const uint32_t n_rows = q0 < count_q ? min(kQueries, count_q - q0) : 0u;
+      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<char *>(a.q + (int64_t)(begin_q + q0) * a.q_t + head * a.q_h), 0,
+          n_rows ? (int)((n_rows - 1u) * (uint32_t)a.q_t + 2u * D) : 0, 0x00020000);
+#pragma unroll
+      for (uint32_t s = 0; s < (uint32_t)KS; ++s) {
+        const uint32_t i = s * 64u + ln, row = i / kPieces;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(at + s * 64u), 16,
+                                                 (int)(row * (uint32_t)a.q_t + key_piece<D>(row, i % kPieces) * 16u), 0, 0, 0);
+      }
+      wait_lds_copy();
+#pragma unroll
+      for (int s = 0; s < KS; ++s)
+        qf[s] = (at[(ln & 31u) * kPieces + key_piece<D>(ln & 31u, 2 * s + (ln >> 5))] & a.q_and) ^ a.q_xor;
+    }
 
     // The two products are written in the order in which their instructions
     // should run, which the barriers keep the compiler to: LDS reads several
@@ -289,10 +315,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
       // (a mark stays for the tiles after: they take the longer way for nothing)
       const bool special_here = lds_special[t & 1u] != 0u;
       if (t >= mine) return;
-      // what follows from the lane's number is worked out again here, or it
-      // would take registers from the loop over whole tiles
-      uint32_t ln = lane;
-      asm volatile("" : "+v"(ln));
+      const uint32_t ln = fresh(lane);
       f32x16 s[2];
       scores(s, kt, ln);
       const int seen = (int)min(max((int64_t)(q0 + (ln & 31u)) + shift + 1 - (int64_t)t * kTile, (int64_t)0), (int64_t)kTile) - 4 * (int)(ln >> 5);
@@ -337,23 +360,38 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             }
           }
       }
-    if (qi < count_q) {
-      char *op = a.out + (int64_t)(begin_q + qi) * a.o_t + head * a.o_h;
+    // rows out by way of the place of the tile before the last, which every
+    // wavefront has left, so that a store writes whole rows
+    {
+      const uint32_t ln = fresh(lane);
+      u32x4 *at = tiles & 1u ? quarter(lds_k1, lds_v1) : quarter(lds_k0, lds_v0);
 #pragma unroll
       for (int d = 0; d < DT; ++d)
 #pragma unroll
         for (int r = 0; r < 16; r += 4)
-          *reinterpret_cast<u32x2 *>(op + (32 * d + 2 * r + 4 * half) * 2) =
+          reinterpret_cast<u32x2 *>(at)[2u * ((ln & 31u) * kPieces + key_piece<D>(ln & 31u, 4 * d + r / 4)) + (ln >> 5)] =
               (u32x2){Elem<T>::pack2(o[d][r], o[d][r + 1]), Elem<T>::pack2(o[d][r + 2], o[d][r + 3])};
+#pragma unroll
+      for (uint32_t s = 0; s < (uint32_t)KS; ++s) {
+        const uint32_t i = s * 64u + ln, row = i / kPieces, c = i % kPieces;
+        const u32x4 w = at[row * kPieces + key_piece<D>(row, c)];
+        if (q0 + row < count_q)
+          *reinterpret_cast<u32x4 *>(a.out + (int64_t)(begin_q + q0 + row) * a.o_t + head * a.o_h + c * 16u) = w;
+      }
     }
   }
 }
 
 template <entro_dtype T, int D>
-static entro_status launch_prompt(const PromptArg &a, hipStream_t s) {
-  constexpr uint32_t rows = 32u * kWaves4;
+static entro_status launch_prompt(PromptArg &a, hipStream_t s) {
+  const uint32_t group = a.n_heads / a.n_kv;
+  // sequences of 64 queries on average: 256 x 64 (32 / 8 heads of 128) 215 us
+  // by queries, 140 by heads; 128 x 128 the same; 16 x 1024 212 and 220
+  const bool small = a.total_q <= 64ull * a.n_seq;
+  a.heads = !small ? 1u : group % 4u == 0u ? 4u : group % 2u == 0u ? 2u : 1u;
+  const uint32_t rows = 32u * kWaves4 / a.heads;
   uint64_t grid = std::min<uint64_t>(a.total_q, (uint64_t)a.total_q / rows + a.n_seq);
-  grid = std::min<uint64_t>(grid * a.n_heads, 1u << 30);
+  grid = std::min<uint64_t>(grid * (a.n_heads / a.heads), 1u << 30);
   grid = std::max<uint64_t>(1, cap_grid(grid));
   (void)hipGetLastError();
   hipLaunchKernelGGL((attn_prompt_kernel<T, D>), dim3((uint32_t)grid), dim3(256), 0, s, a);
@@ -375,8 +413,8 @@ extern "C" entro_status entro_attn_prompt(const entro_attn_prompt_args *a, uint3
   if ((st = check_rows(a->q, a->total_q)) != ENTRO_OK || (st = check_rows(a->out, a->total_q)) != ENTRO_OK ||
       (st = check_rows(a->k, a->total_k)) != ENTRO_OK || (st = check_rows(a->v, a->total_k)) != ENTRO_OK)
     return st;
-  // the copies of a tile reach 64 rows with 32-bit offsets
-  if (a->k.stride_t > (1 << 23) || a->v.stride_t > (1 << 23)) return ENTRO_E_UNSUPPORTED;
+  // copies reach up to 64 rows with 32-bit offsets
+  if (a->q.stride_t > (1 << 23) || a->k.stride_t > (1 << 23) || a->v.stride_t > (1 << 23)) return ENTRO_E_UNSUPPORTED;
   PromptArg p{};
   p.q = static_cast<const char *>(a->q.d);
   p.k = static_cast<const char *>(a->k.d);
