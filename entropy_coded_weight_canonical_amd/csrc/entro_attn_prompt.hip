@@ -163,30 +163,35 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3
     // keys that the workgroup, and this wavefront, see
     const int64_t wg_end = max((int64_t)0, (int64_t)min(wg0 + rows, count_q) + shift);
     const int64_t my_end = q0 < count_q ? max((int64_t)0, (int64_t)min(q0 + kQueries, count_q) + shift) : 0;
-    const uint32_t tiles = (uint32_t)((wg_end + kTile - 1) / kTile);
+    const uint32_t tiles = rfl((uint32_t)((wg_end + kTile - 1) / kTile));
     const uint32_t mine = (uint32_t)((my_end + kTile - 1) / kTile);
     // tiles that every query of the workgroup sees whole, an even number
     const uint32_t full = (uint32_t)min((int64_t)tiles, max((int64_t)0, (int64_t)wg0 + shift + 1) / kTile) & ~1u;
 
     // 32 rows for this wavefront in a tile's place
     auto quarter = [&](u32x4 *k, u32x4 *v) { return (wave < 2u ? k : v) + (wave & 1u) * (kBytes / 32u); };
-    auto copy = [&](uint32_t tile, u32x4 *to_k, u32x4 *to_v) {
-      const uint32_t n_rows = min(kTile, count_k - tile * kTile);
-      const __amdgpu_buffer_rsrc_t rk = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<char *>(kb + (int64_t)(tile * kTile) * a.k_t), 0, (int)((n_rows - 1u) * (uint32_t)a.k_t + 2u * D), 0x00020000);
-      const __amdgpu_buffer_rsrc_t rv = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<char *>(vb + (int64_t)(tile * kTile) * a.v_t), 0, (int)((n_rows - 1u) * (uint32_t)a.v_t + 2u * D), 0x00020000);
+    // A tile's rows (none past the last tile: the copies then write zeros), and
+    // piece s of this wavefront's N copies.
+    auto rows_at = [&](const char *from, int64_t stride, uint32_t tile) {
+      const uint32_t n_rows = tile < tiles ? min(kTile, count_k - tile * kTile) : 0u;
+      const uint32_t bytes = n_rows ? (n_rows - 1u) * (uint32_t)stride + 2u * D : 0u;
+      return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(from + (int64_t)(tile * kTile) * stride), 0, (int)rfl(bytes),
+                                               0x00020000);
+    };
+    auto copy = [&](__amdgpu_buffer_rsrc_t r, const uint32_t (&off)[N], u32x4 *to, uint32_t s) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + (wave * N + s) * 64u), 16, (int)off[s], 0, 0, 0);
+    };
+    auto copy_all = [&](uint32_t tile, u32x4 *to_k, u32x4 *to_v) {
+      const __amdgpu_buffer_rsrc_t rk = rows_at(kb, a.k_t, tile), rv = rows_at(vb, a.v_t, tile);
 #pragma unroll
-      for (uint32_t s = 0; s < (uint32_t)N; ++s)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (lds_void *)(to_k + (wave * N + s) * 64u), 16, (int)k_off[s], 0, 0, 0);
+      for (uint32_t s = 0; s < (uint32_t)N; ++s) copy(rk, k_off, to_k, s);
 #pragma unroll
-      for (uint32_t s = 0; s < (uint32_t)N; ++s)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (lds_void *)(to_v + (wave * N + s) * 64u), 16, (int)v_off[s], 0, 0, 0);
+      for (uint32_t s = 0; s < (uint32_t)N; ++s) copy(rv, v_off, to_v, s);
     };
     __syncthreads();   // the last item's tiles and marks have been read
     if (tid < 2u) lds_special[tid] = 0u;
     __syncthreads();   // no mark is set before
-    if (tiles) copy(0, lds_k0, lds_v0);
+    if (tiles) copy_all(0, lds_k0, lds_v0);
     // the wavefront's queries, by way of its quarter of the other tile's place
     // (whole rows a copy; rows past the end are zeros)
     u32x4 qf[KS];
@@ -218,7 +223,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3
       const uint32_t at = r * (2u * D) + (uint32_t)(i / KS * 64 * D) + key_piece<D>(r, 2 * (i % KS) + (ln >> 5)) * 16u;
       return *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(kt) + at);
     };
-    auto scores = [&](f32x16 (&s)[2], const u32x4 *kt, uint32_t ln) {
+    auto scores = [&](f32x16 (&s)[2], const u32x4 *kt, uint32_t ln, auto between) {
       constexpr int AHEAD = 6;
       u32x4 w[AHEAD];
 #pragma unroll
@@ -231,6 +236,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3
           for (int r = 0; r < 16; ++r) s[i / KS][r] = 0.0f;
         s[i / KS] = Elem<T>::mfma32(w[i % AHEAD], qf[i % KS], s[i / KS]);
         if (i + AHEAD < 2 * KS) w[i % AHEAD] = key(kt, ln, i + AHEAD);
+        between(i);
         in_order();
       }
     };
@@ -294,9 +300,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3
     auto whole = [&](uint32_t t, const u32x4 *kt, const u32x4 *vt, u32x4 *next_k, u32x4 *next_v) {
       wait_lds_copy();
       __syncthreads();   // tile t is there; the other buffer has been read
-      if (t + 1u < tiles) copy(t + 1u, next_k, next_v);
+      // the next tile's copies between the products: one after another they
+      // keep the wavefront from anything else
+      const __amdgpu_buffer_rsrc_t rk = rows_at(kb, a.k_t, t + 1u), rv = rows_at(vb, a.v_t, t + 1u);
       f32x16 s[2];
-      scores(s, kt, lane);
+      scores(s, kt, lane, [&](int i) {
+        if (i % 2) return;
+        if (i / 2 < N) copy(rk, k_off, next_k, i / 2);
+        else if (i / 2 < 2 * N) copy(rv, v_off, next_v, i / 2 - N);
+      });
       raise_to(s);
       outputs(s, vt, lane, [](u32x4 w) { return w; });
     };
@@ -311,13 +323,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3
       }
       if (any) lds_special[t & 1u] = 1u;
       __syncthreads();
-      if (t + 1u < tiles) copy(t + 1u, next_k, next_v);
+      if (t + 1u < tiles) copy_all(t + 1u, next_k, next_v);
       // (a mark stays for the tiles after: they take the longer way for nothing)
       const bool special_here = lds_special[t & 1u] != 0u;
       if (t >= mine) return;
       const uint32_t ln = fresh(lane);
       f32x16 s[2];
-      scores(s, kt, ln);
+      scores(s, kt, ln, [](int) {});
       const int seen = (int)min(max((int64_t)(q0 + (ln & 31u)) + shift + 1 - (int64_t)t * kTile, (int64_t)0), (int64_t)kTile) - 4 * (int)(ln >> 5);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
