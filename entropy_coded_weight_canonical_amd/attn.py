@@ -191,11 +191,11 @@ def _empty(shape, dtype, like, stream):
     """Memory of a result: from the stream that writes it, so that torch does
     not hand it out again before."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(*shape, dtype=dtype, device=like.device)
     if not hasattr(stream, "cuda_stream"):
         raise ValueError("on a raw stream handle the caller gives the memory of results and workspace")
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return torch.empty(*shape, dtype=dtype, device=like.device)
 
 
 def attn_prompt(q, k, v, cu_q, cu_k, status, scale=None, out=None, stream=None):

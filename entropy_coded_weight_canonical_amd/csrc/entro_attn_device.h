@@ -141,6 +141,15 @@ __device__ __forceinline__ Found find_item(uint32_t item, uint32_t n_seq, uint32
   return {n_seq, 0u};
 }
 
+// All sequences' items together.
+template <typename Count>
+__device__ __forceinline__ uint32_t count_items(uint32_t n_seq, uint32_t lane, Count count) {
+  uint32_t sum = 0;
+  for (uint32_t b0 = 0; b0 < n_seq; b0 += 64u)
+    sum += __builtin_amdgcn_readlane(wave_scan(b0 + lane < n_seq ? count(b0 + lane) : 0u), 63);
+  return sum;
+}
+
 // Rows of sequence b from its running sums, with what is wrong with them.
 struct Span {
   uint32_t begin, count;

@@ -14,6 +14,7 @@ struct PromptArg {
   int64_t q_t, q_h, k_t, k_h, v_t, v_h, o_t, o_h;   // bytes
   const int32_t *cu_q, *cu_k;
   uint32_t n_seq, total_q, total_k, n_heads, n_kv;
+  uint32_t turned;                                  // this many of the first items in reverse order
   uint32_t heads;                                   // query heads of a workgroup: 1, 2 or 4 of one key/value head
   float scale;                                      // magnitude, times log2(e); 1 where the scale is 0
   uint32_t q_and, q_xor;                            // on a pair of q: the scale's sign, and 0 where the scale is 0
@@ -138,14 +139,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3
     v_off[s] = r * (uint32_t)a.v_t + value_piece<D>(r, c) * 16u;
   }
 
+  auto items = [&](uint32_t b) {   // workgroups of sequence b for a key/value head
+    return span_of(a.cu_k, b, a.total_k).ok ? (span_of(a.cu_q, b, a.total_q).count + rows - 1u) / rows : 0u;
+  };
+  const uint32_t turned = a.turned ? min(a.turned, count_items(a.n_seq, lane, items)) : 0u;
   for (uint64_t id = blockIdx.x;; id += gridDim.x) {
     // a key/value head's query heads and tiles stay on one XCD (workgroups go
     // around the 8 in turn) where n_kv is a multiple of 8
     const uint32_t slots = a.n_heads / a.heads, slot = (uint32_t)(id % slots);
     const uint32_t kvh = slot % a.n_kv, head = kvh * (a.n_heads / a.n_kv) + slot / a.n_kv * a.heads + wave % a.heads;
-    const Found f = find_item((uint32_t)(id / slots), a.n_seq, lane, [&](uint32_t b) {
-      return span_of(a.cu_k, b, a.total_k).ok ? (span_of(a.cu_q, b, a.total_q).count + rows - 1u) / rows : 0u;
-    });
+    uint32_t item = (uint32_t)(id / slots);
+    if (item < turned) item = turned - 1u - item;
+    const Found f = find_item(item, a.n_seq, lane, items);
     if (f.seq == a.n_seq) break;
     const Span sq = span_of(a.cu_q, f.seq, a.total_q), sk = span_of(a.cu_k, f.seq, a.total_k);
     const uint32_t count_q = rfl(sq.count), count_k = rfl(sk.count), begin_q = rfl(sq.begin), begin_k = rfl(sk.begin);
@@ -405,6 +410,10 @@ static entro_status launch_prompt(PromptArg &a, hipStream_t s) {
   uint64_t grid = std::min<uint64_t>(a.total_q, (uint64_t)a.total_q / rows + a.n_seq);
   grid = std::min<uint64_t>(grid * (a.n_heads / a.heads), 1u << 30);
   grid = std::max<uint64_t>(1, cap_grid(grid));
+  // Where all workgroups run at once, the 256 first get a CU each and the rest
+  // follow in the same order: the first ones' order is turned around, so that
+  // the CUs with the least of them to do get the most of the rest.
+  a.turned = grid <= 512u ? 256u / (a.n_heads / a.heads) : 0u;
   (void)hipGetLastError();
   hipLaunchKernelGGL((attn_prompt_kernel<T, D>), dim3((uint32_t)grid), dim3(256), 0, s, a);
   return hipGetLastError() == hipSuccess ? ENTRO_OK : ENTRO_E_HIP;
