@@ -69,6 +69,7 @@ _PROMPT = struct.Struct("@PqqPqqPqqPqqPPIIIIIIif")
 _STORE = struct.Struct("@PqqPqqPPIi")
 _CACHE = struct.Struct("@PqqPqqPIifPQ")
 _TABLE = struct.Struct("@PIIIi")
+_PAGES = struct.Struct("@PPPPIIII")
 
 # torch and what of it the calls use, from the first call on (the package's
 # host side works without)
@@ -119,7 +120,7 @@ class KVCache:
     ``k_scales`` / ``v_scales`` float32 [pages][kv heads].  Holds the tensors,
     so that the device memory outlives the calls."""
 
-    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "tensors", "desc")
+    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "tensors", "kv_heads", "dim", "desc")
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
         _torch_once()
@@ -128,16 +129,13 @@ class KVCache:
         pages, kv, page, dim = k_codes.shape
         if v_codes.shape != (pages, kv, dim, page) or k_scales.shape != (pages, kv) or v_scales.shape != (pages, kv):
             raise ValueError("the shapes of codes and scales do not belong together")
-        i8, f32 = torch.int8, torch.float32
-        if not (k_codes.dtype is i8 and v_codes.dtype is i8 and k_scales.dtype is f32 and v_scales.dtype is f32
-                and k_codes.is_cuda and v_codes.is_cuda and k_scales.is_cuda and v_scales.is_cuda
-                and k_codes.is_contiguous() and v_codes.is_contiguous() and k_scales.is_contiguous()
-                and v_scales.is_contiguous()):
-            raise ValueError("int8 codes and float32 scales, contiguous and on the GPU, expected")
-        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
-        self.tensors = (k_codes, v_codes, k_scales, v_scales)
-        self.desc = Cache(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), pages, page, kv,
-                          dim)
+        for x, dtype in ((k_codes, torch.int8), (v_codes, torch.int8), (k_scales, torch.float32), (v_scales, torch.float32)):
+            if x.dtype is not dtype or not x.is_cuda or not x.is_contiguous():
+                raise ValueError("int8 codes and float32 scales, contiguous and on the GPU, expected")
+        self.tensors = self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.kv_heads, self.dim = kv, dim
+        self.desc = _PAGES.pack(k_codes.data_ptr(), v_codes.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), pages, page,
+                                kv, dim)
 
     @classmethod
     def empty(cls, n_pages: int, n_kv_heads: int, head_dim: int, page_tokens: int = 64, device="cuda"):
@@ -233,13 +231,13 @@ def kv_store(cache: KVCache, k, v, table, held, cu_new, status, stream=None) -> 
     sequence (``entro_kv_store``)."""
     _torch_once()
     n = table.shape[0]
-    kv, dim = cache.k_codes.shape[1], cache.k_codes.shape[3]
+    kv, dim = cache.kv_heads, cache.dim
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v have the same rows")
     t = k.dtype
     a = _STORE.pack(*_rows(k, "k", t, kv, dim), *_rows(v, "v", t, kv, dim), _ints(held, "held", n),
                     _ints(cu_new, "cu_new", n + 1), k.shape[0], _dtype_id(t))
-    _call("entro_kv_store", ctypes.byref(cache.desc), _table(table, n), a, _ints(status, "status", n),
+    _call("entro_kv_store", cache.desc, _table(table, n), a, _ints(status, "status", n),
           _on(stream, k, v, *cache.tensors, table, held, cu_new, status))
 
 
@@ -250,7 +248,7 @@ def kv_load(cache: KVCache, table, first, cu_out, total: int, status, dtype=None
     bfloat16) or the pair ``out``."""
     _torch_once()
     n = table.shape[0]
-    kv, dim = cache.k_codes.shape[1], cache.k_codes.shape[3]
+    kv, dim = cache.kv_heads, cache.dim
     if out is None:
         dtype = torch.bfloat16 if dtype is None else dtype
         out = (_empty((total, kv, dim), dtype, cache.k_codes, stream), _empty((total, kv, dim), dtype, cache.k_codes, stream))
@@ -260,7 +258,7 @@ def kv_load(cache: KVCache, table, first, cu_out, total: int, status, dtype=None
     t = k.dtype
     a = _STORE.pack(*_rows(k, "k", t, kv, dim), *_rows(v, "v", t, kv, dim), _ints(first, "first", n),
                     _ints(cu_out, "cu_out", n + 1), total, _dtype_id(t))
-    _call("entro_kv_load", ctypes.byref(cache.desc), _table(table, n), a, _ints(status, "status", n),
+    _call("entro_kv_load", cache.desc, _table(table, n), a, _ints(status, "status", n),
           _on(stream, k, v, *cache.tensors, table, first, cu_out, status))
     return k, v
 
@@ -286,9 +284,9 @@ def attn_cache(q, cache: KVCache, table, lens, status, scale=None, out=None, wor
     if q.dim() != 3:
         raise ValueError("q is [sequences][heads][dim]")
     n, heads, dim = q.shape
-    kv = cache.desc.n_kv_heads
-    if dim != cache.desc.head_dim:
-        raise ValueError(f"q has head dimension {dim}, the cache {cache.desc.head_dim}")
+    kv = cache.kv_heads
+    if dim != cache.dim:
+        raise ValueError(f"q has head dimension {dim}, the cache {cache.dim}")
     t = q.dtype
     if out is None:
         out = _empty((n, heads, dim), t, q, stream)
@@ -308,6 +306,6 @@ def attn_cache(q, cache: KVCache, table, lens, status, scale=None, out=None, wor
         raise ValueError("work: a contiguous tensor on the GPU expected")
     a = _CACHE.pack(*_rows(q, "q", t, heads, dim), *ro, _ints(lens, "lens", n), heads, _dtype_id(t),
                     1.0 / math.sqrt(dim) if scale is None else scale, work.data_ptr(), work.numel() * work.element_size())
-    _call("entro_attn_cache", ctypes.byref(cache.desc), _table(table, n), a, _ints(status, "status", n),
+    _call("entro_attn_cache", cache.desc, _table(table, n), a, _ints(status, "status", n),
           _on(stream, q, *cache.tensors, table, lens, status, out, work))
     return out

@@ -131,9 +131,6 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
   __shared__ f32x2 red_ml[kCacheWaves][kHeadsPerWg];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
   const uint32_t n = lane & 15u, g = lane >> 4;
-  const uint32_t kvh = blockIdx.y / a.parts, h0 = (blockIdx.y % a.parts) * kHeadsPerWg;
-  const uint32_t heads = min(kHeadsPerWg, a.group - h0);
-  const uint32_t head0 = kvh * a.group + h0;
   const uint32_t page = 1u << a.page_log2;
   if (blockIdx.x == 0u && blockIdx.y == 0u)
     for (uint32_t b = tid; b < a.n_seq; b += 256u) {
@@ -141,220 +138,224 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
       cache_len(a, b, &ok);
       if (!ok) atomicOr(a.status + b, ENTRO_F_LENGTH);
     }
-  // empty sequences have no piece
-  if (blockIdx.x == 0u)
-    for (uint32_t b = wave; b < a.n_seq; b += kCacheWaves)
-      if (cache_len(a, b) == 0u)
-        for (uint32_t i = lane; i < heads * (D / 2u); i += 64u)
-          *reinterpret_cast<uint32_t *>(a.out + b * a.o_t + (int64_t)(head0 + i / (D / 2u)) * a.o_h + i % (D / 2u) * 4u) = 0u;
   Shares sh{};
   if (a.shares) sh = shares_of(a, lane);
   const uint32_t units = a.shares ? sh.n : a.n_seq;
-  for (uint32_t w = blockIdx.x; w < units; w += gridDim.x) {
-  // the tiles t0 .. t1 - 1 of sequence `seq` that come next, of the `left` that the share still has
-  uint32_t seq, t0;
-  uint64_t left;
-  if (a.shares) {
-    const uint64_t begin = sh.begin(w);
-    left = sh.begin(w + 1u) - begin;
-    uint64_t before = 0;
-    seq = 0u;
-    t0 = 0u;
-    for (uint32_t b0 = 0; b0 < a.n_seq; b0 += 64u) {
-      const uint32_t own = b0 + lane < a.n_seq ? tiles_of(a, b0 + lane) : 0u;
-      const uint32_t run = wave_scan(own);
-      const uint64_t past = __ballot(before + run > begin);
-      if (past) {
-        const uint32_t at = (uint32_t)__builtin_ctzll(past);
-        seq = rfl(b0 + at);
-        t0 = rfl((uint32_t)(begin - before - __builtin_amdgcn_readlane(run - own, at)));
-        break;
-      }
-      before += __builtin_amdgcn_readlane(run, 63);
-    }
-  } else {
-    seq = w;
-    t0 = 0u;
-    left = tiles_of(a, w);
-  }
-  for (; left; ++seq, t0 = 0u) {
-    const uint32_t len = cache_len(a, seq), all_tiles = (len + kTile - 1u) / kTile;
-    const uint32_t t1 = (uint32_t)min((uint64_t)all_tiles, t0 + left);
-    if (t1 == t0) continue;   // an empty sequence
-    left -= t1 - t0;
-    const int32_t *row = a.table + (uint64_t)seq * a.table_stride;
-
-    // the query head of this lane's column, as f16 times 2^-e
-    f16v8 qf[KS];
-    float c;                               // score = c * key scale * product
-    {
-      u32x4 raw[KS];
-      const char *q = a.q + seq * a.q_t + (int64_t)(head0 + min(n, heads - 1u)) * a.q_h;
-#pragma unroll
-      for (int s = 0; s < S64; ++s) {
-        raw[2 * s] = *reinterpret_cast<const u32x4 *>(q + (64 * s + 16 * g) * 2);
-        raw[2 * s + 1] = *reinterpret_cast<const u32x4 *>(q + (64 * s + 16 * g + 8) * 2);
-      }
-      if (S32) raw[KS - 1] = *reinterpret_cast<const u32x4 *>(q + (64 * S64 + 8 * g) * 2);
-      float top = 0.0f;
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(Elem<T>::lo(raw[s][e])), fabsf(Elem<T>::hi(raw[s][e]))));
-      top = max32(max16(top));
-      int e2 = 0;
-      if (T == ENTRO_BF16) e2 = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;   // bf16 denormals: -127
-      c = ldexpf(a.scale, e2);
-#pragma unroll
-      for (int s = 0; s < KS; ++s) {
-        if (T == ENTRO_F16) {
-          qf[s] = __builtin_bit_cast(f16v8, raw[s]);
-        } else {
-          u32x4 w;
-          for (int e = 0; e < 4; ++e)
-            w[e] = Elem<ENTRO_F16>::pack2(ldexpf(Elem<T>::lo(raw[s][e]), -e2), ldexpf(Elem<T>::hi(raw[s][e]), -e2));
-          qf[s] = __builtin_bit_cast(f16v8, w);
+  for (uint32_t part = blockIdx.y; part < a.n_kv * a.parts; part += gridDim.y)
+    for (uint32_t w = blockIdx.x; w < units; w += gridDim.x) {
+      const uint32_t kvh = part / a.parts, h0 = (part % a.parts) * kHeadsPerWg;
+      const uint32_t heads = min(kHeadsPerWg, a.group - h0);
+      const uint32_t head0 = kvh * a.group + h0;
+      // empty sequences have no piece
+      if (w == 0u)
+        for (uint32_t b = wave; b < a.n_seq; b += kCacheWaves)
+          if (cache_len(a, b) == 0u)
+            for (uint32_t i = lane; i < heads * (D / 2u); i += 64u)
+              *reinterpret_cast<uint32_t *>(a.out + b * a.o_t + (int64_t)(head0 + i / (D / 2u)) * a.o_h + i % (D / 2u) * 4u) = 0u;
+      // the tiles t0 .. t1 - 1 of sequence `seq` that come next, of the `left` that the share still has
+      uint32_t seq, t0;
+      uint64_t left;
+      if (a.shares) {
+        const uint64_t begin = sh.begin(w);
+        left = sh.begin(w + 1u) - begin;
+        uint64_t before = 0;
+        seq = 0u;
+        t0 = 0u;
+        for (uint32_t b0 = 0; b0 < a.n_seq; b0 += 64u) {
+          const uint32_t own = b0 + lane < a.n_seq ? tiles_of(a, b0 + lane) : 0u;
+          const uint32_t run = wave_scan(own);
+          const uint64_t past = __ballot(before + run > begin);
+          if (past) {
+            const uint32_t at = (uint32_t)__builtin_ctzll(past);
+            seq = rfl(b0 + at);
+            t0 = rfl((uint32_t)(begin - before - __builtin_amdgcn_readlane(run - own, at)));
+            break;
+          }
+          before += __builtin_amdgcn_readlane(run, 63);
         }
-      }
-    }
-
-    f32x4 o[DT];
-#pragma unroll
-    for (int d = 0; d < DT; ++d) o[d] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    float m = -INFINITY, l = 0.0f;   // l: this lane's tokens only
-    bool bad = false;
-
-    // Pages of the 16-token blocks that this lane reads keys of (n / 4) and
-    // values of (g).  A block past the end, or of a page that does not exist,
-    // reads page 0 and counts as hidden.
-    struct Pages {
-      int32_t k, v;
-    };
-    auto pages = [&](uint32_t tile) {
-      const uint32_t tk = tile * kTile + (n >> 2) * 16u, tv = tile * kTile + g * 16u;
-      return (Pages){tk < len ? row[tk >> a.page_log2] : 0, tv < len ? row[tv >> a.page_log2] : 0};
-    };
-    u32x4 kq[4][S64], vq[DT];
-    u32x2 kq2[4];
-    auto keys = [&](uint32_t tile, int32_t p) {
-      const uint32_t tk = tile * kTile + (n >> 2) * 16u;
-      const uint64_t at = (uint64_t)((uint32_t)p < a.n_pages ? (uint32_t)p : 0u) * a.n_kv + kvh;
-      const int8_t *kp = a.k_codes + ((at << a.page_log2) + (tk & (page - 1u)) + (n & 3u)) * D;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int s = 0; s < S64; ++s) kq[i][s] = *reinterpret_cast<const u32x4 *>(kp + 4 * i * D + 64 * s + 16 * g);
-        if (S32) kq2[i] = *reinterpret_cast<const u32x2 *>(kp + 4 * i * D + 64 * S64 + 8 * g);
-      }
-    };
-    const uint32_t first = t0 + wave;
-    Pages now{}, next{};
-    if (first < t1) {
-      now = pages(first);
-      keys(first, now.k);
-    }
-    for (uint32_t tile = first; tile < t1; tile += kCacheWaves) {
-      const bool more = tile + kCacheWaves < t1;
-      if (more) next = pages(tile + kCacheWaves);
-      const uint32_t tv = tile * kTile + g * 16u;
-      const bool v_bad = (uint32_t)now.v >= a.n_pages;
-      bad |= v_bad;
-      const uint64_t av = (uint64_t)(v_bad ? 0u : (uint32_t)now.v) * a.n_kv + kvh;
-      const int8_t *vp = a.v_codes + ((av * D + n) << a.page_log2) + (tv & (page - 1u));
-      const float ks = a.k_scales[av] * c;   // rows 4 g + r of the products are tokens of block g
-      const float vs = fmaxf(a.v_scales[av], 1.17549435e-38f);
-#pragma unroll
-      for (int d = 0; d < DT; ++d) vq[d] = *reinterpret_cast<const u32x4 *>(vp + ((uint64_t)(16 * d) << a.page_log2));
-
-      f32x4 s4[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s4[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int s = 0; s < S64; ++s) {
-          s4[i] = mfma16(half8(kq[i][s].x, kq[i][s].y), qf[2 * s], s4[i]);
-          s4[i] = mfma16(half8(kq[i][s].z, kq[i][s].w), qf[2 * s + 1], s4[i]);
-        }
-        if (S32) s4[i] = mfma16(half8(kq2[i].x, kq2[i].y), qf[KS - 1], s4[i]);
-      }
-      if (more) keys(tile + kCacheWaves, next.k);
-      now = next;
-      // scores in powers of two, with the value scale's logarithm
-      const float lv = __log2f(vs), iv = 1.0f / vs;
-      const uint32_t seen = v_bad || tv >= len ? 0u : min(16u, len - tv);
-      float mx = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        for (int r = 0; r < 4; ++r) {
-          const float t = (uint32_t)(4 * i + r) < seen ? s4[i][r] * ks + lv : -INFINITY;
-          s4[i][r] = t;
-          mx = fmaxf(mx, t);
-        }
-      mx = max32(max16(mx));
-      if (__any(mx > m)) {
-        const float mn = fmaxf(m, mx);
-        const float k = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
-        m = mn;
-        l *= k;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[d] *= k;
-      }
-      const float off = m == -INFINITY ? 0.0f : m - 15.0f;
-      float sum = 0.0f;
-      u32x4 pw[2];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float p[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          p[r] = exp2_fast(s4[i][r] - off);
-          sum += p[r];
-        }
-        pw[i >> 1][2 * (i & 1)] = Elem<ENTRO_F16>::pack2(p[0], p[1]);
-        pw[i >> 1][2 * (i & 1) + 1] = Elem<ENTRO_F16>::pack2(p[2], p[3]);
-      }
-      l += seen ? sum * iv : 0.0f;
-      const f16v8 p0 = __builtin_bit_cast(f16v8, pw[0]), p1 = __builtin_bit_cast(f16v8, pw[1]);
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        o[d] = mfma16(half8(vq[d].x, vq[d].y), p0, o[d]);
-        o[d] = mfma16(half8(vq[d].z, vq[d].w), p1, o[d]);
-      }
-    }
-    if (bad) atomicOr(a.status + seq, ENTRO_F_PAGE);
-    l = add32(add16(l));
-
-    // join the wavefronts
-    if (g == 0u) red_ml[wave][n] = (f32x2){m, l};
-#pragma unroll
-    for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(&red_o[wave][n][16 * d + 4 * g]) = o[d];
-    __syncthreads();
-    const bool whole = t1 - t0 == all_tiles;
-    for (uint32_t i = tid; i < heads * (D / 2u); i += 256u) {
-      const uint32_t h = i / (D / 2u), d = i % (D / 2u) * 2u;
-      float mm = -INFINITY;
-#pragma unroll
-      for (uint32_t v = 0; v < kCacheWaves; ++v) mm = fmaxf(mm, red_ml[v][h].x);
-      float x = 0.0f, y = 0.0f, ll = 0.0f;
-#pragma unroll
-      for (uint32_t v = 0; v < kCacheWaves; ++v) {
-        const float k = join_factor(red_ml[v][h].x, mm);
-        x += k * red_o[v][h][d];
-        y += k * red_o[v][h][d + 1u];
-        ll += k * red_ml[v][h].y;
-      }
-      if (whole) {
-        const float r = ll > 0.0f ? 1.0f / ll : ll == 0.0f ? 0.0f : ll;   // NaN stays
-        *reinterpret_cast<uint32_t *>(a.out + seq * a.o_t + (int64_t)(head0 + h) * a.o_h + d * 2u) =
-            Elem<T>::pack2(x * r, y * r);
       } else {
-        const uint64_t at = ((uint64_t)w + seq) * a.n_heads + head0 + h;
-        *reinterpret_cast<f32x2 *>(a.part_o + at * D + d) = (f32x2){x, y};
-        if (d == 0u) a.part_ml[at] = (f32x2){mm, ll};
+        seq = w;
+        t0 = 0u;
+        left = tiles_of(a, w);
+      }
+      for (; left; ++seq, t0 = 0u) {
+        const uint32_t len = cache_len(a, seq), all_tiles = (len + kTile - 1u) / kTile;
+        const uint32_t t1 = (uint32_t)min((uint64_t)all_tiles, t0 + left);
+        if (t1 == t0) continue;   // an empty sequence
+        left -= t1 - t0;
+        const int32_t *row = a.table + (uint64_t)seq * a.table_stride;
+
+        // the query head of this lane's column, as f16 times 2^-e
+        f16v8 qf[KS];
+        float c;                               // score = c * key scale * product
+        {
+          u32x4 raw[KS];
+          const char *q = a.q + seq * a.q_t + (int64_t)(head0 + min(n, heads - 1u)) * a.q_h;
+#pragma unroll
+          for (int s = 0; s < S64; ++s) {
+            raw[2 * s] = *reinterpret_cast<const u32x4 *>(q + (64 * s + 16 * g) * 2);
+            raw[2 * s + 1] = *reinterpret_cast<const u32x4 *>(q + (64 * s + 16 * g + 8) * 2);
+          }
+          if (S32) raw[KS - 1] = *reinterpret_cast<const u32x4 *>(q + (64 * S64 + 8 * g) * 2);
+          float top = 0.0f;
+#pragma unroll
+          for (int s = 0; s < KS; ++s)
+            for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(Elem<T>::lo(raw[s][e])), fabsf(Elem<T>::hi(raw[s][e]))));
+          top = max32(max16(top));
+          int e2 = 0;
+          if (T == ENTRO_BF16) e2 = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;   // bf16 denormals: -127
+          c = ldexpf(a.scale, e2);
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {
+            if (T == ENTRO_F16) {
+              qf[s] = __builtin_bit_cast(f16v8, raw[s]);
+            } else {
+              u32x4 w;
+              for (int e = 0; e < 4; ++e)
+                w[e] = Elem<ENTRO_F16>::pack2(ldexpf(Elem<T>::lo(raw[s][e]), -e2), ldexpf(Elem<T>::hi(raw[s][e]), -e2));
+              qf[s] = __builtin_bit_cast(f16v8, w);
+            }
+          }
+        }
+
+        f32x4 o[DT];
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        float m = -INFINITY, l = 0.0f;   // l: this lane's tokens only
+        bool bad = false;
+
+        // Pages of the 16-token blocks that this lane reads keys of (n / 4) and
+        // values of (g).  A block past the end, or of a page that does not exist,
+        // reads page 0 and counts as hidden.
+        struct Pages {
+          int32_t k, v;
+        };
+        auto pages = [&](uint32_t tile) {
+          const uint32_t tk = tile * kTile + (n >> 2) * 16u, tv = tile * kTile + g * 16u;
+          return (Pages){tk < len ? row[tk >> a.page_log2] : 0, tv < len ? row[tv >> a.page_log2] : 0};
+        };
+        u32x4 kq[4][S64], vq[DT];
+        u32x2 kq2[4];
+        auto keys = [&](uint32_t tile, int32_t p) {
+          const uint32_t tk = tile * kTile + (n >> 2) * 16u;
+          const uint64_t at = (uint64_t)((uint32_t)p < a.n_pages ? (uint32_t)p : 0u) * a.n_kv + kvh;
+          const int8_t *kp = a.k_codes + ((at << a.page_log2) + (tk & (page - 1u)) + (n & 3u)) * D;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int s = 0; s < S64; ++s) kq[i][s] = *reinterpret_cast<const u32x4 *>(kp + 4 * i * D + 64 * s + 16 * g);
+            if (S32) kq2[i] = *reinterpret_cast<const u32x2 *>(kp + 4 * i * D + 64 * S64 + 8 * g);
+          }
+        };
+        const uint32_t first = t0 + wave;
+        Pages now{}, next{};
+        if (first < t1) {
+          now = pages(first);
+          keys(first, now.k);
+        }
+        for (uint32_t tile = first; tile < t1; tile += kCacheWaves) {
+          const bool more = tile + kCacheWaves < t1;
+          if (more) next = pages(tile + kCacheWaves);
+          const uint32_t tv = tile * kTile + g * 16u;
+          const bool v_bad = (uint32_t)now.v >= a.n_pages;
+          bad |= v_bad;
+          const uint64_t av = (uint64_t)(v_bad ? 0u : (uint32_t)now.v) * a.n_kv + kvh;
+          const int8_t *vp = a.v_codes + ((av * D + n) << a.page_log2) + (tv & (page - 1u));
+          const float ks = a.k_scales[av] * c;   // rows 4 g + r of the products are tokens of block g
+          const float vs = fmaxf(a.v_scales[av], 1.17549435e-38f);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) vq[d] = *reinterpret_cast<const u32x4 *>(vp + ((uint64_t)(16 * d) << a.page_log2));
+
+          f32x4 s4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s4[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < S64; ++s) {
+              s4[i] = mfma16(half8(kq[i][s].x, kq[i][s].y), qf[2 * s], s4[i]);
+              s4[i] = mfma16(half8(kq[i][s].z, kq[i][s].w), qf[2 * s + 1], s4[i]);
+            }
+            if (S32) s4[i] = mfma16(half8(kq2[i].x, kq2[i].y), qf[KS - 1], s4[i]);
+          }
+          if (more) keys(tile + kCacheWaves, next.k);
+          now = next;
+          // scores in powers of two, with the value scale's logarithm
+          const float lv = __log2f(vs), iv = 1.0f / vs;
+          const uint32_t seen = v_bad || tv >= len ? 0u : min(16u, len - tv);
+          float mx = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            for (int r = 0; r < 4; ++r) {
+              const float t = (uint32_t)(4 * i + r) < seen ? s4[i][r] * ks + lv : -INFINITY;
+              s4[i][r] = t;
+              mx = fmaxf(mx, t);
+            }
+          mx = max32(max16(mx));
+          if (__any(mx > m)) {
+            const float mn = fmaxf(m, mx);
+            const float k = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
+            m = mn;
+            l *= k;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= k;
+          }
+          const float off = m == -INFINITY ? 0.0f : m - 15.0f;
+          float sum = 0.0f;
+          u32x4 pw[2];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float p[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              p[r] = exp2_fast(s4[i][r] - off);
+              sum += p[r];
+            }
+            pw[i >> 1][2 * (i & 1)] = Elem<ENTRO_F16>::pack2(p[0], p[1]);
+            pw[i >> 1][2 * (i & 1) + 1] = Elem<ENTRO_F16>::pack2(p[2], p[3]);
+          }
+          l += seen ? sum * iv : 0.0f;
+          const f16v8 p0 = __builtin_bit_cast(f16v8, pw[0]), p1 = __builtin_bit_cast(f16v8, pw[1]);
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            o[d] = mfma16(half8(vq[d].x, vq[d].y), p0, o[d]);
+            o[d] = mfma16(half8(vq[d].z, vq[d].w), p1, o[d]);
+          }
+        }
+        if (bad) atomicOr(a.status + seq, ENTRO_F_PAGE);
+        l = add32(add16(l));
+
+        // join the wavefronts
+        if (g == 0u) red_ml[wave][n] = (f32x2){m, l};
+#pragma unroll
+        for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(&red_o[wave][n][16 * d + 4 * g]) = o[d];
+        __syncthreads();
+        const bool whole = t1 - t0 == all_tiles;
+        for (uint32_t i = tid; i < heads * (D / 2u); i += 256u) {
+          const uint32_t h = i / (D / 2u), d = i % (D / 2u) * 2u;
+          float mm = -INFINITY;
+#pragma unroll
+          for (uint32_t v = 0; v < kCacheWaves; ++v) mm = fmaxf(mm, red_ml[v][h].x);
+          float x = 0.0f, y = 0.0f, ll = 0.0f;
+#pragma unroll
+          for (uint32_t v = 0; v < kCacheWaves; ++v) {
+            const float k = join_factor(red_ml[v][h].x, mm);
+            x += k * red_o[v][h][d];
+            y += k * red_o[v][h][d + 1u];
+            ll += k * red_ml[v][h].y;
+          }
+          if (whole) {
+            const float r = ll > 0.0f ? 1.0f / ll : ll == 0.0f ? 0.0f : ll;   // NaN stays
+            *reinterpret_cast<uint32_t *>(a.out + seq * a.o_t + (int64_t)(head0 + h) * a.o_h + d * 2u) =
+                Elem<T>::pack2(x * r, y * r);
+          } else {
+            const uint64_t at = ((uint64_t)w + seq) * a.n_heads + head0 + h;
+            *reinterpret_cast<f32x2 *>(a.part_o + at * D + d) = (f32x2){x, y};
+            if (d == 0u) a.part_ml[at] = (f32x2){mm, ll};
+          }
+        }
+        __syncthreads();
       }
     }
-    __syncthreads();
-  }
-  }
 }
 
 // Joins the pieces of a split sequence: one workgroup per sequence and query
@@ -366,59 +367,62 @@ __global__ __launch_bounds__(256) void attn_join_kernel(CacheArg a) {
   __shared__ float red_o[4][D];
   __shared__ f32x2 red_ml[4];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, group = tid >> 6;
-  const uint32_t b = blockIdx.x, head = blockIdx.y;
   const Shares sh = shares_of(a, lane);
-  const uint32_t tiles = rfl(tiles_of(a, b));
-  if (tiles == 0u) return;
-  const uint64_t begin = tiles_before(a, b, lane);
-  const uint32_t w0 = sh.of(begin), n = sh.of(begin + tiles - 1u) - w0 + 1u;
-  if (n == 1u) return;
-  const uint64_t at = ((uint64_t)w0 + b) * a.n_heads + head;
-  const f32x2 *ml = a.part_ml + at;
-  const float *po = a.part_o + at * D;
-  const uint32_t d = min(lane * 2u, D - 2u);
-  float m = -INFINITY, x = 0.0f, y = 0.0f, l = 0.0f;
-  for (uint32_t i0 = group; i0 < n; i0 += 32u) {
-    f32x2 v[8], p[8];
+  for (uint32_t head = blockIdx.y; head < a.n_heads; head += gridDim.y)
+    for (uint32_t b = blockIdx.x; b < a.n_seq; b += gridDim.x) {
+      const uint32_t tiles = rfl(tiles_of(a, b));
+      if (tiles == 0u) continue;
+      const uint64_t begin = tiles_before(a, b, lane);
+      const uint32_t w0 = sh.of(begin), n = sh.of(begin + tiles - 1u) - w0 + 1u;
+      if (n == 1u) continue;
+      const uint64_t at = ((uint64_t)w0 + b) * a.n_heads + head;
+      const f32x2 *ml = a.part_ml + at;
+      const float *po = a.part_o + at * D;
+      const uint32_t d = min(lane * 2u, D - 2u);
+      float m = -INFINITY, x = 0.0f, y = 0.0f, l = 0.0f;
+      for (uint32_t i0 = group; i0 < n; i0 += 32u) {
+        f32x2 v[8], p[8];
 #pragma unroll
-    for (uint32_t j = 0; j < 8; ++j) {
-      const uint64_t i = min(i0 + 4u * j, n - 1u);
-      v[j] = ml[i * a.n_heads];
-      p[j] = *reinterpret_cast<const f32x2 *>(po + i * a.n_heads * D + d);
-    }
-    float mn = m;
+        for (uint32_t j = 0; j < 8; ++j) {
+          const uint64_t i = min(i0 + 4u * j, n - 1u);
+          v[j] = ml[i * a.n_heads];
+          p[j] = *reinterpret_cast<const f32x2 *>(po + i * a.n_heads * D + d);
+        }
+        float mn = m;
 #pragma unroll
-    for (uint32_t j = 0; j < 8; ++j) mn = fmaxf(mn, v[j].x);
-    float k = join_factor(m, mn);
-    x *= k;
-    y *= k;
-    l *= k;
-    m = mn;
+        for (uint32_t j = 0; j < 8; ++j) mn = fmaxf(mn, v[j].x);
+        float k = join_factor(m, mn);
+        x *= k;
+        y *= k;
+        l *= k;
+        m = mn;
 #pragma unroll
-    for (uint32_t j = 0; j < 8; ++j) {
-      if (i0 + 4u * j >= n) break;
-      k = join_factor(v[j].x, m);
-      x += k * p[j].x;
-      y += k * p[j].y;
-      l += k * v[j].y;
+        for (uint32_t j = 0; j < 8; ++j) {
+          if (i0 + 4u * j >= n) break;
+          k = join_factor(v[j].x, m);
+          x += k * p[j].x;
+          y += k * p[j].y;
+          l += k * v[j].y;
+        }
+      }
+      if (lane * 2u < D) *reinterpret_cast<f32x2 *>(&red_o[group][d]) = (f32x2){x, y};
+      if (lane == 0u) red_ml[group] = (f32x2){m, l};
+      __syncthreads();
+      if (group == 0u && lane * 2u < D) {
+        m = -INFINITY;
+        x = y = l = 0.0f;
+        for (int g = 0; g < 4; ++g) m = fmaxf(m, red_ml[g].x);
+        for (int g = 0; g < 4; ++g) {
+          const float k = join_factor(red_ml[g].x, m);
+          x += k * red_o[g][d];
+          y += k * red_o[g][d + 1u];
+          l += k * red_ml[g].y;
+        }
+        const float r = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
+        *reinterpret_cast<uint32_t *>(a.out + b * a.o_t + head * a.o_h + d * 2u) = Elem<T>::pack2(x * r, y * r);
+      }
+      __syncthreads();   // red_o and red_ml are written again
     }
-  }
-  if (lane * 2u < D) *reinterpret_cast<f32x2 *>(&red_o[group][d]) = (f32x2){x, y};
-  if (lane == 0u) red_ml[group] = (f32x2){m, l};
-  __syncthreads();
-  if (group == 0u && lane * 2u < D) {
-    m = -INFINITY;
-    x = y = l = 0.0f;
-    for (int g = 0; g < 4; ++g) m = fmaxf(m, red_ml[g].x);
-    for (int g = 0; g < 4; ++g) {
-      const float k = join_factor(red_ml[g].x, m);
-      x += k * red_o[g][d];
-      y += k * red_o[g][d + 1u];
-      l += k * red_ml[g].y;
-    }
-    const float r = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-    *reinterpret_cast<uint32_t *>(a.out + b * a.o_t + head * a.o_h + d * 2u) = Elem<T>::pack2(x * r, y * r);
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -430,19 +434,16 @@ static uint32_t cache_shares(uint32_t n_kv, uint32_t parts) { return std::max(1u
 
 template <entro_dtype T, int D>
 static entro_status launch_cache(CacheArg &a, hipStream_t s) {
-  const uint32_t y = a.n_kv * a.parts;
   // where no sequence is longer than the least share: a workgroup each, nothing to join
   const uint64_t tiles = (((uint64_t)a.table_pages << a.page_log2) + kTile - 1u) / kTile;
   const bool split = tiles > kShareTiles;
   a.part_ml = reinterpret_cast<f32x2 *>(a.part_o + ((uint64_t)a.n_seq + a.shares) * a.n_heads * D);
-  uint64_t grid = split ? a.shares : a.n_seq;
   if (!split) a.shares = 0;
-  grid = std::max<uint64_t>(1, cap_grid(grid * y) / y);
   (void)hipGetLastError();
-  hipLaunchKernelGGL((attn_cache_kernel<T, D>), dim3((uint32_t)grid, y), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((attn_cache_kernel<T, D>), grid2(split ? a.shares : a.n_seq, a.n_kv * a.parts), dim3(256), 0, s, a);
   if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
   if (split) {
-    hipLaunchKernelGGL((attn_join_kernel<T, D>), dim3(a.n_seq, a.n_heads), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((attn_join_kernel<T, D>), grid2(a.n_seq, a.n_heads), dim3(256), 0, s, a);
     if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
   }
   return ENTRO_OK;

@@ -97,11 +97,11 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 // ---------------------------------------------------------------------------
 // One workgroup takes 128 rows of one sequence and key/value head, a wavefront
 // 32 of them: 128 queries of one query head or, for short prompts that would
-// leave wavefronts empty, 32 (64) queries of four (two).  The keys come in tiles of 64 that all four wavefronts read from LDS,
-// two tiles in turn: the next one's copies (global memory to LDS, 16 bytes a
-// lane) are in flight while one is computed, one barrier a tile.  Copies go
-// through a buffer resource that ends with the sequence's last row, so rows
-// past it arrive as zeros.
+// leave wavefronts empty, 32 (64) queries of four (two).  The keys come in
+// tiles of 64 that all four wavefronts read from LDS, two tiles in turn: the
+// next one's copies (global memory to LDS, 16 bytes a lane) are in flight while
+// one is computed, one barrier a tile.  Copies go through a buffer resource
+// that ends with the sequence's last row, so rows past it arrive as zeros.
 //
 // Scores are K Q^T and outputs V^T P^T with the queries as columns: a lane and
 // the one 32 further hold one query's softmax, whose statistics need one
@@ -115,8 +115,11 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 // wavefronts that copied it, and where it holds infinities or NaN these are
 // left out of the product and added at the end, to the queries that see them.
 // ---------------------------------------------------------------------------
+constexpr int wavefronts_per_simd(int d) { return d == 64 ? 3 : 2; }   // what the registers allow
+
 template <entro_dtype T, int D>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3 : 2, D == 64 ? 3 : 2))) void attn_prompt_kernel(PromptArg a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(wavefronts_per_simd(D), wavefronts_per_simd(D)))) void
+attn_prompt_kernel(PromptArg a) {
   constexpr int KS = D / 16, DT = D / 32, N = D / 32;
   constexpr uint32_t kBytes = kTile * D * 2u, kPieces = D / 8u;   // of a tile, of a row
   constexpr uint32_t kQueries = 32u;
@@ -126,7 +129,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3
   __shared__ uint32_t lds_special[2];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = rfl(tid >> 6), n = lane & 31u, half = lane >> 5;
   const uint32_t rows = kQueries * kWaves4 / a.heads;   // queries of a workgroup
-  if (blockIdx.x == 0u)
+  if (blockIdx.x == 0u && blockIdx.y == 0u)
     for (uint32_t b = tid; b < a.n_seq; b += 256u)
       if (!span_of(a.cu_q, b, a.total_q).ok || !span_of(a.cu_k, b, a.total_k).ok) atomicOr(a.status + b, ENTRO_F_LENGTH);
 
@@ -143,260 +146,260 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(D == 64 ? 3
     return span_of(a.cu_k, b, a.total_k).ok ? (span_of(a.cu_q, b, a.total_q).count + rows - 1u) / rows : 0u;
   };
   const uint32_t turned = a.turned ? min(a.turned, count_items(a.n_seq, lane, items)) : 0u;
-  for (uint64_t id = blockIdx.x;; id += gridDim.x) {
-    // a key/value head's query heads and tiles stay on one XCD (workgroups go
-    // around the 8 in turn) where n_kv is a multiple of 8
-    const uint32_t slots = a.n_heads / a.heads, slot = (uint32_t)(id % slots);
-    const uint32_t kvh = slot % a.n_kv, head = kvh * (a.n_heads / a.n_kv) + slot / a.n_kv * a.heads + wave % a.heads;
-    uint32_t item = (uint32_t)(id / slots);
-    if (item < turned) item = turned - 1u - item;
-    const Found f = find_item(item, a.n_seq, lane, items);
-    if (f.seq == a.n_seq) break;
-    const Span sq = span_of(a.cu_q, f.seq, a.total_q), sk = span_of(a.cu_k, f.seq, a.total_k);
-    const uint32_t count_q = rfl(sq.count), count_k = rfl(sk.count), begin_q = rfl(sq.begin), begin_k = rfl(sk.begin);
-    // the last queries first: they have the most keys
-    const uint32_t wg0 = ((count_q + rows - 1u) / rows - 1u - f.local) * rows;
-    const uint32_t q0 = wg0 + wave / a.heads * kQueries, qi = q0 + n;
-    const int64_t shift = (int64_t)count_k - count_q;       // query i sees keys up to i + shift
-    const char *kb = a.k + begin_k * a.k_t + kvh * a.k_h, *vb = a.v + begin_k * a.v_t + kvh * a.v_h;
+  for (uint32_t slot = blockIdx.x; slot < a.n_heads / a.heads; slot += gridDim.x)
+    for (uint32_t at = blockIdx.y;; at += gridDim.y) {
+      // a key/value head's query heads and tiles stay on one XCD (workgroups go
+      // around the 8 in turn) where n_kv is a multiple of 8
+      const uint32_t kvh = slot % a.n_kv, head = kvh * (a.n_heads / a.n_kv) + slot / a.n_kv * a.heads + wave % a.heads;
+      const uint32_t item = at < turned ? turned - 1u - at : at;
+      const Found f = find_item(item, a.n_seq, lane, items);
+      if (f.seq == a.n_seq) break;
+      const Span sq = span_of(a.cu_q, f.seq, a.total_q), sk = span_of(a.cu_k, f.seq, a.total_k);
+      const uint32_t count_q = rfl(sq.count), count_k = rfl(sk.count), begin_q = rfl(sq.begin), begin_k = rfl(sk.begin);
+      // the last queries first: they have the most keys
+      const uint32_t wg0 = ((count_q + rows - 1u) / rows - 1u - f.local) * rows;
+      const uint32_t q0 = wg0 + wave / a.heads * kQueries, qi = q0 + n;
+      const int64_t shift = (int64_t)count_k - count_q;       // query i sees keys up to i + shift
+      const char *kb = a.k + begin_k * a.k_t + kvh * a.k_h, *vb = a.v + begin_k * a.v_t + kvh * a.v_h;
 
-    f32x16 o[DT];
-    float m = -INFINITY, l = 0.0f;   // l: this lane's keys only
+      f32x16 o[DT];
+      float m = -INFINITY, l = 0.0f;   // l: this lane's keys only
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
-      for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
-    // keys that the workgroup, and this wavefront, see
-    const int64_t wg_end = max((int64_t)0, (int64_t)min(wg0 + rows, count_q) + shift);
-    const int64_t my_end = q0 < count_q ? max((int64_t)0, (int64_t)min(q0 + kQueries, count_q) + shift) : 0;
-    const uint32_t tiles = rfl((uint32_t)((wg_end + kTile - 1) / kTile));
-    const uint32_t mine = (uint32_t)((my_end + kTile - 1) / kTile);
-    // tiles that every query of the workgroup sees whole, an even number
-    const uint32_t full = (uint32_t)min((int64_t)tiles, max((int64_t)0, (int64_t)wg0 + shift + 1) / kTile) & ~1u;
+      for (int d = 0; d < DT; ++d)
+        for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
+      // keys that the workgroup, and this wavefront, see
+      const int64_t wg_end = max((int64_t)0, (int64_t)min(wg0 + rows, count_q) + shift);
+      const int64_t my_end = q0 < count_q ? max((int64_t)0, (int64_t)min(q0 + kQueries, count_q) + shift) : 0;
+      const uint32_t tiles = rfl((uint32_t)((wg_end + kTile - 1) / kTile));
+      const uint32_t mine = (uint32_t)((my_end + kTile - 1) / kTile);
+      // tiles that every query of the workgroup sees whole, an even number
+      const uint32_t full = (uint32_t)min((int64_t)tiles, max((int64_t)0, (int64_t)wg0 + shift + 1) / kTile) & ~1u;
 
-    // 32 rows for this wavefront in a tile's place
-    auto quarter = [&](u32x4 *k, u32x4 *v) { return (wave < 2u ? k : v) + (wave & 1u) * (kBytes / 32u); };
-    // A tile's rows (none past the last tile: the copies then write zeros), and
-    // piece s of this wavefront's N copies.
-    auto rows_at = [&](const char *from, int64_t stride, uint32_t tile) {
-      const uint32_t n_rows = tile < tiles ? min(kTile, count_k - tile * kTile) : 0u;
-      const uint32_t bytes = n_rows ? (n_rows - 1u) * (uint32_t)stride + 2u * D : 0u;
-      return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(from + (int64_t)(tile * kTile) * stride), 0, (int)rfl(bytes),
-                                               0x00020000);
-    };
-    auto copy = [&](__amdgpu_buffer_rsrc_t r, const uint32_t (&off)[N], u32x4 *to, uint32_t s) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + (wave * N + s) * 64u), 16, (int)off[s], 0, 0, 0);
-    };
-    auto copy_all = [&](uint32_t tile, u32x4 *to_k, u32x4 *to_v) {
-      const __amdgpu_buffer_rsrc_t rk = rows_at(kb, a.k_t, tile), rv = rows_at(vb, a.v_t, tile);
-#pragma unroll
-      for (uint32_t s = 0; s < (uint32_t)N; ++s) copy(rk, k_off, to_k, s);
-#pragma unroll
-      for (uint32_t s = 0; s < (uint32_t)N; ++s) copy(rv, v_off, to_v, s);
-    };
-    __syncthreads();   // the last item's tiles and marks have been read
-    if (tid < 2u) lds_special[tid] = 0u;
-    __syncthreads();   // no mark is set before
-    if (tiles) copy_all(0, lds_k0, lds_v0);
-    // the wavefront's queries, by way of its quarter of the other tile's place
-    // (whole rows a copy; rows past the end are zeros)
-    u32x4 qf[KS];
-    {
-      const uint32_t ln = fresh(lane);
-      u32x4 *at = quarter(lds_k1, lds_v1);
-      const uint32_t n_rows = q0 < count_q ? min(kQueries, count_q - q0) : 0u;
-      const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-          const_cast<char *>(a.q + (int64_t)(begin_q + q0) * a.q_t + head * a.q_h), 0,
-          n_rows ? (int)((n_rows - 1u) * (uint32_t)a.q_t + 2u * D) : 0, 0x00020000);
-#pragma unroll
-      for (uint32_t s = 0; s < (uint32_t)KS; ++s) {
-        const uint32_t i = s * 64u + ln, row = i / kPieces;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(at + s * 64u), 16,
-                                                 (int)(row * (uint32_t)a.q_t + key_piece<D>(row, i % kPieces) * 16u), 0, 0, 0);
-      }
-      wait_lds_copy();
-#pragma unroll
-      for (int s = 0; s < KS; ++s)
-        qf[s] = (at[(ln & 31u) * kPieces + key_piece<D>(ln & 31u, 2 * s + (ln >> 5))] & a.q_and) ^ a.q_xor;
-    }
-
-    // The two products are written in the order in which their instructions
-    // should run, which the barriers keep the compiler to: LDS reads several
-    // products ahead of their use, and the exponentials of the next 16 keys
-    // between the products of the last.  (Its own order waited for each read.)
-    auto key = [&](const u32x4 *kt, uint32_t ln, int i) {   // keys 32 (i / KS) on, dimensions 16 (i % KS) on
-      const uint32_t r = ln & 31u;
-      const uint32_t at = r * (2u * D) + (uint32_t)(i / KS * 64 * D) + key_piece<D>(r, 2 * (i % KS) + (ln >> 5)) * 16u;
-      return *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(kt) + at);
-    };
-    auto scores = [&](f32x16 (&s)[2], const u32x4 *kt, uint32_t ln, auto between) {
-      constexpr int AHEAD = 6;
-      u32x4 w[AHEAD];
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) w[i] = key(kt, ln, i);
-      in_order();
-#pragma unroll
-      for (int i = 0; i < 2 * KS; ++i) {
-        if (i % KS == 0)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) s[i / KS][r] = 0.0f;
-        s[i / KS] = Elem<T>::mfma32(w[i % AHEAD], qf[i % KS], s[i / KS]);
-        if (i + AHEAD < 2 * KS) w[i % AHEAD] = key(kt, ln, i + AHEAD);
-        between(i);
-        in_order();
-      }
-    };
-    // Maximum of the lane's query up to this tile.
-    auto raise_to = [&](const f32x16 (&s)[2]) {
-      float mx = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[i][r]);
-      mx = max32(mx);
-      const bool raise = mx * a.scale > m * a.scale + kLag<T>;
-      if (__any(raise)) {
-        const float mn = raise ? mx : m;
-        const float k = mn == -INFINITY ? 1.0f : exp2_fast((m - mn) * a.scale);
-        m = mn;
-        l *= k;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) scale_in_place(o[d], k);
-      }
-    };
-    // Values of 16 tokens from 16 c on, of dimensions 32 d on: the lane gives
-    // the place of row 4 half + (lane / 4) % 4 and the one 8 further.
-    auto value = [&](const u32x4 *vt, uint32_t ln, int c, int d) {
-      const uint32_t r = 4u * (ln >> 5) + ((ln >> 2) & 3u), piece = 2u * ((ln >> 4) & 1u) + ((ln >> 1) & 1u);
-      // (one step from the array: further ones, and the compiler loses track
-      // of which it is)
-      const uint32_t at = (uint32_t)(c * 32 * D) + r * (2u * D) + (ln & 1u) * 8u + value_piece<D>(r, 4 * d + piece) * 16u;
-      const u32x2 lo = read_turned(reinterpret_cast<const char *>(vt) + at),
-                  hi = read_turned(reinterpret_cast<const char *>(vt) + (at + 16u * D));
-      return (u32x4){lo.x, lo.y, hi.x, hi.y};
-    };
-    // Outputs of a tile; kept(w): w, or what is left of it.
-    auto outputs = [&](const f32x16 (&s)[2], const u32x4 *vt, uint32_t ln, auto kept) {
-      const float off = m == -INFINITY ? 0.0f : kLift<T> - m * a.scale;
-      u32x4 p[2], w[DT];
-      auto pair = [&](int c, int e) {   // weights of keys 16 c + 2 e, 2 e + 1 (in the products' order)
-        const float x = exp2_fast(__builtin_fmaf(s[c / 2][c % 2 * 8 + 2 * e], a.scale, off));
-        const float y = exp2_fast(__builtin_fmaf(s[c / 2][c % 2 * 8 + 2 * e + 1], a.scale, off));
-        p[c % 2][e] = Elem<T>::pack2(x, y);
-        l = Elem<T>::add2(p[c % 2][e], l);
+      // 32 rows for this wavefront in a tile's place
+      auto quarter = [&](u32x4 *k, u32x4 *v) { return (wave < 2u ? k : v) + (wave & 1u) * (kBytes / 32u); };
+      // A tile's rows (none past the last tile: the copies then write zeros), and
+      // piece s of this wavefront's N copies.
+      auto rows_at = [&](const char *from, int64_t stride, uint32_t tile) {
+        const uint32_t n_rows = tile < tiles ? min(kTile, count_k - tile * kTile) : 0u;
+        const uint32_t bytes = n_rows ? (n_rows - 1u) * (uint32_t)stride + 2u * D : 0u;
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char *>(from + (int64_t)(tile * kTile) * stride), 0, (int)rfl(bytes),
+                                                 0x00020000);
       };
+      auto copy = [&](__amdgpu_buffer_rsrc_t r, const uint32_t (&off)[N], u32x4 *to, uint32_t s) {
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(to + (wave * N + s) * 64u), 16, (int)off[s], 0, 0, 0);
+      };
+      auto copy_all = [&](uint32_t tile, u32x4 *to_k, u32x4 *to_v) {
+        const __amdgpu_buffer_rsrc_t rk = rows_at(kb, a.k_t, tile), rv = rows_at(vb, a.v_t, tile);
 #pragma unroll
-      for (int d = 0; d < DT; ++d) w[d] = value(vt, ln, 0, d);
-      in_order();
+        for (uint32_t s = 0; s < (uint32_t)N; ++s) copy(rk, k_off, to_k, s);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) pair(0, e);
+        for (uint32_t s = 0; s < (uint32_t)N; ++s) copy(rv, v_off, to_v, s);
+      };
+      __syncthreads();   // the last item's tiles and marks have been read
+      if (tid < 2u) lds_special[tid] = 0u;
+      __syncthreads();   // no mark is set before
+      if (tiles) copy_all(0, lds_k0, lds_v0);
+      // the wavefront's queries, by way of its quarter of the other tile's place
+      // (whole rows a copy; rows past the end are zeros)
+      u32x4 qf[KS];
+      {
+        const uint32_t ln = fresh(lane);
+        u32x4 *at = quarter(lds_k1, lds_v1);
+        const uint32_t n_rows = q0 < count_q ? min(kQueries, count_q - q0) : 0u;
+        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char *>(a.q + (int64_t)(begin_q + q0) * a.q_t + head * a.q_h), 0,
+            n_rows ? (int)((n_rows - 1u) * (uint32_t)a.q_t + 2u * D) : 0, 0x00020000);
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+        for (uint32_t s = 0; s < (uint32_t)KS; ++s) {
+          const uint32_t i = s * 64u + ln, row = i / kPieces;
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)(at + s * 64u), 16,
+                                                   (int)(row * (uint32_t)a.q_t + key_piece<D>(row, i % kPieces) * 16u), 0, 0, 0);
+        }
+        wait_lds_copy();
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          o[d] = Elem<T>::mfma32(kept(w[d]), p[c % 2], o[d]);
-          if (c < 3) {
-            w[d] = value(vt, ln, c + 1, d);
+        for (int s = 0; s < KS; ++s)
+          qf[s] = (at[(ln & 31u) * kPieces + key_piece<D>(ln & 31u, 2 * s + (ln >> 5))] & a.q_and) ^ a.q_xor;
+      }
+
+      // The two products are written in the order in which their instructions
+      // should run, which the barriers keep the compiler to: LDS reads several
+      // products ahead of their use, and the exponentials of the next 16 keys
+      // between the products of the last.  (Its own order waited for each read.)
+      auto key = [&](const u32x4 *kt, uint32_t ln, int i) {   // keys 32 (i / KS) on, dimensions 16 (i % KS) on
+        const uint32_t r = ln & 31u;
+        const uint32_t at = r * (2u * D) + (uint32_t)(i / KS * 64 * D) + key_piece<D>(r, 2 * (i % KS) + (ln >> 5)) * 16u;
+        return *reinterpret_cast<const u32x4 *>(reinterpret_cast<const char *>(kt) + at);
+      };
+      auto scores = [&](f32x16 (&s)[2], const u32x4 *kt, uint32_t ln, auto between) {
+        constexpr int AHEAD = 6;
+        u32x4 w[AHEAD];
 #pragma unroll
-            for (int e = 4 * d / DT; e < 4 * (d + 1) / DT; ++e) pair(c + 1, e);
-          }
+        for (int i = 0; i < AHEAD; ++i) w[i] = key(kt, ln, i);
+        in_order();
+#pragma unroll
+        for (int i = 0; i < 2 * KS; ++i) {
+          if (i % KS == 0)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) s[i / KS][r] = 0.0f;
+          s[i / KS] = Elem<T>::mfma32(w[i % AHEAD], qf[i % KS], s[i / KS]);
+          if (i + AHEAD < 2 * KS) w[i % AHEAD] = key(kt, ln, i + AHEAD);
+          between(i);
           in_order();
         }
-    };
+      };
+      // Maximum of the lane's query up to this tile.
+      auto raise_to = [&](const f32x16 (&s)[2]) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[i][r]);
+        mx = max32(mx);
+        const bool raise = mx * a.scale > m * a.scale + kLag<T>;
+        if (__any(raise)) {
+          const float mn = raise ? mx : m;
+          const float k = mn == -INFINITY ? 1.0f : exp2_fast((m - mn) * a.scale);
+          m = mn;
+          l *= k;
+#pragma unroll
+          for (int d = 0; d < DT; ++d) scale_in_place(o[d], k);
+        }
+      };
+      // Values of 16 tokens from 16 c on, of dimensions 32 d on: the lane gives
+      // the place of row 4 half + (lane / 4) % 4 and the one 8 further.
+      auto value = [&](const u32x4 *vt, uint32_t ln, int c, int d) {
+        const uint32_t r = 4u * (ln >> 5) + ((ln >> 2) & 3u), piece = 2u * ((ln >> 4) & 1u) + ((ln >> 1) & 1u);
+        // (one step from the array: further ones, and the compiler loses track
+        // of which it is)
+        const uint32_t at = (uint32_t)(c * 32 * D) + r * (2u * D) + (ln & 1u) * 8u + value_piece<D>(r, 4 * d + piece) * 16u;
+        const u32x2 lo = read_turned(reinterpret_cast<const char *>(vt) + at),
+                    hi = read_turned(reinterpret_cast<const char *>(vt) + (at + 16u * D));
+        return (u32x4){lo.x, lo.y, hi.x, hi.y};
+      };
+      // Outputs of a tile; kept(w): w, or what is left of it.
+      auto outputs = [&](const f32x16 (&s)[2], const u32x4 *vt, uint32_t ln, auto kept) {
+        const float off = m == -INFINITY ? 0.0f : kLift<T> - m * a.scale;
+        u32x4 p[2], w[DT];
+        auto pair = [&](int c, int e) {   // weights of keys 16 c + 2 e, 2 e + 1 (in the products' order)
+          const float x = exp2_fast(__builtin_fmaf(s[c / 2][c % 2 * 8 + 2 * e], a.scale, off));
+          const float y = exp2_fast(__builtin_fmaf(s[c / 2][c % 2 * 8 + 2 * e + 1], a.scale, off));
+          p[c % 2][e] = Elem<T>::pack2(x, y);
+          l = Elem<T>::add2(p[c % 2][e], l);
+        };
+#pragma unroll
+        for (int d = 0; d < DT; ++d) w[d] = value(vt, ln, 0, d);
+        in_order();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pair(0, e);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            o[d] = Elem<T>::mfma32(kept(w[d]), p[c % 2], o[d]);
+            if (c < 3) {
+              w[d] = value(vt, ln, c + 1, d);
+#pragma unroll
+              for (int e = 4 * d / DT; e < 4 * (d + 1) / DT; ++e) pair(c + 1, e);
+            }
+            in_order();
+          }
+      };
 
-    auto whole = [&](uint32_t t, const u32x4 *kt, const u32x4 *vt, u32x4 *next_k, u32x4 *next_v) {
-      wait_lds_copy();
-      __syncthreads();   // tile t is there; the other buffer has been read
-      // the next tile's copies between the products: one after another they
-      // keep the wavefront from anything else
-      const __amdgpu_buffer_rsrc_t rk = rows_at(kb, a.k_t, t + 1u), rv = rows_at(vb, a.v_t, t + 1u);
-      f32x16 s[2];
-      scores(s, kt, lane, [&](int i) {
-        if (i % 2) return;
-        if (i / 2 < N) copy(rk, k_off, next_k, i / 2);
-        else if (i / 2 < 2 * N) copy(rv, v_off, next_v, i / 2 - N);
-      });
-      raise_to(s);
-      outputs(s, vt, lane, [](u32x4 w) { return w; });
-    };
-    bool left_out = false;   // infinities or NaN among the values of a tile seen in part
-    auto part = [&](uint32_t t, const u32x4 *kt, const u32x4 *vt, u32x4 *next_k, u32x4 *next_v) {
-      wait_lds_copy();
-      uint32_t any = 0;
+      auto whole = [&](uint32_t t, const u32x4 *kt, const u32x4 *vt, u32x4 *next_k, u32x4 *next_v) {
+        wait_lds_copy();
+        __syncthreads();   // tile t is there; the other buffer has been read
+        // the next tile's copies between the products: one after another they
+        // keep the wavefront from anything else
+        const __amdgpu_buffer_rsrc_t rk = rows_at(kb, a.k_t, t + 1u), rv = rows_at(vb, a.v_t, t + 1u);
+        f32x16 s[2];
+        scores(s, kt, lane, [&](int i) {
+          if (i % 2) return;
+          if (i / 2 < N) copy(rk, k_off, next_k, i / 2);
+          else if (i / 2 < 2 * N) copy(rv, v_off, next_v, i / 2 - N);
+        });
+        raise_to(s);
+        outputs(s, vt, lane, [](u32x4 w) { return w; });
+      };
+      bool left_out = false;   // infinities or NaN among the values of a tile seen in part
+      auto part = [&](uint32_t t, const u32x4 *kt, const u32x4 *vt, u32x4 *next_k, u32x4 *next_v) {
+        wait_lds_copy();
+        uint32_t any = 0;
 #pragma unroll
-      for (uint32_t i = 0; i < (uint32_t)N; ++i) {
-        const u32x4 w = vt[(wave * N + i) * 64u + lane];
-        for (int e = 0; e < 4; ++e) any |= special<T>(w[e]);
-      }
-      if (any) lds_special[t & 1u] = 1u;
-      __syncthreads();
-      if (t + 1u < tiles) copy_all(t + 1u, next_k, next_v);
-      // (a mark stays for the tiles after: they take the longer way for nothing)
-      const bool special_here = lds_special[t & 1u] != 0u;
-      if (t >= mine) return;
-      const uint32_t ln = fresh(lane);
-      f32x16 s[2];
-      scores(s, kt, ln, [](int) {});
-      const int seen = (int)min(max((int64_t)(q0 + (ln & 31u)) + shift + 1 - (int64_t)t * kTile, (int64_t)0), (int64_t)kTile) - 4 * (int)(ln >> 5);
+        for (uint32_t i = 0; i < (uint32_t)N; ++i) {
+          const u32x4 w = vt[(wave * N + i) * 64u + lane];
+          for (int e = 0; e < 4; ++e) any |= special<T>(w[e]);
+        }
+        if (any) lds_special[t & 1u] = 1u;
+        __syncthreads();
+        if (t + 1u < tiles) copy_all(t + 1u, next_k, next_v);
+        // (a mark stays for the tiles after: they take the longer way for nothing)
+        const bool special_here = lds_special[t & 1u] != 0u;
+        if (t >= mine) return;
+        const uint32_t ln = fresh(lane);
+        f32x16 s[2];
+        scores(s, kt, ln, [](int) {});
+        const int64_t keys = (int64_t)(q0 + (ln & 31u)) + shift + 1 - (int64_t)t * kTile;   // of this tile, seen by the query
+        const int seen = (int)min(max(keys, (int64_t)0), (int64_t)kTile) - 4 * (int)(ln >> 5);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        for (int r = 0; r < 16; ++r) s[i][r] = 32 * i + 8 * (r / 4) + r % 4 < seen ? s[i][r] : -INFINITY;
-      raise_to(s);
-      if (special_here) {
-        left_out = true;
-        outputs(s, vt, ln, [](u32x4 w) { return without_special<T>(w); });
-      } else {
-        outputs(s, vt, ln, [](u32x4 w) { return w; });
+        for (int i = 0; i < 2; ++i)
+          for (int r = 0; r < 16; ++r) s[i][r] = 32 * i + 8 * (r / 4) + r % 4 < seen ? s[i][r] : -INFINITY;
+        raise_to(s);
+        if (special_here) {
+          left_out = true;
+          outputs(s, vt, ln, [](u32x4 w) { return without_special<T>(w); });
+        } else {
+          outputs(s, vt, ln, [](u32x4 w) { return w; });
+        }
+      };
+      uint32_t t = 0;
+      for (; t < full; t += 2u) {
+        whole(t, lds_k0, lds_v0, lds_k1, lds_v1);
+        whole(t + 1u, lds_k1, lds_v1, lds_k0, lds_v0);
       }
-    };
-    uint32_t t = 0;
-    for (; t < full; t += 2u) {
-      whole(t, lds_k0, lds_v0, lds_k1, lds_v1);
-      whole(t + 1u, lds_k1, lds_v1, lds_k0, lds_v0);
-    }
-    for (; t < tiles; ++t) {
-      const bool odd = t & 1u;
-      part(t, odd ? lds_k1 : lds_k0, odd ? lds_v1 : lds_v0, odd ? lds_k0 : lds_k1, odd ? lds_v0 : lds_v1);
-    }
+      for (; t < tiles; ++t) {
+        const bool odd = t & 1u;
+        part(t, odd ? lds_k1 : lds_k0, odd ? lds_v1 : lds_v0, odd ? lds_k0 : lds_k1, odd ? lds_v0 : lds_v1);
+      }
 
-    const float sum = add32(l);
-    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;   // NaN stays
+      const float sum = add32(l);
+      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;   // NaN stays
 #pragma unroll
-    for (int d = 0; d < DT; ++d) o[d] *= inv;
-    if (left_out)
-      for (int64_t j = (int64_t)full * kTile; j < my_end; ++j) {
-        const char *vp = vb + j * a.v_t + half * 8u;
+      for (int d = 0; d < DT; ++d) o[d] *= inv;
+      if (left_out)
+        for (int64_t j = (int64_t)full * kTile; j < my_end; ++j) {
+          const char *vp = vb + j * a.v_t + half * 8u;
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4) {
+              const u32x2 w = *reinterpret_cast<const u32x2 *>(vp + (32 * d + 2 * r) * 2);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t x = e & 1 ? w[e / 2] >> 16 : w[e / 2];
+                const bool add = j <= (int64_t)qi + shift && (x & Elem<T>::kInf) == Elem<T>::kInf;
+                o[d][r + e] += add ? Elem<T>::lo(x) : 0.0f;
+              }
+            }
+        }
+      // rows out by way of the place of the tile before the last, which every
+      // wavefront has left, so that a store writes whole rows
+      {
+        const uint32_t ln = fresh(lane);
+        u32x4 *at = tiles & 1u ? quarter(lds_k1, lds_v1) : quarter(lds_k0, lds_v0);
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-          for (int r = 0; r < 16; r += 4) {
-            const u32x2 w = *reinterpret_cast<const u32x2 *>(vp + (32 * d + 2 * r) * 2);
+          for (int r = 0; r < 16; r += 4)
+            reinterpret_cast<u32x2 *>(at)[2u * ((ln & 31u) * kPieces + key_piece<D>(ln & 31u, 4 * d + r / 4)) + (ln >> 5)] =
+                (u32x2){Elem<T>::pack2(o[d][r], o[d][r + 1]), Elem<T>::pack2(o[d][r + 2], o[d][r + 3])};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t x = e & 1 ? w[e / 2] >> 16 : w[e / 2];
-              const bool add = j <= (int64_t)qi + shift && (x & Elem<T>::kInf) == Elem<T>::kInf;
-              o[d][r + e] += add ? Elem<T>::lo(x) : 0.0f;
-            }
-          }
-      }
-    // rows out by way of the place of the tile before the last, which every
-    // wavefront has left, so that a store writes whole rows
-    {
-      const uint32_t ln = fresh(lane);
-      u32x4 *at = tiles & 1u ? quarter(lds_k1, lds_v1) : quarter(lds_k0, lds_v0);
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; r += 4)
-          reinterpret_cast<u32x2 *>(at)[2u * ((ln & 31u) * kPieces + key_piece<D>(ln & 31u, 4 * d + r / 4)) + (ln >> 5)] =
-              (u32x2){Elem<T>::pack2(o[d][r], o[d][r + 1]), Elem<T>::pack2(o[d][r + 2], o[d][r + 3])};
-#pragma unroll
-      for (uint32_t s = 0; s < (uint32_t)KS; ++s) {
-        const uint32_t i = s * 64u + ln, row = i / kPieces, c = i % kPieces;
-        const u32x4 w = at[row * kPieces + key_piece<D>(row, c)];
-        if (q0 + row < count_q)
-          *reinterpret_cast<u32x4 *>(a.out + (int64_t)(begin_q + q0 + row) * a.o_t + head * a.o_h + c * 16u) = w;
+        for (uint32_t s = 0; s < (uint32_t)KS; ++s) {
+          const uint32_t i = s * 64u + ln, row = i / kPieces, c = i % kPieces;
+          const u32x4 w = at[row * kPieces + key_piece<D>(row, c)];
+          if (q0 + row < count_q)
+            *reinterpret_cast<u32x4 *>(a.out + (int64_t)(begin_q + q0 + row) * a.o_t + head * a.o_h + c * 16u) = w;
+        }
       }
     }
-  }
 }
 
 template <entro_dtype T, int D>
@@ -407,15 +410,14 @@ static entro_status launch_prompt(PromptArg &a, hipStream_t s) {
   const bool small = a.total_q <= 64ull * a.n_seq;
   a.heads = !small ? 1u : group % 4u == 0u ? 4u : group % 2u == 0u ? 2u : 1u;
   const uint32_t rows = 32u * kWaves4 / a.heads;
-  uint64_t grid = std::min<uint64_t>(a.total_q, (uint64_t)a.total_q / rows + a.n_seq);
-  grid = std::min<uint64_t>(grid * (a.n_heads / a.heads), 1u << 30);
-  grid = std::max<uint64_t>(1, cap_grid(grid));
+  const uint32_t slots = a.n_heads / a.heads;
+  const uint64_t items = std::min<uint64_t>(a.total_q, (uint64_t)a.total_q / rows + a.n_seq);
   // Where all workgroups run at once, the 256 first get a CU each and the rest
   // follow in the same order: the first ones' order is turned around, so that
   // the CUs with the least of them to do get the most of the rest.
-  a.turned = grid <= 512u ? 256u / (a.n_heads / a.heads) : 0u;
+  a.turned = items * slots <= 512u ? 256u / slots : 0u;
   (void)hipGetLastError();
-  hipLaunchKernelGGL((attn_prompt_kernel<T, D>), dim3((uint32_t)grid), dim3(256), 0, s, a);
+  hipLaunchKernelGGL((attn_prompt_kernel<T, D>), grid2(slots, items), dim3(256), 0, s, a);
   return hipGetLastError() == hipSuccess ? ENTRO_OK : ENTRO_E_HIP;
 }
 

@@ -49,8 +49,8 @@ __device__ __forceinline__ void kv_check(const KvArg &a, uint32_t page) {
     if (!kv_span(a, b, page).ok) atomicOr(a.status + b, ENTRO_F_LENGTH);
 }
 
-// What a workgroup does: the page of item `id % items` (the sequences' pages
-// one after another) for one head, keys and values.  Neighbouring workgroups
+// What a workgroup does: one page (the sequences' pages that take part are
+// numbered one after another) for one head, keys and values.  Neighbouring workgroups
 // take the pages of one head: with the heads of one page side by side, reading
 // 58371 tokens back took 98 us instead of 74.
 struct KvItem {
@@ -60,10 +60,9 @@ struct KvItem {
   int64_t first;       // packed row of page row 0
   uint64_t at;         // place of the page's and head's scale
 };
-__device__ __forceinline__ KvItem kv_item(const KvArg &a, uint32_t page, uint64_t id, uint32_t lane) {
+__device__ __forceinline__ KvItem kv_item(const KvArg &a, uint32_t page, uint32_t item, uint32_t head, uint32_t lane) {
   KvItem it{};
-  const uint32_t head = (uint32_t)(id / a.items);
-  const Found f = find_item((uint32_t)(id % a.items), a.n_seq, lane,
+  const Found f = find_item(item, a.n_seq, lane,
                             [&](uint32_t b) { return kv_pages(kv_span(a, b, page), page); });
   if (f.seq == a.n_seq) return it;
   const KvSpan s = kv_span(a, f.seq, page);
@@ -155,118 +154,118 @@ __device__ __forceinline__ Grow grow(float before, float top) {
 // value.
 // ---------------------------------------------------------------------------
 template <entro_dtype T, int D>
-__global__ __launch_bounds__(512) void kv_store_kernel(KvArg a, uint32_t page) {
+__global__ __launch_bounds__(512, 5) void kv_store_kernel(KvArg a, uint32_t page) {
   constexpr uint32_t C = D / 8;           // column groups of eight
   __shared__ uint32_t red[8];
   uint8_t *vt = reinterpret_cast<uint8_t *>(dyn_lds);   // [D][page + 4]
   const uint32_t tid = threadIdx.x, lane = tid & 63u;
   const uint32_t vs = page + 4u, c = tid % C, quad = tid / C;
-  if (blockIdx.x == 0u) kv_check(a, page);
-  for (uint64_t id = blockIdx.x; id < a.items * a.n_kv; id += gridDim.x) {
-    const KvItem it = kv_item(a, page, id, lane);
-    if (!it.any) continue;
-    const bool mine = quad * 4u < page;
-    u32x4 kx[4], vx[4];
-    auto rows = [&](u32x4 (&x)[4], const KvSide &s) {
-      const char *from = s.x + (it.first + quad * 4u) * s.stride_t + it.head * s.stride_h + c * 16u;
+  if (blockIdx.x == 0u && blockIdx.y == 0u) kv_check(a, page);
+  for (uint32_t head = blockIdx.y; head < a.n_kv; head += gridDim.y)
+    for (uint64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
+      const KvItem it = kv_item(a, page, (uint32_t)item, head, lane);
+      if (!it.any) continue;
+      const bool mine = quad * 4u < page;
+      u32x4 kx[4], vx[4];
+      // (a place that is no new row gets the nearest one: it changes no maximum,
+      // and what is made of it is not written; all loads go out together)
+      auto rows = [&](u32x4 (&x)[4], const KvSide &s) {
+        const char *from = s.x + it.first * s.stride_t + it.head * s.stride_h + c * 16u;
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
-        const uint32_t r = quad * 4u + i;
-        x[i] = (u32x4){0u, 0u, 0u, 0u};
-        if (mine && r >= it.r0 && r < it.r1) x[i] = *reinterpret_cast<const u32x4 *>(from + i * s.stride_t);
-      }
-    };
-    rows(kx, a.side[0]);
-    rows(vx, a.side[1]);
-    // the new scale, written, and the codes of the thread's rows in place of them
-    auto quantize = [&](u32x4 (&x)[4], u32x2 (&q)[4], float *scale) {
-      const float before = it.r0 ? *scale : 0.0f;   // rows before r0 are held
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        for (int e = 0; e < 4; ++e) top = top_of<T, false>(x[i][e], top);
-      top = wg_max(top, red);
-      if (top >= Elem<T>::kInf) {   // the same in every thread
-        top = 0;
+        for (uint32_t i = 0; i < 4; ++i)
+          x[i] = *reinterpret_cast<const u32x4 *>(from + min(max(quad * 4u + i, it.r0), it.r1 - 1u) * s.stride_t);
+      };
+      rows(kx, a.side[0]);
+      rows(vx, a.side[1]);
+      // the new scale, written, and the codes of the thread's rows in place of them
+      auto quantize = [&](u32x4 (&x)[4], u32x2 (&q)[4], float *scale) {
+        const float before = it.r0 ? *scale : 0.0f;   // rows before r0 are held
+        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          for (int e = 0; e < 4; ++e) top = top_of<T, true>(x[i][e], top);
+          for (int e = 0; e < 4; ++e) top = top_of<T, false>(x[i][e], top);
         top = wg_max(top, red);
-      }
-      const Grow g = grow(before, Elem<T>::lo(top));
-      if (tid == 0u) *scale = g.scale;
+        if (top >= Elem<T>::kInf) {   // the same in every thread
+          top = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t e[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          e[2 * j] = code_of(Elem<T>::lo(x[i][j]) * g.fresh);
-          e[2 * j + 1] = code_of(Elem<T>::hi(x[i][j]) * g.fresh);
+          for (int i = 0; i < 4; ++i)
+            for (int e = 0; e < 4; ++e) top = top_of<T, true>(x[i][e], top);
+          top = wg_max(top, red);
         }
-        q[i] = (u32x2){pack4(e[0], e[1], e[2], e[3]), pack4(e[4], e[5], e[6], e[7])};
-        __builtin_amdgcn_sched_barrier(0);   // one row after another: registers are occupancy here
-      }
-      return g.again;
-    };
-    u32x2 q[4];
-    {
-      int8_t *codes = a.side[0].codes + it.at * (page * D);
-      const float again = quantize(kx, q, a.side[0].scales + it.at);
+        const Grow g = grow(before, Elem<T>::lo(top));
+        if (tid == 0u) *scale = g.scale;
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
-        const uint32_t r = quad * 4u + i;
-        if (mine && r >= it.r0 && r < it.r1) *reinterpret_cast<u32x2 *>(codes + r * D + c * 8u) = q[i];
-      }
-      if (again != 1.0f)   // the range grew
-#pragma unroll 1
-        for (uint32_t i = tid; i < it.r0 * (D / 4u); i += blockDim.x) {
-          uint32_t *w = reinterpret_cast<uint32_t *>(codes) + i;
-          *w = again4(*w, again);
-        }
-    }
-    {
-      int8_t *codes = a.side[1].codes + it.at * (page * D);
-      const float again = quantize(vx, q, a.side[1].scales + it.at);
-      if (mine)
+        for (int i = 0; i < 4; ++i) {
+          uint32_t e[8];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const u32x4 w = turn4(q[0][h], q[1][h], q[2][h], q[3][h]);
-          uint8_t *to = vt + (c * 8u + h * 4u) * vs + quad * 4u;
-#pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) *reinterpret_cast<uint32_t *>(to + e * vs) = w[e];
-        }
-      __syncthreads();
-      const uint32_t pieces = page / 16u;
-#pragma unroll 1
-      for (uint32_t p = tid; p < D * pieces; p += blockDim.x) {
-        const uint32_t t0 = p % pieces * 16u;
-        const uint8_t *from = vt + p / pieces * vs + t0;
-        u32x4 w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t *>(from + 4 * e);
-        u32x4 *to = reinterpret_cast<u32x4 *>(codes + p * 16u);   // of dimension p / pieces
-        if (t0 < it.r0 || t0 + 16u > it.r1) {
-          if (t0 >= it.r1 || (t0 + 16u <= it.r0 && again == 1.0f)) continue;
-          const u32x4 was = *to;
-#pragma unroll
-          for (uint32_t e = 0; e < 4; ++e) {
-            const uint32_t re = again == 1.0f ? was[e] : again4(was[e], again);
-            uint32_t out = 0;
-#pragma unroll
-            for (uint32_t j = 0; j < 4; ++j) {
-              const uint32_t r = t0 + 4u * e + j;
-              const uint32_t src = r < it.r0 ? re : r < it.r1 ? w[e] : was[e];
-              out |= src & (0xFFu << (8u * j));
-            }
-            w[e] = out;
-            __builtin_amdgcn_sched_barrier(0);
+          for (int j = 0; j < 4; ++j) {
+            e[2 * j] = code_of(Elem<T>::lo(x[i][j]) * g.fresh);
+            e[2 * j + 1] = code_of(Elem<T>::hi(x[i][j]) * g.fresh);
           }
+          q[i] = (u32x2){pack4(e[0], e[1], e[2], e[3]), pack4(e[4], e[5], e[6], e[7])};
+          __builtin_amdgcn_sched_barrier(0);   // one row after another: registers are occupancy here
         }
-        *to = w;
+        return g.again;
+      };
+      u32x2 q[4];
+      {
+        int8_t *codes = a.side[0].codes + it.at * (page * D);
+        const float again = quantize(kx, q, a.side[0].scales + it.at);
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t r = quad * 4u + i;
+          if (mine && r >= it.r0 && r < it.r1) *reinterpret_cast<u32x2 *>(codes + r * D + c * 8u) = q[i];
+        }
+        if (again != 1.0f)   // the range grew
+#pragma unroll 1
+          for (uint32_t i = tid; i < it.r0 * (D / 4u); i += blockDim.x) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(codes) + i;
+            *w = again4(*w, again);
+          }
       }
+      {
+        int8_t *codes = a.side[1].codes + it.at * (page * D);
+        const float again = quantize(vx, q, a.side[1].scales + it.at);
+        if (mine)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const u32x4 w = turn4(q[0][h], q[1][h], q[2][h], q[3][h]);
+            uint8_t *to = vt + (c * 8u + h * 4u) * vs + quad * 4u;
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) *reinterpret_cast<uint32_t *>(to + e * vs) = w[e];
+          }
+        __syncthreads();
+        const uint32_t pieces = page / 16u;
+#pragma unroll 1
+        for (uint32_t p = tid; p < D * pieces; p += blockDim.x) {
+          const uint32_t t0 = p % pieces * 16u;
+          const uint8_t *from = vt + p / pieces * vs + t0;
+          u32x4 w;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = *reinterpret_cast<const uint32_t *>(from + 4 * e);
+          u32x4 *to = reinterpret_cast<u32x4 *>(codes + p * 16u);   // of dimension p / pieces
+          if (t0 < it.r0 || t0 + 16u > it.r1) {
+            if (t0 >= it.r1 || (t0 + 16u <= it.r0 && again == 1.0f)) continue;
+            const u32x4 was = *to;
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e) {
+              const uint32_t re = again == 1.0f ? was[e] : again4(was[e], again);
+              uint32_t out = 0;
+#pragma unroll
+              for (uint32_t j = 0; j < 4; ++j) {
+                const uint32_t r = t0 + 4u * e + j;
+                const uint32_t src = r < it.r0 ? re : r < it.r1 ? w[e] : was[e];
+                out |= src & (0xFFu << (8u * j));
+              }
+              w[e] = out;
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+          *to = w;
+        }
+      }
+      __syncthreads();   // vt and red are written again
     }
-    __syncthreads();   // vt and red are written again
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -286,49 +285,50 @@ __global__ __launch_bounds__(512, 8) void kv_load_kernel(KvArg a, uint32_t page)
   uint8_t *vt = reinterpret_cast<uint8_t *>(dyn_lds);   // [D][page + 4]
   const uint32_t tid = threadIdx.x, lane = tid & 63u;
   const uint32_t vs = page + 4u, c = tid % C, quad = tid / C;
-  if (blockIdx.x == 0u) kv_check(a, page);
-  for (uint64_t id = blockIdx.x; id < a.items * a.n_kv; id += gridDim.x) {
-    const KvItem it = kv_item(a, page, id, lane);
-    if (!it.any) continue;
-    const bool mine = quad * 4u < page;
-    const uint32_t pieces = page / 16u;
-    const int8_t *kc = a.side[0].codes + it.at * (page * D), *vc = a.side[1].codes + it.at * (page * D);
-    const float k_scale = a.side[0].scales[it.at], v_scale = a.side[1].scales[it.at];
-    u32x2 w[4];
-    if (mine)
+  if (blockIdx.x == 0u && blockIdx.y == 0u) kv_check(a, page);
+  for (uint32_t head = blockIdx.y; head < a.n_kv; head += gridDim.y)
+    for (uint64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
+      const KvItem it = kv_item(a, page, (uint32_t)item, head, lane);
+      if (!it.any) continue;
+      const bool mine = quad * 4u < page;
+      const uint32_t pieces = page / 16u;
+      const int8_t *kc = a.side[0].codes + it.at * (page * D), *vc = a.side[1].codes + it.at * (page * D);
+      const float k_scale = a.side[0].scales[it.at], v_scale = a.side[1].scales[it.at];
+      u32x2 w[4];
+      if (mine)
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const u32x2 *>(kc + (quad * 4u + i) * D + c * 8u);
-    for (uint32_t p = tid; p < D * pieces; p += blockDim.x) {
-      const u32x4 x = *reinterpret_cast<const u32x4 *>(vc + p * 16u);   // of dimension p / pieces
-      uint8_t *to = vt + p / pieces * vs + p % pieces * 16u;
+        for (uint32_t i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const u32x2 *>(kc + (quad * 4u + i) * D + c * 8u);
+      for (uint32_t p = tid; p < D * pieces; p += blockDim.x) {
+        const u32x4 x = *reinterpret_cast<const u32x4 *>(vc + p * 16u);   // of dimension p / pieces
+        uint8_t *to = vt + p / pieces * vs + p % pieces * 16u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t *>(to + 4 * e) = x[e];
+        for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t *>(to + 4 * e) = x[e];
+      }
+      auto put = [&](const KvSide &s, float scale) {
+        char *to = s.x + (it.first + quad * 4u) * s.stride_t + it.head * s.stride_h + c * 16u;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+          const uint32_t r = quad * 4u + i;
+          if (mine && r >= it.r0 && r < it.r1)
+            *reinterpret_cast<u32x4 *>(to + i * s.stride_t) = values8<T>(w[i].x, w[i].y, scale);
+        }
+      };
+      put(a.side[0], k_scale);
+      __syncthreads();
+      if (mine)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t *from = vt + (c * 8u + h * 4u) * vs + quad * 4u;
+          uint32_t b[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const uint32_t *>(from + e * vs);
+          const u32x4 r = turn4(b[0], b[1], b[2], b[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e][h] = r[e];
+        }
+      put(a.side[1], v_scale);
+      __syncthreads();   // vt is written again
     }
-    auto put = [&](const KvSide &s, float scale) {
-      char *to = s.x + (it.first + quad * 4u) * s.stride_t + it.head * s.stride_h + c * 16u;
-#pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) {
-        const uint32_t r = quad * 4u + i;
-        if (mine && r >= it.r0 && r < it.r1)
-          *reinterpret_cast<u32x4 *>(to + i * s.stride_t) = values8<T>(w[i].x, w[i].y, scale);
-      }
-    };
-    put(a.side[0], k_scale);
-    __syncthreads();
-    if (mine)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint8_t *from = vt + (c * 8u + h * 4u) * vs + quad * 4u;
-        uint32_t b[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = *reinterpret_cast<const uint32_t *>(from + e * vs);
-        const u32x4 r = turn4(b[0], b[1], b[2], b[3]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e][h] = r[e];
-      }
-    put(a.side[1], v_scale);
-    __syncthreads();   // vt is written again
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -341,11 +341,10 @@ static entro_status launch_kv(KvArg &a, uint32_t page, hipStream_t s) {
   // of a sequence are not full
   const uint64_t items = std::min<uint64_t>(a.total, (uint64_t)a.total / page + 2ull * a.n_seq);
   a.items = items;
-  const uint64_t grid = std::max<uint64_t>(1, cap_grid(std::min<uint64_t>(items * a.n_kv, 1u << 30)));
   const uint32_t threads = (D / 8u * (page / 4u) + 63u) & ~63u;
   const size_t lds = (size_t)D * (page + 4u);
   (void)hipGetLastError();
-  hipLaunchKernelGGL((STORE ? kv_store_kernel<T, D> : kv_load_kernel<T, D>), dim3((uint32_t)grid), dim3(threads), lds, s,
+  hipLaunchKernelGGL((STORE ? kv_store_kernel<T, D> : kv_load_kernel<T, D>), grid2(items, a.n_kv), dim3(threads), lds, s,
                      a, page);
   return hipGetLastError() == hipSuccess ? ENTRO_OK : ENTRO_E_HIP;
 }

@@ -189,6 +189,7 @@ def test_packed_arguments_have_the_structures_layout():
         (attn._STORE, attn.StoreArgs, (1, 2, 3, 4, 5, 6, 7, 8, 9, 1)),
         (attn._CACHE, attn.CacheArgs, (1, 2, 3, 4, 5, 6, 7, 8, 1, 0.5, 9, 10)),
         (attn._TABLE, attn.Table, (1, 2, 3, 4, 0)),
+        (attn._PAGES, attn.Cache, (1, 2, 3, 4, 5, 6, 7, 8)),
     ):
         assert packed.size == ctypes.sizeof(structure)
         got, want = structure.from_buffer_copy(packed.pack(*values)), []
