@@ -359,13 +359,15 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
 }
 
 // Joins the pieces of a split sequence: one workgroup per sequence and query
-// head.  Four groups of 64 threads (two dimensions each) take every fourth
-// piece, eight at a time, then the groups are joined; the order is the same in
-// every call.
-template <entro_dtype T, int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(CacheArg a) {
-  __shared__ float red_o[4][D];
-  __shared__ f32x2 red_ml[4];
+// head.  G groups of 64 threads (two dimensions each) take every G-th piece,
+// four at a time, then the groups are joined; the order is the same in every
+// call.  The pieces' reads wait for one another only from batch to batch: with
+// few workgroups (one long sequence: 64 pieces) 16 groups read them at once,
+// with many (few pieces each) four leave room for more workgroups.
+template <entro_dtype T, int D, int G>
+__global__ __launch_bounds__(64 * G) void attn_join_kernel(CacheArg a) {
+  __shared__ float red_o[G][D];
+  __shared__ f32x2 red_ml[G];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, group = tid >> 6;
   const Shares sh = shares_of(a, lane);
   for (uint32_t head = blockIdx.y; head < a.n_heads; head += gridDim.y)
@@ -380,25 +382,25 @@ __global__ __launch_bounds__(256) void attn_join_kernel(CacheArg a) {
       const float *po = a.part_o + at * D;
       const uint32_t d = min(lane * 2u, D - 2u);
       float m = -INFINITY, x = 0.0f, y = 0.0f, l = 0.0f;
-      for (uint32_t i0 = group; i0 < n; i0 += 32u) {
-        f32x2 v[8], p[8];
+      for (uint32_t i0 = group; i0 < n; i0 += 4u * G) {
+        f32x2 v[4], p[4];
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) {
-          const uint64_t i = min(i0 + 4u * j, n - 1u);
+        for (uint32_t j = 0; j < 4; ++j) {
+          const uint64_t i = min(i0 + (uint32_t)G * j, n - 1u);
           v[j] = ml[i * a.n_heads];
           p[j] = *reinterpret_cast<const f32x2 *>(po + i * a.n_heads * D + d);
         }
         float mn = m;
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) mn = fmaxf(mn, v[j].x);
+        for (uint32_t j = 0; j < 4; ++j) mn = fmaxf(mn, v[j].x);
         float k = join_factor(m, mn);
         x *= k;
         y *= k;
         l *= k;
         m = mn;
 #pragma unroll
-        for (uint32_t j = 0; j < 8; ++j) {
-          if (i0 + 4u * j >= n) break;
+        for (uint32_t j = 0; j < 4; ++j) {
+          if (i0 + (uint32_t)G * j >= n) break;
           k = join_factor(v[j].x, m);
           x += k * p[j].x;
           y += k * p[j].y;
@@ -411,8 +413,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(CacheArg a) {
       if (group == 0u && lane * 2u < D) {
         m = -INFINITY;
         x = y = l = 0.0f;
-        for (int g = 0; g < 4; ++g) m = fmaxf(m, red_ml[g].x);
-        for (int g = 0; g < 4; ++g) {
+        for (int g = 0; g < G; ++g) m = fmaxf(m, red_ml[g].x);
+        for (int g = 0; g < G; ++g) {
           const float k = join_factor(red_ml[g].x, m);
           x += k * red_o[g][d];
           y += k * red_o[g][d + 1u];
@@ -443,7 +445,10 @@ static entro_status launch_cache(CacheArg &a, hipStream_t s) {
   hipLaunchKernelGGL((attn_cache_kernel<T, D>), grid2(split ? a.shares : a.n_seq, a.n_kv * a.parts), dim3(256), 0, s, a);
   if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
   if (split) {
-    hipLaunchKernelGGL((attn_join_kernel<T, D>), grid2(a.n_seq, a.n_heads), dim3(256), 0, s, a);
+    if ((uint64_t)a.n_seq * a.n_heads <= 256u)
+      hipLaunchKernelGGL((attn_join_kernel<T, D, 16>), grid2(a.n_seq, a.n_heads), dim3(1024), 0, s, a);
+    else
+      hipLaunchKernelGGL((attn_join_kernel<T, D, 4>), grid2(a.n_seq, a.n_heads), dim3(256), 0, s, a);
     if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
   }
   return ENTRO_OK;
