@@ -11,7 +11,12 @@ constexpr uint32_t kTile = 64;          // tokens a wavefront takes at a time
 constexpr uint32_t kCacheWaves = 4;     // wavefronts per workgroup, interleaved over its tiles
 constexpr uint32_t kHeadsPerWg = 16;    // query heads of one key/value head (columns of the matrix products)
 constexpr uint32_t kShareTiles = 4;     // least tiles of a workgroup's share
-constexpr uint32_t kShares = 512;       // shares of a call, all heads together: two workgroups on each of 256 CUs
+
+// Shares of a call, all heads together: the workgroups that 256 CUs hold at
+// once by the kernel's registers, two on each at head dimension 128 and three
+// below.  32 ragged sequences (32 heads, f16), two against three: up to 16384
+// tokens at 64 119 and 117 us (four: 132), up to 8192 at 96 113 and 111.
+constexpr uint32_t shares_at(uint32_t head_dim) { return head_dim == 128u ? 512u : 768u; }
 
 struct CacheArg {
   const int8_t *k_codes, *v_codes;
@@ -432,7 +437,9 @@ __global__ __launch_bounds__(64 * G) void attn_join_kernel(CacheArg a) {
 // ---------------------------------------------------------------------------
 
 // Shares of one key/value head's tokens.
-static uint32_t cache_shares(uint32_t n_kv, uint32_t parts) { return std::max(1u, kShares / (n_kv * parts)); }
+static uint32_t cache_shares(uint32_t n_kv, uint32_t parts, uint32_t head_dim) {
+  return std::max(1u, shares_at(head_dim) / (n_kv * parts));
+}
 
 template <entro_dtype T, int D>
 static entro_status launch_cache(CacheArg &a, hipStream_t s) {
@@ -461,7 +468,7 @@ using namespace entro;
 extern "C" uint64_t entro_attn_cache_work_bytes(uint32_t n_seq, uint32_t n_heads, uint32_t n_kv_heads, uint32_t head_dim) {
   if (n_seq == 0 || check_heads(n_heads, n_kv_heads, head_dim, ENTRO_BF16) != ENTRO_OK) return 0;
   const uint32_t parts = (n_heads / n_kv_heads + kHeadsPerWg - 1u) / kHeadsPerWg;
-  return ((uint64_t)n_seq + cache_shares(n_kv_heads, parts)) * n_heads * (head_dim + 2ull) * 4ull;
+  return ((uint64_t)n_seq + cache_shares(n_kv_heads, parts, head_dim)) * n_heads * (head_dim + 2ull) * 4ull;
 }
 
 extern "C" entro_status entro_attn_cache(const entro_kv_cache *c, const entro_kv_table *t, const entro_attn_cache_args *a,
@@ -501,7 +508,7 @@ extern "C" entro_status entro_attn_cache(const entro_kv_cache *c, const entro_kv
   k.n_heads = a->n_heads;
   k.group = a->n_heads / c->n_kv_heads;
   k.parts = (k.group + kHeadsPerWg - 1u) / kHeadsPerWg;
-  k.shares = cache_shares(k.n_kv, k.parts);
+  k.shares = cache_shares(k.n_kv, k.parts, c->head_dim);
   k.scale = a->scale * kLog2e;
   k.part_o = static_cast<float *>(a->d_work);
   k.status = d_status;
