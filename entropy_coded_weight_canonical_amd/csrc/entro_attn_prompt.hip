@@ -142,8 +142,11 @@ attn_prompt_kernel(PromptArg a) {
     v_off[s] = r * (uint32_t)a.v_t + value_piece<D>(r, c) * 16u;
   }
 
+  Span lq{}, lk{};                 // of the sequence this lane looked at last
   auto items = [&](uint32_t b) {   // workgroups of sequence b for a key/value head
-    return span_of(a.cu_k, b, a.total_k).ok ? (span_of(a.cu_q, b, a.total_q).count + rows - 1u) / rows : 0u;
+    lq = span_of(a.cu_q, b, a.total_q);
+    lk = span_of(a.cu_k, b, a.total_k);
+    return lk.ok ? (lq.count + rows - 1u) / rows : 0u;
   };
   const uint32_t turned = a.turned ? min(a.turned, count_items(a.n_seq, lane, items)) : 0u;
   for (uint32_t slot = blockIdx.x; slot < a.n_heads / a.heads; slot += gridDim.x)
@@ -154,8 +157,9 @@ attn_prompt_kernel(PromptArg a) {
       const uint32_t item = at < turned ? turned - 1u - at : at;
       const Found f = find_item(item, a.n_seq, lane, items);
       if (f.seq == a.n_seq) break;
-      const Span sq = span_of(a.cu_q, f.seq, a.total_q), sk = span_of(a.cu_k, f.seq, a.total_k);
-      const uint32_t count_q = rfl(sq.count), count_k = rfl(sk.count), begin_q = rfl(sq.begin), begin_k = rfl(sk.begin);
+      const uint32_t in = f.seq % 64u;   // the lane that has the sequence
+      const uint32_t count_q = __builtin_amdgcn_readlane(lq.count, in), count_k = __builtin_amdgcn_readlane(lk.count, in);
+      const uint32_t begin_q = __builtin_amdgcn_readlane(lq.begin, in), begin_k = __builtin_amdgcn_readlane(lk.begin, in);
       // the last queries first: they have the most keys
       const uint32_t wg0 = ((count_q + rows - 1u) / rows - 1u - f.local) * rows;
       const uint32_t q0 = wg0 + wave / a.heads * kQueries, qi = q0 + n;
@@ -208,7 +212,7 @@ attn_prompt_kernel(PromptArg a) {
         const uint32_t n_rows = q0 < count_q ? min(kQueries, count_q - q0) : 0u;
         const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
             const_cast<char *>(a.q + (int64_t)(begin_q + q0) * a.q_t + head * a.q_h), 0,
-            n_rows ? (int)((n_rows - 1u) * (uint32_t)a.q_t + 2u * D) : 0, 0x00020000);
+            (int)rfl(n_rows ? (n_rows - 1u) * (uint32_t)a.q_t + 2u * D : 0u), 0x00020000);
 #pragma unroll
         for (uint32_t s = 0; s < (uint32_t)KS; ++s) {
           const uint32_t i = s * 64u + ln, row = i / kPieces;
@@ -253,10 +257,9 @@ attn_prompt_kernel(PromptArg a) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[i][r]);
-        mx = max32(mx);
-        const bool raise = mx * a.scale > m * a.scale + kLag<T>;
-        if (__any(raise)) {
-          const float mn = raise ? mx : m;
+        if (__any(mx * a.scale > m * a.scale + kLag<T>)) {
+          mx = max32(mx);
+          const float mn = mx * a.scale > m * a.scale + kLag<T> ? mx : m;
           const float k = mn == -INFINITY ? 1.0f : exp2_fast((m - mn) * a.scale);
           m = mn;
           l *= k;
