@@ -62,10 +62,14 @@ struct KvItem {
 };
 __device__ __forceinline__ KvItem kv_item(const KvArg &a, uint32_t page, uint32_t item, uint32_t head, uint32_t lane) {
   KvItem it{};
-  const Found f = find_item(item, a.n_seq, lane,
-                            [&](uint32_t b) { return kv_pages(kv_span(a, b, page), page); });
+  KvSpan own{};   // of the sequence this lane looked at last
+  const Found f = find_item(item, a.n_seq, lane, [&](uint32_t b) {
+    own = kv_span(a, b, page);
+    return kv_pages(own, page);
+  });
   if (f.seq == a.n_seq) return it;
-  const KvSpan s = kv_span(a, f.seq, page);
+  const auto there = [&](uint32_t v) { return (uint32_t)__builtin_amdgcn_readlane((int)v, (int)(f.seq % 64u)); };
+  const KvSpan s{there(own.begin), there(own.count), there(own.pos), true};
   const uint32_t index = s.pos / page + f.local;
   const int32_t page_id = a.table[(uint64_t)f.seq * a.table_stride + index];
   if (page_id < 0 || (uint32_t)page_id >= a.n_pages) {
@@ -166,6 +170,8 @@ __global__ __launch_bounds__(512, 5) void kv_store_kernel(KvArg a, uint32_t page
       const KvItem it = kv_item(a, page, (uint32_t)item, head, lane);
       if (!it.any) continue;
       const bool mine = quad * 4u < page;
+      // rows before r0 are held, by these scales
+      const float k_before = it.r0 ? a.side[0].scales[it.at] : 0.0f, v_before = it.r0 ? a.side[1].scales[it.at] : 0.0f;
       u32x4 kx[4], vx[4];
       // (a place that is no new row gets the nearest one: it changes no maximum,
       // and what is made of it is not written; all loads go out together)
@@ -178,8 +184,7 @@ __global__ __launch_bounds__(512, 5) void kv_store_kernel(KvArg a, uint32_t page
       rows(kx, a.side[0]);
       rows(vx, a.side[1]);
       // the new scale, written, and the codes of the thread's rows in place of them
-      auto quantize = [&](u32x4 (&x)[4], u32x2 (&q)[4], float *scale) {
-        const float before = it.r0 ? *scale : 0.0f;   // rows before r0 are held
+      auto quantize = [&](u32x4 (&x)[4], u32x2 (&q)[4], float before, float *scale) {
         uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -210,7 +215,7 @@ __global__ __launch_bounds__(512, 5) void kv_store_kernel(KvArg a, uint32_t page
       u32x2 q[4];
       {
         int8_t *codes = a.side[0].codes + it.at * (page * D);
-        const float again = quantize(kx, q, a.side[0].scales + it.at);
+        const float again = quantize(kx, q, k_before, a.side[0].scales + it.at);
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) {
           const uint32_t r = quad * 4u + i;
@@ -225,7 +230,7 @@ __global__ __launch_bounds__(512, 5) void kv_store_kernel(KvArg a, uint32_t page
       }
       {
         int8_t *codes = a.side[1].codes + it.at * (page * D);
-        const float again = quantize(vx, q, a.side[1].scales + it.at);
+        const float again = quantize(vx, q, v_before, a.side[1].scales + it.at);
         if (mine)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
