@@ -141,6 +141,13 @@ __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
 // a page's values rides in the exponent, and f16 covers weights down to 2^-29
 // of the largest with 11 bits.  The sum of the softmax is of the same numbers
 // before rounding, divided by the value scale, in 32 bits.
+//
+// Bound by the reading of the cache: 131072 tokens of one sequence (32 / 8 heads
+// of 128) 44 us, 6.1 TB/s, which is what a kernel that only reads reaches; 64
+// ragged sequences of up to 16384 tokens 120 us, 5.2 TB/s; 8 of up to 4099 (32
+// heads of 96) 16 us, 3.7 TB/s, a third of it the way to the first key and the
+// wavefronts' join.  90 tokens: 4.8 us.  At head dimension 128 registers for a
+// third workgroup a CU would take spills: 120 -> 135 us.
 // ---------------------------------------------------------------------------
 template <entro_dtype T, int D>
 __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
@@ -385,7 +392,8 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
 // four at a time, then the groups are joined; the order is the same in every
 // call.  The pieces' reads wait for one another only from batch to batch: with
 // few workgroups (one long sequence: 64 pieces) 16 groups read them at once,
-// with many (few pieces each) four leave room for more workgroups.
+// with many (few pieces each) four leave room for more workgroups.  4 to 5.5 us,
+// a chain of reads: what it moves would take less than one.
 template <entro_dtype T, int D, int G>
 __global__ __launch_bounds__(64 * G) void attn_join_kernel(CacheArg a) {
   __shared__ float red_o[G][D];

@@ -16,7 +16,8 @@
  * 16-bit operands (q, k, v, out) are indexed [token][head][dim]: element
  * (t, h, d) at t * stride_t + h * stride_h + d, strides in elements, so that
  * slices of a joint projection need no copy.  Pointers are 16-byte aligned and
- * strides multiples of 8 (ENTRO_E_INVAL otherwise).
+ * strides multiples of 8 (ENTRO_E_INVAL otherwise).  entro_attn_prompt takes
+ * row strides of q, k and v up to 2^23 elements (ENTRO_E_UNSUPPORTED beyond).
  *
  * Packed sequences.  d_cu holds n_seq + 1 running sums: sequence b has rows
  * d_cu[b] .. d_cu[b + 1] - 1.  A sequence may be empty.
@@ -101,8 +102,10 @@ typedef struct {
  * a query's range have no influence on it, whatever they hold.  Products of
  * 16-bit values are exact and summed in 32 bits, as are the softmax's
  * statistics; the weights are rounded to the element type for the product
- * with v, the result once at the end.  Sequences of any length up to 2^31 - 1
- * rows; out must not overlap the inputs. */
+ * with v and for their sum, the result once at the end.  An infinite value
+ * that a query sees gives it an infinity or, where its weight is no longer above
+ * 0, NaN.  Sequences of any length up to 2^31 - 1 rows; out must not overlap the
+ * inputs. */
 entro_status entro_attn_prompt(const entro_attn_prompt_args *a, uint32_t *d_status, hipStream_t stream);
 
 typedef struct {
@@ -119,9 +122,9 @@ typedef struct {
  *   s1 = max(s0, max |x| * float(1 / 127)) over the new finite x
  *   new codes = rint(x * (1 / s1)), limited to +-127 (infinities are
  *   limited, NaN becomes 0); codes held before = rint(code * (s0 / s1)),
- * in 32-bit arithmetic with rint to even, the scale s1 stored; where s1 or
- * the finite 1 / s1 does not exist (all zero, or below 2^-126) the codes are
- * 0.  No two sequences of a call may write to the same page. */
+ * in 32-bit arithmetic with rint to even, the scale s1 stored; where s1 is
+ * below 2^-126 (all values zero, for one) the codes are 0.  No two sequences of
+ * a call may write to the same page. */
 entro_status entro_kv_store(const entro_kv_cache *c, const entro_kv_table *t, const entro_kv_store_args *a,
                             uint32_t *d_status, hipStream_t stream);
 
