@@ -271,8 +271,9 @@ def decode_gemm(tensors, items, n_tokens: int, d_status: int, stream=None) -> No
 
 
 def set_max_workgroups(n: int) -> int:
-    """``entro_set_max_workgroups``: cap the workgroups of later launches (0:
-    no cap); returns the previous cap."""
+    """``entro_set_max_workgroups`` and ``entro_attn_set_max_workgroups``: cap
+    the workgroups of later launches (0: no cap); returns the previous cap."""
+    load().entro_attn_set_max_workgroups(int(n))
     return int(load().entro_set_max_workgroups(int(n)))
 
 

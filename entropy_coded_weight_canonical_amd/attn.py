@@ -63,6 +63,8 @@ def _bind(lib):
     lib.entro_attn_prompt.restype = ctypes.c_int
     lib.entro_attn_cache_work_bytes.argtypes = [_U32] * 4
     lib.entro_attn_cache_work_bytes.restype = ctypes.c_uint64
+    lib.entro_attn_set_max_workgroups.argtypes = [_U32]
+    lib.entro_attn_set_max_workgroups.restype = _U32
 
 
 _PROMPT = struct.Struct("@PqqPqqPqqPqqPPIIIIIIif")

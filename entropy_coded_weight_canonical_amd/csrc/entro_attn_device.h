@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -162,13 +163,18 @@ __device__ __forceinline__ Span span_of(const int32_t *cu, uint32_t b, uint32_t 
   return {ok ? (uint32_t)lo : 0u, ok ? (uint32_t)(hi - lo) : 0u, ok};
 }
 
-// host side: a grid of x by y workgroups (x going fastest), fewer where
-// entro_set_max_workgroups says so or the launch cannot have as many: the
-// kernels step through both by the grid's extent.
+// Workgroup cap of the attention's and cache's launches
+// (entro_attn_set_max_workgroups; 0: none).
+inline std::atomic<uint32_t> g_attn_max_workgroups{0};
+
+// host side: a grid of x by y workgroups (x going fastest), fewer where the
+// cap says so or the launch cannot have as many: the kernels step through both
+// by the grid's extent.
 inline dim3 grid2(uint64_t x, uint64_t y) {
   const uint64_t gx = std::min<uint64_t>(std::max<uint64_t>(x, 1), 1u << 24);
   const uint64_t gy = std::min<uint64_t>(std::max<uint64_t>(y, 1), 65535u);
-  const uint64_t most = cap_grid(gx * gy), cx = std::min(gx, most);
+  const uint32_t cap = g_attn_max_workgroups.load(std::memory_order_relaxed);
+  const uint64_t most = cap ? std::min<uint64_t>(gx * gy, cap) : gx * gy, cx = std::min(gx, most);
   return dim3((uint32_t)cx, (uint32_t)std::min(gy, std::max<uint64_t>(most / cx, 1)));
 }
 

@@ -488,3 +488,5 @@ extern "C" entro_status entro_attn_prompt(const entro_attn_prompt_args *a, uint3
          : a->head_dim == 96u ? launch_prompt<ENTRO_F16, 96>(p, stream)
                               : launch_prompt<ENTRO_F16, 128>(p, stream);
 }
+
+extern "C" uint32_t entro_attn_set_max_workgroups(uint32_t n) { return g_attn_max_workgroups.exchange(n); }

@@ -2764,7 +2764,7 @@ __global__ __launch_bounds__(kBlockThreads) __attribute__((amdgpu_waves_per_eu(4
 // Workgroup cap of every launch (entro_set_max_workgroups; 0: none).
 static std::atomic<uint32_t> g_max_workgroups{0};
 
-uint64_t cap_grid(uint64_t grid) {
+static uint64_t cap_grid(uint64_t grid) {
   const uint32_t cap = g_max_workgroups.load(std::memory_order_relaxed);
   return cap && grid > cap ? cap : grid;
 }

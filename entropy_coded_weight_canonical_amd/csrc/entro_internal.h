@@ -21,9 +21,6 @@ constexpr uint32_t kInvalidLen = 31u;         // length field of an entry withou
 constexpr uint32_t kFOverrun = 0x01u, kFUnderrun = 0x02u, kFBadCode = 0x04u,
                    kFPadding = 0x08u, kFOffsets = 0x10u, kFLut = 0x20u;
 
-// grid workgroups, or the cap of entro_set_max_workgroups where that is less
-uint64_t cap_grid(uint64_t grid);
-
 enum Mode : int { kModeU8 = 0, kModeBf16 = 1, kModeGemv = 2 };
 
 // One tensor of a launch.

@@ -234,8 +234,8 @@ entro_status entro_decode_gemv(const entro_tensor *t, size_t n, const entro_gemv
 entro_status entro_decode_gemm(const entro_tensor *t, size_t n, const entro_gemv_item *g,
                                uint32_t n_tokens, uint32_t *d_status, hipStream_t stream);
 
-/* Cap the workgroups of every later launch of this library in this process
- * (0, the default: no cap).  A launch then spreads its chunks, tasks or tiles
+/* Cap the workgroups of every later launch of this header's functions in this
+ * process (0, the default: no cap; entro_attn.h has a cap of its own).  A launch then spreads its chunks, tasks or tiles
  * over at most n workgroups (the fused GEMV's streamed launches: at least one
  * per tensor), which leaves CUs free for work on other streams and gives
  * each wavefront a longer run; results do not depend on it.  A launch

@@ -165,6 +165,10 @@ uint64_t entro_attn_cache_work_bytes(uint32_t n_seq, uint32_t n_heads, uint32_t 
 entro_status entro_attn_cache(const entro_kv_cache *c, const entro_kv_table *t, const entro_attn_cache_args *a,
                               uint32_t *d_status, hipStream_t stream);
 
+/* entro_set_max_workgroups for the launches of this header: at most n
+ * workgroups each from now on (0, the default: no cap); returns the cap before. */
+uint32_t entro_attn_set_max_workgroups(uint32_t n);
+
 #ifdef __cplusplus
 }
 #endif
