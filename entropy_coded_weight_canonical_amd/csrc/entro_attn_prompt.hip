@@ -104,8 +104,8 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 // that ends with the sequence's last row, so rows past it arrive as zeros.
 //
 // Scores are K Q^T and outputs V^T P^T with the queries as columns: a lane and
-// the one 32 further hold one query's softmax, whose statistics need one
-// exchange between them a tile, and the weights leave the first product in
+// the one 32 further hold one query's softmax, whose statistics they exchange
+// where its maximum rises and at the end, and the weights leave the first product in
 // the order in which the second takes them (row 8 (r / 4) + 4 half + r % 4 of a
 // product is element r of a half; the values' tokens are read in that order).
 // Values are turned on the way from LDS to registers.
@@ -117,18 +117,20 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 //
 // Bound by the matrix cores, and on them by the card's power: 16384 tokens of
 // 32 / 8 heads of 128 (bf16, normal values) take 2.0 ms, 1080 TFLOP/s, at a
-// clock of 1.5 GHz with the matrix cores busy 61% of it; with all values zero
-// the same work runs at 1480 TFLOP/s (a large library product: 1150 and 1690).
-// 8192 tokens of 32 heads: of 96 447 us, 920 TFLOP/s; of 64 305 us, 900, with
+// clock of 1.5 to 1.7 GHz with the matrix cores busy 63% of it; with all values
+// zero the same work runs at 1480 TFLOP/s (a library product of 8192^3: 1150 and
+// 1690).  8192 tokens of 32 heads: of 96 447 us, 920 TFLOP/s; of 64 305 us, 900, with
 // 6 vector instructions (the exponentials at a quarter of the rate among
 // them) a matrix product at 96.  4096 tokens (32 / 8 heads of 128) 146 us, 2048
-// 51 us, 512 36 us for 8 sequences.  37 tokens 6.6 us, which is latency: sums,
+// 51 us, 8 sequences of 512 42 us.  37 tokens 6.6 us, which is latency: sums,
 // the first tile, the queries, one tile's work, the outputs.
 //
 // Measured and not taken: the scores of the next tile between the exponentials
 // of this one (their registers do not fit at 128; 2048 tokens 52 -> 66 us, 8192
 // tokens of 96 5% slower), wavefront priorities, eight LDS reads ahead instead
-// of six (nothing), packed sequences sorted by length (nothing).
+// of six (nothing), 12 packed sequences longest first (131 -> 136 us), heads in
+// groups of eight, whose keys an XCD's L2 holds (8192 tokens of 32 heads of 96
+// 464 -> 482 us).
 // ---------------------------------------------------------------------------
 constexpr int wavefronts_per_simd(int d) { return d == 64 ? 3 : 2; }   // what the registers allow
 
