@@ -379,6 +379,12 @@ attn_prompt_kernel(PromptArg a) {
         const bool odd = t & 1u;
         part(t, odd ? lds_k1 : lds_k0, odd ? lds_v1 : lds_v0, odd ? lds_k0 : lds_k1, odd ? lds_v0 : lds_v1);
       }
+      // the last tile was seen whole: the copies (of zeros) sent out during it
+      // may still be on their way to the place that the outputs pass through
+      if (full == tiles) {
+        wait_lds_copy();
+        __syncthreads();
+      }
 
       const float sum = add32(l);
       const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;   // NaN stays

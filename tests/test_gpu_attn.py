@@ -147,6 +147,15 @@ def test_prompt_long(ent, dtype):
     run_prompt(ent, (2, 2, 96), dtype, [513], [513])
 
 
+@pytest.mark.parametrize("heads", HEADS)
+def test_prompt_last_tile_seen_whole(ent, heads):
+    """One query behind a multiple of two tiles' keys: every tile is seen whole,
+    and the outputs go out right behind the last one."""
+    say(f"prompt: last tile seen whole, {heads}")
+    run_prompt(ent, heads, "bf16", [1] * 40, [128 * (1 + i % 3) for i in range(40)])
+    run_prompt(ent, heads, "f16", [1] * 9, [256] * 9)
+
+
 def test_prompt_many_sequences(ent):
     say("prompt: 150 sequences")
     lq = [(7 * i) % 11 for i in range(150)]
