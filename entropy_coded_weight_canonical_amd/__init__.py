@@ -23,11 +23,12 @@ __all__ = [
     "quantize", "code_lengths", "encode_layout", "encode",
     "rans_freqs", "rans_table_build", "rans_encode", "rans_decode", "rans_decode_dequant",
     "SCHEME_ASYMMETRIC", "SCHEME_UNSIGNED", "SCHEME_MIXED",
-    "KVCache", "attn_prompt", "kv_store", "kv_load", "attn_cache", "attn_cache_work_bytes",
+    "KVCache", "attn_prompt", "kv_store", "kv_load", "attn_cache", "attn_prompt_work_bytes",
+    "attn_cache_work_bytes",
 ]
 
 from . import attn
-from .attn import KVCache, attn_cache, attn_cache_work_bytes, attn_prompt, kv_load, kv_store
+from .attn import KVCache, attn_cache, attn_cache_work_bytes, attn_prompt, attn_prompt_work_bytes, kv_load, kv_store
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libentro.so")

@@ -18,7 +18,7 @@ import ctypes
 import math
 import struct
 
-__all__ = ["KVCache", "attn_prompt", "kv_store", "kv_load", "attn_cache", "attn_cache_work_bytes"]
+__all__ = ["KVCache", "attn_prompt", "kv_store", "kv_load", "attn_cache", "attn_prompt_work_bytes", "attn_cache_work_bytes"]
 
 _P, _U32, _I64 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_int64
 
@@ -43,7 +43,7 @@ class Table(ctypes.Structure):
 class PromptArgs(ctypes.Structure):
     _fields_ = [("q", Rows), ("k", Rows), ("v", Rows), ("out", Rows), ("d_cu_q", _P), ("d_cu_k", _P), ("n_seq", _U32),
                 ("total_q", _U32), ("total_k", _U32), ("n_heads", _U32), ("n_kv_heads", _U32), ("head_dim", _U32),
-                ("dtype", ctypes.c_int), ("scale", ctypes.c_float)]
+                ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("d_work", _P), ("work_bytes", ctypes.c_uint64)]
 
 
 class StoreArgs(ctypes.Structure):
@@ -61,13 +61,15 @@ def _bind(lib):
         getattr(lib, name).restype = ctypes.c_int
     lib.entro_attn_prompt.argtypes = [_P, _P, _P]
     lib.entro_attn_prompt.restype = ctypes.c_int
+    lib.entro_attn_prompt_work_bytes.argtypes = [_U32] * 6
+    lib.entro_attn_prompt_work_bytes.restype = ctypes.c_uint64
     lib.entro_attn_cache_work_bytes.argtypes = [_U32] * 4
     lib.entro_attn_cache_work_bytes.restype = ctypes.c_uint64
     lib.entro_attn_set_max_workgroups.argtypes = [_U32]
     lib.entro_attn_set_max_workgroups.restype = _U32
 
 
-_PROMPT = struct.Struct("@PqqPqqPqqPqqPPIIIIIIif")
+_PROMPT = struct.Struct("@PqqPqqPqqPqqPPIIIIIIifPQ")
 _STORE = struct.Struct("@PqqPqqPPIi")
 _CACHE = struct.Struct("@PqqPqqPIifPQ")
 _TABLE = struct.Struct("@PIIIi")
@@ -198,13 +200,31 @@ def _empty(shape, dtype, like, stream):
         return torch.empty(*shape, dtype=dtype, device=like.device)
 
 
-def attn_prompt(q, k, v, cu_q, cu_k, status, scale=None, out=None, stream=None):
+def _workspace(work):
+    """(pointer, bytes) of a workspace."""
+    if not work.is_cuda or not work.is_contiguous():
+        raise ValueError("work: a contiguous tensor on the GPU expected")
+    return work.data_ptr(), work.numel() * work.element_size()
+
+
+def attn_prompt_work_bytes(n_seq: int, rows_q: int, rows_k: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    """``entro_attn_prompt_work_bytes``: the workspace of ``attn_prompt`` (0:
+    none)."""
+    from . import load
+
+    return int(load().entro_attn_prompt_work_bytes(n_seq, rows_q, rows_k, n_heads, n_kv_heads, head_dim))
+
+
+def attn_prompt(q, k, v, cu_q, cu_k, status, scale=None, out=None, stream=None, work=None):
     """Causal attention of packed sequences (``entro_attn_prompt``): ``q``
     [rows][heads][dim], ``k`` and ``v`` [rows][kv heads][dim] with any row and
     head strides that are multiples of 8, ``cu_q`` and ``cu_k`` int32 running
     sums (n + 1).  A sequence's last keys are its queries' own; more keys than
-    queries are tokens in front of them.  Returns ``out`` [rows][heads][dim]
-    (rows of no sequence are left as they are)."""
+    queries are tokens in front of them.  ``work``: a contiguous tensor of at
+    least ``attn_prompt_work_bytes`` bytes that no call on another stream uses
+    meanwhile (made for the call by default, but on a raw stream handle: there
+    the keys of few queries are then not split over more workgroups).  Returns
+    ``out`` [rows][heads][dim] (rows of no sequence are left as they are)."""
     _torch_once()
     n = cu_q.shape[0] - 1
     if n < 0 or q.dim() != 3 or k.dim() != 3:
@@ -221,10 +241,19 @@ def attn_prompt(q, k, v, cu_q, cu_k, status, scale=None, out=None, stream=None):
         ro = _rows(out, "out", t, heads, dim)
         if out.shape[0] != rows:
             raise ValueError("out has the rows of q")
+    w = size = 0
+    if work is not None:
+        w, size = _workspace(work)
+    elif n and k.shape[0] >= 1024 * n and (stream is None or hasattr(stream, "cuda_stream")):   # (none below)
+        size = attn_prompt_work_bytes(n, rows, k.shape[0], heads, kv, dim)
+        if size:
+            work = _empty((size,), torch.uint8, q, stream)
+            w = work.data_ptr()
     a = _PROMPT.pack(*_rows(q, "q", t, heads, dim), *_rows(k, "k", t, kv, dim), *_rows(v, "v", t, kv, dim), *ro,
                      _ints(cu_q, "cu_q", n + 1), _ints(cu_k, "cu_k", n + 1), n, rows,
-                     k.shape[0], heads, kv, dim, _dtype_id(t), 1.0 / math.sqrt(dim) if scale is None else scale)
-    _call("entro_attn_prompt", a, _ints(status, "status", n), _on(stream, q, k, v, cu_q, cu_k, status, out))
+                     k.shape[0], heads, kv, dim, _dtype_id(t), 1.0 / math.sqrt(dim) if scale is None else scale, w, size)
+    used = (q, k, v, cu_q, cu_k, status, out) if work is None else (q, k, v, cu_q, cu_k, status, out, work)
+    _call("entro_attn_prompt", a, _ints(status, "status", n), _on(stream, *used))
     return out
 
 
@@ -304,10 +333,9 @@ def attn_cache(q, cache: KVCache, table, lens, status, scale=None, out=None, wor
                 _work_sizes.clear()
             need = _work_sizes[n, heads, kv, dim] = attn_cache_work_bytes(n, heads, kv, dim)
         work = _empty((max(need, 16),), torch.uint8, q, stream)
-    elif not work.is_cuda or not work.is_contiguous():
-        raise ValueError("work: a contiguous tensor on the GPU expected")
+    w, size = _workspace(work)
     a = _CACHE.pack(*_rows(q, "q", t, heads, dim), *ro, _ints(lens, "lens", n), heads, _dtype_id(t),
-                    1.0 / math.sqrt(dim) if scale is None else scale, work.data_ptr(), work.numel() * work.element_size())
+                    1.0 / math.sqrt(dim) if scale is None else scale, w, size)
     _call("entro_attn_cache", cache.desc, _table(table, n), a, _ints(status, "status", n),
           _on(stream, q, *cache.tensors, table, lens, status, out, work))
     return out

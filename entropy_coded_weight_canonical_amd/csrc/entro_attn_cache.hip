@@ -111,10 +111,6 @@ __device__ __forceinline__ f16v8 half8(uint32_t w0, uint32_t w1) {
   return __builtin_bit_cast(f16v8, (u32x4){a.x, a.y, b.x, b.y});
 }
 
-// Factor of a part with maximum m where the parts' is `all`: parts without
-// tokens (both -inf) count with their zeros, NaN passes through.
-__device__ __forceinline__ float join_factor(float m, float all) { return m == all ? 1.0f : exp2_fast(m - all); }
-
 __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }

@@ -93,6 +93,10 @@ __device__ __forceinline__ float add16(float v) {
   return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
 }
 
+// Factor of a part with maximum m where the parts' is `all`: parts without
+// tokens (both -inf) count with their zeros, NaN passes through.
+__device__ __forceinline__ float join_factor(float m, float all) { return m == all ? 1.0f : exp2_fast(m - all); }
+
 // Inclusive running sum (maximum) over the wavefront's lanes: within rows of 16
 // by shifts, then the rows' ends to the rows after (vector instructions only;
 // all lanes active).

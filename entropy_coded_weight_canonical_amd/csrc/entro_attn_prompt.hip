@@ -16,6 +16,9 @@ struct PromptArg {
   uint32_t n_seq, total_q, total_k, n_heads, n_kv;
   uint32_t turned;                                  // this many of the first items in reverse order
   uint32_t heads;                                   // query heads of a workgroup: 1, 2 or 4 of one key/value head
+  uint32_t parts;                                   // workgroups that share an item's keys
+  float *part_o;                                    // parts > 1: [parts][total_q][n_heads][D]
+  f32x2 *part_ml;                                   // [parts][total_q][n_heads]: maximum in powers of two, sum
   float scale;                                      // magnitude, times log2(e); 1 where the scale is 0
   uint32_t q_and, q_xor;                            // on a pair of q: the scale's sign, and 0 where the scale is 0
   uint32_t *status;
@@ -115,6 +118,11 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 // wavefronts that copied it, and where it holds infinities or NaN these are
 // left out of the product and added at the end, to the queries that see them.
 //
+// Few queries with many keys (a piece of a prompt behind a long prefix) are too
+// few workgroups, each with a long way: `parts` of them then take an equal
+// share of an item's tiles each and leave their sums, which a second kernel
+// joins.
+//
 // Bound by the matrix cores, and on them by the card's power: 16384 tokens of
 // 32 / 8 heads of 128 (bf16, normal values) take 2.0 ms, 1080 TFLOP/s, at a
 // clock of 1.5 to 1.7 GHz with the matrix cores busy 63% of it; with all values
@@ -122,7 +130,7 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 // 1690).  8192 tokens of 32 heads: of 96 447 us, 920 TFLOP/s; of 64 305 us, 900, with
 // 6 vector instructions (the exponentials at a quarter of the rate among
 // them) a matrix product at 96.  4096 tokens (32 / 8 heads of 128) 146 us, 2048
-// 51 us, 8 sequences of 512 42 us.  37 tokens 6.6 us, which is latency: sums,
+// 48 us, 8 sequences of 512 42 us.  37 tokens 6.6 us, which is latency: sums,
 // the first tile, the queries, one tile's work, the outputs.
 //
 // Measured and not taken: the scores of the next tile between the exponentials
@@ -167,7 +175,8 @@ attn_prompt_kernel(PromptArg a) {
   };
   const uint32_t turned = a.turned ? min(a.turned, count_items(a.n_seq, lane, items)) : 0u;
   for (uint32_t slot = blockIdx.x; slot < a.n_heads / a.heads; slot += gridDim.x)
-    for (uint32_t at = blockIdx.y;; at += gridDim.y) {
+    for (uint32_t y = blockIdx.y;; y += gridDim.y) {
+      const uint32_t at = y / a.parts, share = y % a.parts;
       // a key/value head's query heads and tiles stay on one XCD (workgroups go
       // around the 8 in turn) where n_kv is a multiple of 8
       const uint32_t kvh = slot % a.n_kv, head = kvh * (a.n_heads / a.n_kv) + slot / a.n_kv * a.heads + wave % a.heads;
@@ -191,8 +200,11 @@ attn_prompt_kernel(PromptArg a) {
       // keys that the workgroup, and this wavefront, see
       const int64_t wg_end = max((int64_t)0, (int64_t)min(wg0 + rows, count_q) + shift);
       const int64_t my_end = q0 < count_q ? max((int64_t)0, (int64_t)min(q0 + kQueries, count_q) + shift) : 0;
-      const uint32_t tiles = rfl((uint32_t)((wg_end + kTile - 1) / kTile));
+      const uint32_t all_tiles = rfl((uint32_t)((wg_end + kTile - 1) / kTile)), pairs = (all_tiles + 1u) / 2u;
       const uint32_t mine = (uint32_t)((my_end + kTile - 1) / kTile);
+      // this workgroup's tiles: `begin`, even, to `tiles`
+      const uint32_t begin = rfl((uint32_t)((uint64_t)pairs * share / a.parts) * 2u);
+      const uint32_t tiles = rfl(min(all_tiles, (uint32_t)((uint64_t)pairs * (share + 1u) / a.parts) * 2u));
       // tiles that every query of the workgroup sees whole, an even number
       const uint32_t full = (uint32_t)min((int64_t)tiles, max((int64_t)0, (int64_t)wg0 + shift + 1) / kTile) & ~1u;
 
@@ -219,7 +231,7 @@ attn_prompt_kernel(PromptArg a) {
       __syncthreads();   // the last item's tiles and marks have been read
       if (tid < 2u) lds_special[tid] = 0u;
       __syncthreads();   // no mark is set before
-      if (tiles) copy_all(0, lds_k0, lds_v0);
+      if (begin < tiles) copy_all(begin, lds_k0, lds_v0);
       // the wavefront's queries, by way of its quarter of the other tile's place
       // (whole rows a copy; rows past the end are zeros)
       u32x4 qf[KS];
@@ -370,7 +382,7 @@ attn_prompt_kernel(PromptArg a) {
           outputs(s, vt, ln, [](u32x4 w) { return w; });
         }
       };
-      uint32_t t = 0;
+      uint32_t t = begin;
       for (; t < full; t += 2u) {
         whole(t, lds_k0, lds_v0, lds_k1, lds_v1);
         whole(t + 1u, lds_k1, lds_v1, lds_k0, lds_v0);
@@ -385,13 +397,14 @@ attn_prompt_kernel(PromptArg a) {
         wait_lds_copy();
         __syncthreads();
       }
+      const int64_t at_row = (int64_t)begin_q + q0;
 
       const float sum = add32(l);
-      const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;   // NaN stays
+      const float inv = a.parts > 1u ? 1.0f : sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;   // NaN stays
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d] *= inv;
       if (left_out)
-        for (int64_t j = (int64_t)full * kTile; j < my_end; ++j) {
+        for (int64_t j = (int64_t)max(begin, full) * kTile; j < min(my_end, (int64_t)tiles * kTile); ++j) {
           const char *vp = vb + j * a.v_t + half * 8u;
 #pragma unroll
           for (int d = 0; d < DT; ++d)
@@ -406,6 +419,20 @@ attn_prompt_kernel(PromptArg a) {
               }
             }
         }
+      if (a.parts > 1u) {
+        const uint32_t ln = fresh(lane);
+        if (q0 + (ln & 31u) < count_q) {
+          const uint64_t row = ((uint64_t)share * a.total_q + (uint64_t)(at_row + (ln & 31u))) * a.n_heads + head;
+          float *to = a.part_o + row * D + (ln >> 5) * 4u;
+#pragma unroll
+          for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; r += 4)
+              *reinterpret_cast<f32x4 *>(to + 32 * d + 2 * r) = (f32x4){o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]};
+          if (ln < 32u) a.part_ml[row] = (f32x2){m * a.scale, sum};
+        }
+        continue;
+      }
       // rows out by way of the place of the tile before the last, which every
       // wavefront has left, so that a store writes whole rows
       {
@@ -428,28 +455,122 @@ attn_prompt_kernel(PromptArg a) {
     }
 }
 
+// Joins the parts of split items: D / 4 threads a row and head, as many rows of
+// a sequence a workgroup as it has threads for, eight parts' reads at once.
 template <entro_dtype T, int D>
-static entro_status launch_prompt(PromptArg &a, hipStream_t s) {
-  const uint32_t group = a.n_heads / a.n_kv;
+__global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArg a) {
+  constexpr uint32_t L = D / 4u, R = 256u / L, kBatch = 8u;
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, d = tid % L * 4u;
+  Span lq{}, lk{};
+  auto items = [&](uint32_t b) {
+    lq = span_of(a.cu_q, b, a.total_q);
+    lk = span_of(a.cu_k, b, a.total_k);
+    return lk.ok ? (lq.count + R - 1u) / R : 0u;
+  };
+  for (uint32_t head = blockIdx.x; head < a.n_heads; head += gridDim.x)
+    for (uint32_t y = blockIdx.y;; y += gridDim.y) {
+      const Found f = find_item(y, a.n_seq, lane, items);
+      if (f.seq == a.n_seq) break;
+      const uint32_t in = f.seq % 64u;
+      const uint32_t count_q = __builtin_amdgcn_readlane(lq.count, in), begin_q = __builtin_amdgcn_readlane(lq.begin, in);
+      const uint32_t i = f.local * R + tid / L;
+      if (tid < R * L && i < count_q) {
+        const uint64_t row = (uint64_t)(begin_q + i) * a.n_heads + head, step = (uint64_t)a.total_q * a.n_heads;
+        float m = -INFINITY, l = 0.0f;
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (uint32_t p0 = 0; p0 < a.parts; p0 += kBatch) {
+          f32x2 ml[kBatch];
+          f32x4 o[kBatch];
+#pragma unroll
+          for (uint32_t j = 0; j < kBatch; ++j) {
+            const uint64_t at = row + min(p0 + j, a.parts - 1u) * step;
+            ml[j] = a.part_ml[at];
+            o[j] = *reinterpret_cast<const f32x4 *>(a.part_o + at * D + d);
+          }
+          float mn = m;
+#pragma unroll
+          for (uint32_t j = 0; j < kBatch; ++j) mn = fmaxf(mn, ml[j].x);
+          const float k = join_factor(m, mn);
+          x *= k;
+          l *= k;
+          m = mn;
+#pragma unroll
+          for (uint32_t j = 0; j < kBatch; ++j) {
+            if (p0 + j >= a.parts) break;
+            const float kj = join_factor(ml[j].x, m);
+            x += kj * o[j];
+            l += kj * ml[j].y;
+          }
+        }
+        const float r = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;   // NaN stays
+        *reinterpret_cast<u32x2 *>(a.out + (int64_t)(begin_q + i) * a.o_t + head * a.o_h + d * 2u) =
+            (u32x2){Elem<T>::pack2(x[0] * r, x[1] * r), Elem<T>::pack2(x[2] * r, x[3] * r)};
+      }
+    }
+}
+
+// A call's workgroups: `slots` times `items` (at most) times `parts`.
+struct PromptGrid {
+  uint32_t heads, slots, parts;
+  uint64_t items;
+};
+static PromptGrid prompt_grid(uint32_t n_seq, uint32_t total_q, uint32_t total_k, uint32_t n_heads, uint32_t n_kv,
+                              uint32_t head_dim) {
+  PromptGrid g{};
+  const uint32_t group = n_heads / n_kv;
   // sequences of 64 queries on average: 256 x 64 (32 / 8 heads of 128) 215 us
   // by queries, 140 by heads; 128 x 128 the same; 16 x 1024 212 and 220
-  const bool small = a.total_q <= 64ull * a.n_seq;
-  a.heads = !small ? 1u : group % 4u == 0u ? 4u : group % 2u == 0u ? 2u : 1u;
-  const uint32_t rows = 32u * kWaves4 / a.heads;
-  const uint32_t slots = a.n_heads / a.heads;
-  const uint64_t items = std::min<uint64_t>(a.total_q, (uint64_t)a.total_q / rows + a.n_seq);
+  const bool small = total_q <= 64ull * n_seq;
+  g.heads = !small ? 1u : group % 4u == 0u ? 4u : group % 2u == 0u ? 2u : 1u;
+  g.slots = n_heads / g.heads;
+  const uint32_t rows = 32u * kWaves4 / g.heads;
+  g.items = std::min<uint64_t>(total_q, (total_q + (uint64_t)n_seq * (rows - 1u)) / rows);
+  g.parts = 1u;
+  const uint64_t all = g.items * g.slots, tiles = total_k / n_seq / kTile;
+  if (all == 0u || all > 256u || tiles < 16u) return g;
+  // Too few workgroups for the CUs: with n parts the way through the tiles takes
+  // a share of n less (0.6 us a tile at least), the sums of all rows are written and
+  // read n times (about 6 bytes a picosecond), and the second kernel takes some
+  // 6 us.  The n with the least of both, from 4 tiles a part and 32 parts (the
+  // second kernel's own way) on down.  32 / 8 heads of 128, split and not: one
+  // query, 16000 keys 30 and 218 us, 1100 keys 18 and 24; 128 queries behind 4000
+  // keys 29 and 64; 9 x 13 behind 3506 38 and 58; 512 behind 4000 61 and 75, behind
+  // 1000 (not split) 38 and 33.
+  const double way = 0.6 * (double)tiles, sums = (double)total_q * n_heads * head_dim * 8.0 / 6e6;
+  const uint64_t parts = std::min<uint64_t>({512u / all, tiles / 4u, 32u, (uint64_t)std::sqrt(way / sums)});
+  if (parts > 1u && way - way / (double)parts > 6.0 + sums * (double)parts) g.parts = (uint32_t)parts;
+  return g;
+}
+
+template <entro_dtype T, int D>
+static entro_status launch_prompt(PromptArg &a, const PromptGrid &g, hipStream_t s) {
   // Where all workgroups run at once, the 256 first get a CU each and the rest
   // follow in the same order: the first ones' order is turned around, so that
   // the CUs with the least of them to do get the most of the rest.
-  a.turned = items * slots <= 512u ? 256u / slots : 0u;
+  a.turned = a.parts == 1u && g.items * g.slots <= 512u ? 256u / g.slots : 0u;
+  a.part_ml = reinterpret_cast<f32x2 *>(a.part_o + (uint64_t)a.parts * a.total_q * a.n_heads * D);
   (void)hipGetLastError();
-  hipLaunchKernelGGL((attn_prompt_kernel<T, D>), grid2(slots, items), dim3(256), 0, s, a);
-  return hipGetLastError() == hipSuccess ? ENTRO_OK : ENTRO_E_HIP;
+  hipLaunchKernelGGL((attn_prompt_kernel<T, D>), grid2(g.slots, g.items * a.parts), dim3(256), 0, s, a);
+  if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
+  if (a.parts > 1u) {
+    const uint32_t rows = 256u / (D / 4u);
+    const uint64_t items = std::min<uint64_t>(a.total_q, (uint64_t)a.total_q / rows + a.n_seq);
+    hipLaunchKernelGGL((attn_prompt_join_kernel<T, D>), grid2(a.n_heads, items), dim3(256), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
+  }
+  return ENTRO_OK;
 }
 
 }  // namespace entro
 
 using namespace entro;
+
+extern "C" uint64_t entro_attn_prompt_work_bytes(uint32_t n_seq, uint32_t total_q, uint32_t total_k, uint32_t n_heads,
+                                                 uint32_t n_kv_heads, uint32_t head_dim) {
+  if (n_seq == 0 || check_heads(n_heads, n_kv_heads, head_dim, ENTRO_BF16) != ENTRO_OK) return 0;
+  const uint64_t parts = prompt_grid(n_seq, total_q, total_k, n_heads, n_kv_heads, head_dim).parts;
+  return parts > 1u ? parts * total_q * n_heads * (head_dim + 2ull) * 4ull : 0u;
+}
 
 extern "C" entro_status entro_attn_prompt(const entro_attn_prompt_args *a, uint32_t *d_status, hipStream_t stream) {
   if (!a) return ENTRO_E_INVAL;
@@ -462,6 +583,10 @@ extern "C" entro_status entro_attn_prompt(const entro_attn_prompt_args *a, uint3
   if ((st = check_rows(a->q, a->total_q)) != ENTRO_OK || (st = check_rows(a->out, a->total_q)) != ENTRO_OK ||
       (st = check_rows(a->k, a->total_k)) != ENTRO_OK || (st = check_rows(a->v, a->total_k)) != ENTRO_OK)
     return st;
+  if (a->d_work && ((reinterpret_cast<uintptr_t>(a->d_work) & 15u) ||
+                    a->work_bytes < entro_attn_prompt_work_bytes(a->n_seq, a->total_q, a->total_k, a->n_heads,
+                                                                 a->n_kv_heads, a->head_dim)))
+    return ENTRO_E_INVAL;
   // copies reach up to 64 rows with 32-bit offsets
   if (a->q.stride_t > (1 << 23) || a->k.stride_t > (1 << 23) || a->v.stride_t > (1 << 23)) return ENTRO_E_UNSUPPORTED;
   PromptArg p{};
@@ -488,13 +613,17 @@ extern "C" entro_status entro_attn_prompt(const entro_attn_prompt_args *a, uint3
   p.q_and = a->scale == 0.0f ? 0u : 0xFFFFFFFFu;
   p.q_xor = a->scale < 0.0f ? 0x80008000u : 0u;
   p.status = d_status;
+  const PromptGrid g = prompt_grid(a->n_seq, a->total_q, a->total_k, a->n_heads, a->n_kv_heads, a->head_dim);
+  p.heads = g.heads;
+  p.parts = a->d_work ? g.parts : 1u;
+  p.part_o = static_cast<float *>(a->d_work);
   if (a->dtype == ENTRO_BF16)
-    return a->head_dim == 64u   ? launch_prompt<ENTRO_BF16, 64>(p, stream)
-           : a->head_dim == 96u ? launch_prompt<ENTRO_BF16, 96>(p, stream)
-                                : launch_prompt<ENTRO_BF16, 128>(p, stream);
-  return a->head_dim == 64u   ? launch_prompt<ENTRO_F16, 64>(p, stream)
-         : a->head_dim == 96u ? launch_prompt<ENTRO_F16, 96>(p, stream)
-                              : launch_prompt<ENTRO_F16, 128>(p, stream);
+    return a->head_dim == 64u   ? launch_prompt<ENTRO_BF16, 64>(p, g, stream)
+           : a->head_dim == 96u ? launch_prompt<ENTRO_BF16, 96>(p, g, stream)
+                                : launch_prompt<ENTRO_BF16, 128>(p, g, stream);
+  return a->head_dim == 64u   ? launch_prompt<ENTRO_F16, 64>(p, g, stream)
+         : a->head_dim == 96u ? launch_prompt<ENTRO_F16, 96>(p, g, stream)
+                              : launch_prompt<ENTRO_F16, 128>(p, g, stream);
 }
 
 extern "C" uint32_t entro_attn_set_max_workgroups(uint32_t n) { return g_attn_max_workgroups.exchange(n); }

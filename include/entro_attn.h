@@ -92,7 +92,16 @@ typedef struct {
   uint32_t n_heads, n_kv_heads, head_dim;
   entro_dtype dtype;
   float scale;             /* factor of q . k, finite */
+  void *d_work;            /* NULL, or entro_attn_prompt_work_bytes, 16-byte aligned; contents irrelevant */
+  uint64_t work_bytes;
 } entro_attn_prompt_args;
+
+/* Bytes of workspace with which entro_attn_prompt splits the keys of a call
+ * whose few queries have many keys each (a piece of a prompt behind a long
+ * prefix) over more workgroups; 0 where it would not, or where an argument is
+ * out of its range.  Without workspace the keys are not split. */
+uint64_t entro_attn_prompt_work_bytes(uint32_t n_seq, uint32_t total_q, uint32_t total_k, uint32_t n_heads,
+                                      uint32_t n_kv_heads, uint32_t head_dim);
 
 /* Causal attention of packed prompts.  For sequence b with Lq queries and Lk
  * keys (the last Lq of them the queries' own), query i and head h:

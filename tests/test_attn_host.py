@@ -116,6 +116,19 @@ def test_cache_attention_refusals(lib, change):
     assert lib.entro_attn_cache(ctypes.byref(cache()), ctypes.byref(table()), ctypes.byref(over(**change)), P, None) == INVAL
 
 
+def test_prompt_workspace(lib):
+    size = ent.attn_prompt_work_bytes
+    assert size(0, 8, 8, 8, 2, 64) == 0 and size(1, 8, 8000, 7, 2, 64) == 0 and size(1, 8, 8000, 8, 2, 80) == 0
+    assert size(1, 500, 500, 8, 2, 64) == 0 and size(64, 64, 64 * 1000, 8, 2, 64) == 0    # short ones
+    assert size(1, 0, 8000, 8, 2, 64) == 0 and size(1, 8000, 8000, 32, 8, 128) == 0        # nothing, enough workgroups
+    one = 32 * 130 * 4
+    assert size(1, 1, 16000, 32, 8, 128) % one == 0 and size(1, 1, 16000, 32, 8, 128) // one > 8
+    big = dict(total_q=1, total_k=16000, n_seq=1, n_heads=32, n_kv_heads=8, head_dim=128)
+    need = size(1, 1, 16000, 32, 8, 128)
+    for change in (dict(d_work=P, work_bytes=need - 1), dict(d_work=P, work_bytes=0), dict(d_work=P + 8, work_bytes=need)):
+        assert lib.entro_attn_prompt(ctypes.byref(prompt(**big, **change)), P, None) == INVAL
+
+
 def test_work_bytes():
     assert ent.attn_cache_work_bytes(0, 8, 2, 64) == 0
     assert ent.attn_cache_work_bytes(1, 8, 3, 64) == 0
@@ -185,7 +198,7 @@ def test_oracle_store_round_trip():
 
 def test_packed_arguments_have_the_structures_layout():
     for packed, structure, values in (
-        (attn._PROMPT, attn.PromptArgs, (1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 16, 17, 18, 19, 20, 1, 0.5)),
+        (attn._PROMPT, attn.PromptArgs, (1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 16, 17, 18, 19, 20, 1, 0.5, 21, 22)),
         (attn._STORE, attn.StoreArgs, (1, 2, 3, 4, 5, 6, 7, 8, 9, 1)),
         (attn._CACHE, attn.CacheArgs, (1, 2, 3, 4, 5, 6, 7, 8, 1, 0.5, 9, 10)),
         (attn._TABLE, attn.Table, (1, 2, 3, 4, 0)),

@@ -156,6 +156,73 @@ def test_prompt_last_tile_seen_whole(ent, heads):
     run_prompt(ent, heads, "f16", [1] * 9, [256] * 9)
 
 
+SPLIT = [
+    ([5], [1500]),
+    ([1], [4097]),
+    ([26, 1, 3], [3506, 1100, 2000]),
+    ([3, 2, 7, 4], [5000, 0, 70, 129]),          # parts without tiles, rows without keys
+    ([9, 30], [1024, 1024]),
+    ([2, 0, 1], [1, 3000, 4000]),
+    ([70], [2048]),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("lengths", SPLIT, ids=lambda x: "q" + "_".join(map(str, x[0])) + "-k" + "_".join(map(str, x[1])))
+def test_prompt_split_keys_match_oracle(ent, heads, dtype, lengths):
+    """Few queries with many keys: the keys are split over workgroups."""
+    say(f"prompt, keys split: {heads} {dtype} {lengths}")
+    lq, lk = lengths
+    assert ent.attn_prompt_work_bytes(len(lq), sum(lq) + 3, sum(lk) + 3, *heads) > 0
+    run_prompt(ent, heads, dtype, lq, lk)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_prompt_split_keys_hidden_and_given(ent, dtype):
+    """Hidden infinities and NaN; workspace given, and none on a raw handle; the
+    workgroup cap; another stream."""
+    say(f"prompt, keys split: hidden values, workspace, {dtype}")
+    h, kv, d = 8, 2, 128
+    lq, lk = [20, 3], [2500, 1900]
+    g = torch.Generator(device="cuda").manual_seed(8)
+    q = torch.randn(23, h, d, device="cuda", generator=g).to(TORCH[dtype])
+    k, v = (torch.randn(4400, kv, d, device="cuda", generator=g).to(TORCH[dtype]) for _ in range(2))
+    cq, ck, status = ints(running(lq)), ints(running(lk)), torch.zeros(2, dtype=torch.int32, device="cuda")
+    want = ent.attn_prompt(q, k, v, cq, ck, status)
+    size = ent.attn_prompt_work_bytes(2, 23, 4400, h, kv, d)
+    assert size > 0
+    work = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    assert torch.equal(ent.attn_prompt(q, k, v, cq, ck, status, work=work), want)
+    with pytest.raises(ent.EntroError):
+        ent.attn_prompt(q, k, v, cq, ck, status, work=work[:-16])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = ent.attn_prompt(q, k, v, cq, ck, status, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+    old = ent.set_max_workgroups(5)
+    try:
+        assert torch.equal(ent.attn_prompt(q, k, v, cq, ck, status), want)
+    finally:
+        ent.set_max_workgroups(old)
+    whole = torch.empty_like(want)
+    ent.attn_prompt(q, k, v, cq, ck, status, out=whole, stream=torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    gap = np.abs(np64(whole) - np64(want)).max()
+    # on each side the result is rounded, and weights that sum to 1 (scores and
+    # sums in 32 bits: within a tenth of that)
+    assert gap <= 2 * ROUND[dtype] * (np.abs(np64(want)).max() + 1.1 * np.abs(np64(v)).max())
+    # the first sequence's queries 10 on see tokens 2490 on
+    k[2490], v[2490], v[2495] = math.nan, math.inf, math.nan
+    got = ent.attn_prompt(q, k, v, cq, ck, status)
+    torch.cuda.synchronize()
+    assert not status.any()
+    near(got[:10], want[:10], dtype)
+    near(got[20:], want[20:], dtype)
+    assert not torch.isfinite(got[10:20]).all(-1).any()
+
+
 def test_prompt_many_sequences(ent):
     say("prompt: 150 sequences")
     lq = [(7 * i) % 11 for i in range(150)]
