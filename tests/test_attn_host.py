@@ -194,26 +194,3 @@ def test_oracle_store_round_trip():
     kk, vv = oa.rows_of(*z, t[0], 0, 50)
     # half a step of the page's scale, twice where a code was rounded again
     assert np.abs(kk - k).max() <= 1.02 * z[2].max() and np.abs(vv - v).max() <= 1.02 * z[3].max()
-
-
-def test_packed_arguments_have_the_structures_layout():
-    for packed, structure, values in (
-        (attn._PROMPT, attn.PromptArgs, (1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 16, 17, 18, 19, 20, 1, 0.5, 21, 22)),
-        (attn._STORE, attn.StoreArgs, (1, 2, 3, 4, 5, 6, 7, 8, 9, 1)),
-        (attn._CACHE, attn.CacheArgs, (1, 2, 3, 4, 5, 6, 7, 8, 1, 0.5, 9, 10)),
-        (attn._TABLE, attn.Table, (1, 2, 3, 4, 0)),
-        (attn._PAGES, attn.Cache, (1, 2, 3, 4, 5, 6, 7, 8)),
-    ):
-        assert packed.size == ctypes.sizeof(structure)
-        got, want = structure.from_buffer_copy(packed.pack(*values)), []
-
-        def fields(s):
-            for name, kind in s._fields_:
-                x = getattr(s, name)
-                if isinstance(x, ctypes.Structure):
-                    yield from fields(x)
-                else:
-                    yield x
-
-        want = list(values[:4]) if structure is attn.Table else list(values)
-        assert list(fields(got)) == want
