@@ -157,8 +157,10 @@ __device__ __forceinline__ Grow grow(float before, float top) {
 // are merged with what the page holds.  Memory bound: 2 bytes in and 1 out per
 // value.  32768 tokens of 8 heads of 128: 44 us, 4.6 TB/s of both together (a
 // large copy reaches 4.8); 4522 tokens of 12 sequences, 32 heads of 96 in pages
-// of 32: 25 us, 3.3 TB/s.  One token for each of 16 sequences: 7.5 us, a chain of
-// reads (sums, page, rows and scale, codes held).
+// of 32: 25 us, 3.4 TB/s.  One token for each of 16 sequences: 7.0 us, 7.3 where
+// the range grows: a chain of reads (sums, page, rows and scale, codes held).
+// Reading the codes held with the rows takes registers: it spills and costs the
+// large calls 10%.
 // ---------------------------------------------------------------------------
 template <entro_dtype T, int D>
 __global__ __launch_bounds__(512, 5) void kv_store_kernel(KvArg a, uint32_t page) {
@@ -226,9 +228,15 @@ __global__ __launch_bounds__(512, 5) void kv_store_kernel(KvArg a, uint32_t page
         }
         if (again != 1.0f)   // the range grew
 #pragma unroll 1
-          for (uint32_t i = tid; i < it.r0 * (D / 4u); i += blockDim.x) {
-            uint32_t *w = reinterpret_cast<uint32_t *>(codes) + i;
-            *w = again4(*w, again);
+          for (uint32_t i = tid; i < it.r0 * (D / 16u); i += blockDim.x) {
+            u32x4 *to = reinterpret_cast<u32x4 *>(codes) + i;
+            u32x4 w = *to;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              w[e] = again4(w[e], again);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+            *to = w;
           }
       }
       {
