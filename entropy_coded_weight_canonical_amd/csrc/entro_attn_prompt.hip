@@ -529,15 +529,20 @@ static PromptGrid prompt_grid(uint32_t n_seq, uint32_t total_q, uint32_t total_k
   const uint64_t all = g.items * g.slots, tiles = total_k / n_seq / kTile;
   if (all == 0u || all > 256u || tiles < 16u) return g;
   // Too few workgroups for the CUs: with n parts the way through the tiles takes
-  // a share of n less (0.6 us a tile at least), the sums of all rows are written and
-  // read n times (about 6 bytes a picosecond), and the second kernel takes some
-  // 6 us.  The n with the least of both, from 4 tiles a part and 32 parts (the
-  // second kernel's own way) on down.  32 / 8 heads of 128, split and not: one
-  // query, 16000 keys 30 and 218 us, 1100 keys 18 and 24; 128 queries behind 4000
-  // keys 29 and 64; 9 x 13 behind 3506 38 and 58; 512 behind 4000 61 and 75, behind
-  // 1000 (not split) 38 and 33.
-  const double way = 0.6 * (double)tiles, sums = (double)total_q * n_heads * head_dim * 8.0 / 6e6;
-  const uint64_t parts = std::min<uint64_t>({512u / all, tiles / 4u, 32u, (uint64_t)std::sqrt(way / sums)});
+  // a share of n less (0.6, 0.8, 0.9 us a tile at head dimension 64, 96, 128; the
+  // longest of several sequences is taken to be half longer than the average,
+  // which is all the host knows), the sums of all rows are written and read n
+  // times (about 6 bytes a picosecond), and the second kernel takes some 6 us.
+  // The n with the least of both, from 4 tiles a part and 32 parts (the second
+  // kernel's own way) on down.  32 / 8 heads of 128, split and not: one query,
+  // 16000 keys 30 and 218 us, 1100 keys 17 and 24; 128 queries behind 4000 keys 30
+  // and 64; 9 x 13 behind 3506 37 and 57; 512 behind 4000 55 and 75, behind 1000
+  // (not split) 38 and 33; 6 of up to 45 queries behind up to 3664 keys 27 and 57.
+  // The guess is off for 12 x 20 behind 1300: 30 and 27.
+  const double way = (0.3 + 0.005 * head_dim) * (n_seq > 1u ? 1.5 : 1.0) * (double)tiles;
+  const double sums = (double)total_q * n_heads * head_dim * 8.0 / 6e6;
+  uint64_t parts = std::min<uint64_t>({512u / all, tiles / 4u, 32u, (uint64_t)std::sqrt(way / sums)});
+  if (parts > 8u) parts &= ~7ull;   // the second kernel reads eight at once: 9 parts 28 us where 8 take 26
   if (parts > 1u && way - way / (double)parts > 6.0 + sums * (double)parts) g.parts = (uint32_t)parts;
   return g;
 }
