@@ -553,7 +553,7 @@ static entro_status launch_prompt(PromptArg &a, const PromptGrid &g, hipStream_t
   // follow in the same order: the first ones' order is turned around, so that
   // the CUs with the least of them to do get the most of the rest.
   a.turned = a.parts == 1u && g.items * g.slots <= 512u ? 256u / g.slots : 0u;
-  a.part_ml = reinterpret_cast<f32x2 *>(a.part_o + (uint64_t)a.parts * a.total_q * a.n_heads * D);
+  if (a.parts > 1u) a.part_ml = reinterpret_cast<f32x2 *>(a.part_o + (uint64_t)a.parts * a.total_q * a.n_heads * D);
   (void)hipGetLastError();
   hipLaunchKernelGGL((attn_prompt_kernel<T, D>), grid2(g.slots, g.items * a.parts), dim3(256), 0, s, a);
   if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;

@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -63,7 +64,8 @@ entro_rows rows(const at::Tensor &x, const char *what, at::ScalarType type, int6
 
 void *ints(const at::Tensor &x, const char *what, int64_t n) {
   if (x.scalar_type() != at::kInt || x.dim() != 1 || x.size(0) != n || !x.is_cuda() || (n > 1 && !x.is_contiguous()))
-    refuse(what, ": ", n, " contiguous int32 values on the GPU expected, got ", x.scalar_type(), " ", x.sizes(), " on ", x.device());
+    refuse(what, ": ", n, " contiguous int32 values on the GPU expected, got ", x.scalar_type(), " ", x.sizes(), " on ",
+           x.device());
   return x.data_ptr();
 }
 
@@ -146,6 +148,7 @@ PyObject *prompt(Args a) {
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
   const at::Tensor &cu_q = tensor(a[3], "cu_q"), &cu_k = tensor(a[4], "cu_k"), &status = tensor(a[5], "status");
   const On on{a[9] == Py_True, a[10]};
+  const c10::DeviceGuard guard(q.device());
   if (cu_q.dim() != 1 || cu_q.size(0) < 1 || q.dim() != 3 || k.dim() != 3)
     refuse("q, k, v are [rows][heads][dim], cu_q and cu_k hold n + 1 sums");
   const int64_t n = cu_q.size(0) - 1, heads = q.size(1), dim = q.size(2), kv = k.size(1);
@@ -189,6 +192,7 @@ PyObject *prompt(Args a) {
 template <typename Fn, typename A>
 void kv_call(Fn fn, A p, const char *name, const entro_kv_cache &c, const at::Tensor &k, const at::Tensor &v,
              const at::Tensor &table, const at::Tensor &status, const On &on) {
+  const c10::DeviceGuard guard(k.device());
   const entro_kv_table t = table_of(table, table.dim() ? table.size(0) : 0);
   p.k = rows(k, "k", k.scalar_type(), c.n_kv_heads, c.head_dim);
   p.v = rows(v, "v", k.scalar_type(), c.n_kv_heads, c.head_dim);
@@ -244,6 +248,7 @@ PyObject *cache(Args a) {
   const at::Tensor &q = tensor(a[0], "q"), &lens = tensor(a[3], "lens"), &status = tensor(a[4], "status");
   const entro_kv_cache c = cache_of(a[1]);
   const On on{a[8] == Py_True, a[9]};
+  const c10::DeviceGuard guard(q.device());
   if (q.dim() != 3) refuse("q is [sequences][heads][dim]");
   const int64_t n = q.size(0), heads = q.size(1), dim = q.size(2);
   if (dim != c.head_dim) refuse("q has head dimension ", dim, ", the cache ", c.head_dim);

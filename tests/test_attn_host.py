@@ -150,6 +150,16 @@ def test_python_refusals():
         ent.KVCache.empty(2, 1, 64, 16, device="cpu")
     with pytest.raises(ValueError, match="four"):
         ent.KVCache(x, x, x, x)
+    with pytest.raises(ValueError, match="tensor"):
+        ent.attn_prompt([1.0], x, x, cu, cu, cu[:2])
+    with pytest.raises(ValueError, match="GPU"):
+        ent.attn_prompt(x, x, x, cu, cu, cu[:2])
+    with pytest.raises(ValueError, match="bfloat16 or float16"):
+        ent.attn_prompt(x.float(), x.float(), x.float(), cu, cu, cu[:2], out=x)
+    with pytest.raises(ValueError, match="do not belong together"):
+        ent.KVCache(x[None], x[None], x[0], x[0])
+    with pytest.raises(AttributeError):
+        ent.kv_store(None, x, x, cu, cu, cu, cu)
     assert ent.FLAGS["length"] == 0x40 and ent.FLAGS["page"] == 0x80
 
 
