@@ -465,9 +465,14 @@ static uint32_t cache_shares(uint32_t n_kv, uint32_t parts, uint32_t head_dim) {
 
 template <entro_dtype T, int D>
 static entro_status launch_cache(CacheArg &a, hipStream_t s) {
-  // where no sequence is longer than the least share: a workgroup each, nothing to join
+  // Where no sequence can be long, a workgroup each and nothing to join: the
+  // second kernel and its launch cost more than some rounds of the wavefronts
+  // (12 sequences of up to 393 tokens, 32 / 8 heads of 128, 16 us with and 8 us
+  // without; one of 1000 14 and 10; 16 of up to 1000 17 and 12; one of 2000 14 and
+  // 16).  With more workgroups than run at once the longest come on top: 64 of up
+  // to 800 tokens, 32 heads of 96, 39 and 37, up to 1000 35 and 46.
   const uint64_t tiles = (((uint64_t)a.table_pages << a.page_log2) + kTile - 1u) / kTile;
-  const bool split = tiles > kShareTiles;
+  const bool split = tiles > ((uint64_t)a.n_seq * a.n_kv * a.parts <= shares_at(D) ? 24u : 12u);
   a.part_ml = reinterpret_cast<f32x2 *>(a.part_o + ((uint64_t)a.n_seq + a.shares) * a.n_heads * D);
   if (!split) a.shares = 0;
   (void)hipGetLastError();

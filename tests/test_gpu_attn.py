@@ -586,6 +586,49 @@ def test_cache_attention_many_sequences(ent):
     run_cache(ent, (2, 1, 64), "f16", 32, [(37 * i) % 700 for i in range(200)], check=range(0, 200, 9))
 
 
+@pytest.mark.parametrize("heads", [(2, 1, 64), (6, 3, 96), (8, 2, 128)])
+def test_cache_attention_many_sequences_split(ent, heads):
+    """More than 64 sequences, one long enough to be split; again with few
+    workgroups."""
+    say(f"cache attention: 130 sequences, split, {heads}")
+    lens = [(53 * i) % 400 for i in range(129)] + [1700]
+    run_cache(ent, heads, "bf16", 64, lens, check=[0, 1, 63, 64, 65, 77, 128, 129])
+    old = ent.set_max_workgroups(7)
+    try:
+        run_cache(ent, heads, "f16", 32, lens, check=[0, 1, 63, 64, 65, 77, 128, 129])
+    finally:
+        ent.set_max_workgroups(old)
+
+
+def test_cache_attention_split_graph_replays(ent):
+    say("cache attention: graph replay of split sequences")
+    kv, d, page = 2, 128, 64
+    c = filled_cache(ent, kv, d, page, 70, 6)
+    t = torch.from_numpy(make_table([3000, 500], page, 70, 0)).cuda()
+    lens, status = ints([2900, 480]), torch.zeros(2, dtype=torch.int32, device="cuda")
+    q = torch.zeros(2, 8, d, device="cuda", dtype=torch.bfloat16)
+    out = torch.empty_like(q)
+    work = torch.empty(ent.attn_cache_work_bytes(2, 8, kv, d), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ent.attn_cache(q, c, t, lens, status, out=out, work=work)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ent.attn_cache(q, c, t, lens, status, out=out, work=work)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    for _ in range(4):
+        q.copy_(torch.randn(q.shape, device="cuda", generator=g))
+        graph.replay()
+        got = out.clone()
+        want = ent.attn_cache(q, c, t, lens, status)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        lens += 7
+    assert not status.any()
+
+
 def test_cache_attention_hidden_places(ent):
     """Scales of pages no token lies in, and codes behind the last token."""
     say("cache attention: hidden places")
