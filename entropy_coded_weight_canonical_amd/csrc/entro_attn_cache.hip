@@ -11,6 +11,7 @@ constexpr uint32_t kTile = 64;          // tokens a wavefront takes at a time
 constexpr uint32_t kCacheWaves = 4;     // wavefronts per workgroup, interleaved over its tiles
 constexpr uint32_t kHeadsPerWg = 16;    // query heads of one key/value head (columns of the matrix products)
 constexpr uint32_t kShareTiles = 4;     // least tiles of a workgroup's share
+constexpr float kFloatMax = 3.40282347e38f;
 
 // Shares of a call, all heads together: the workgroups that 256 CUs hold at
 // once by the kernel's registers, two on each at head dimension 128 and three
@@ -34,7 +35,7 @@ struct CacheArg {
   uint32_t shares;              // that the tokens of a key/value head are split into at most; 0: one sequence each
   float scale;                  // times log2(e)
   float *part_o;                // [n_seq + shares][n_heads][D]
-  f32x2 *part_ml;               // [n_seq + shares][n_heads]: maximum, sum
+  f32x2 *part_ml;               // [n_seq + shares][n_heads]: the output's exponent, the weights' sum (logarithms)
   uint32_t *status;
 };
 
@@ -111,6 +112,31 @@ __device__ __forceinline__ f16v8 half8(uint32_t w0, uint32_t w1) {
   return __builtin_bit_cast(f16v8, (u32x4){a.x, a.y, b.x, b.y});
 }
 
+// A piece of a head's tokens, or several, in powers of two: `o`, the exponent of
+// its outputs (times 2^15, see below), and `w`, the logarithm of its softmax's
+// sum.  Both -inf without tokens (o also where all values are zero); w is NaN
+// where the result is.  The two are apart by the values' size, which may be
+// anything: neither is taken relative to the other before the end.
+struct Joined {
+  float o, w;
+  __device__ void raise(f32x2 part) {
+    o = fmaxf(o, part.x);
+    w = fmaxf(w, part.y);
+  }
+};
+// What outputs relative to 2^o, with weights that sum to `sum` relative to 2^w,
+// are multiplied by.
+struct Factor {
+  float r;
+  int e;
+  __device__ Factor(Joined j, float sum) {
+    const float up = fminf(fmaxf(j.o - j.w, -512.0f), 512.0f), whole = floorf(up);
+    r = j.w == -INFINITY && sum == sum ? 0.0f : exp2_fast(up - whole) / sum;
+    e = (int)whole - 15;
+  }
+  __device__ float of(float x) const { return ldexpf(x * r, e); }
+};
+
 __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
@@ -132,11 +158,20 @@ __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
 // from its start.
 //
 // Codes become f16 exactly; q is brought to f16 by a power of two (exact but
-// for values 2^-24 below the row's largest).  With t = s + log2(value scale)
-// and M its running maximum, weights are held as 2^(t - M + 15): the scale of
-// a page's values rides in the exponent, and f16 covers weights down to 2^-29
-// of the largest with 11 bits.  The sum of the softmax is of the same numbers
-// before rounding, divided by the value scale, in 32 bits.
+// for values below 2^-17 of the row's largest, which are rounded at 2^-25 of it).
+// With t = s + log2(value scale) and M its running maximum, weights go into the
+// product as 2^(t - M + 15): the scale of a page's values rides in the exponent,
+// and f16 covers weights down to 2^-29 of the largest with 11 bits.
+//
+// A page's scale may be anything from 0 (values all zero) to the type's largest,
+// so the softmax's sum has a maximum of its own, of the scores s alone, for each
+// lane (16 tokens of a tile, all of one page).  A lane's weights of a tile are
+// computed once, as 2^(s - base): base = M - log2(scale) - 15 makes them those of
+// the product; where the page's scale is so small against M that they would be
+// below 2^-64, base = (largest s) + 64 keeps them for the sum, and f16 takes them
+// as the zeros they are in the product.  The sum is of the weights before
+// rounding, in 32 bits, brought from base to the lane's maximum by one factor a
+// tile.  Lanes, wavefronts and pieces are joined by the logarithms of their sums.
 //
 // Bound by the reading of the cache: 131072 tokens of one sequence (32 / 8 heads
 // of 128) 44 us, 6.1 TB/s, which is what a kernel that only reads reaches; 64
@@ -246,7 +281,8 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
         f32x4 o[DT];
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-        float m = -INFINITY, l = 0.0f;   // l: this lane's tokens only
+        float m = -INFINITY;                     // of score + log2(value scale)
+        float top = -kFloatMax, l = 0.0f;        // of the scores, and the weights' sum: this lane's tokens only
         bool bad = false;
 
         // Pages of the 16-token blocks that this lane reads keys of (n / 4) and
@@ -287,7 +323,7 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
           const uint64_t av = (uint64_t)(v_bad ? 0u : (uint32_t)now.v) * a.n_kv + kvh;
           const int8_t *vp = a.v_codes + ((av * D + n) << a.page_log2) + (tv & (page - 1u));
           const float ks = a.k_scales[av] * c;   // rows 4 g + r of the products are tokens of block g
-          const float vs = fmaxf(a.v_scales[av], 1.17549435e-38f);
+          const float v_scale = a.v_scales[av];
 #pragma unroll
           for (int d = 0; d < DT; ++d) vq[d] = *reinterpret_cast<const u32x4 *>(vp + ((uint64_t)(16 * d) << a.page_log2));
 
@@ -304,27 +340,27 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
           }
           if (more) keys(tile + kCacheWaves, next.k);
           now = next;
-          // scores in powers of two, with the value scale's logarithm
-          const float lv = __log2f(vs), iv = 1.0f / vs;
+          // scores in powers of two; tokens that are not seen are of value scale 0
           const uint32_t seen = v_bad || tv >= len ? 0u : min(16u, len - tv);
+          const float vs = seen ? v_scale : 0.0f, lv = __log2f(vs);
           float mx = -INFINITY;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             for (int r = 0; r < 4; ++r) {
-              const float t = (uint32_t)(4 * i + r) < seen ? s4[i][r] * ks + lv : -INFINITY;
+              const float t = (uint32_t)(4 * i + r) < seen ? s4[i][r] * ks : -INFINITY;
               s4[i][r] = t;
               mx = fmaxf(mx, t);
             }
-          mx = max32(max16(mx));
-          if (__any(mx > m)) {
-            const float mn = fmaxf(m, mx);
+          const float mt = max32(max16(mx + lv));
+          if (__any(mt > m)) {
+            const float mn = fmaxf(m, mt);
             const float k = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
             m = mn;
-            l *= k;
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[d] *= k;
           }
-          const float off = m == -INFINITY ? 0.0f : m - 15.0f;
+          mx = fmaxf(mx, -kFloatMax);
+          const float base = fminf(m - lv - 15.0f, mx + 64.0f);   // (inf - inf counts as no limit)
           float sum = 0.0f;
           u32x4 pw[2];
 #pragma unroll
@@ -332,13 +368,15 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
             float p[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              p[r] = exp2_fast(s4[i][r] - off);
+              p[r] = exp2_fast(s4[i][r] - base);
               sum += p[r];
             }
             pw[i >> 1][2 * (i & 1)] = Elem<ENTRO_F16>::pack2(p[0], p[1]);
             pw[i >> 1][2 * (i & 1) + 1] = Elem<ENTRO_F16>::pack2(p[2], p[3]);
           }
-          l += seen ? sum * iv : 0.0f;
+          const float up = fmaxf(top, mx);
+          l = l * exp2_fast(top - up) + sum * exp2_fast(base - up) + vs * 0.0f;   // NaN where the scale is no number
+          top = up;
           const f16v8 p0 = __builtin_bit_cast(f16v8, pw[0]), p1 = __builtin_bit_cast(f16v8, pw[1]);
 #pragma unroll
           for (int d = 0; d < DT; ++d) {
@@ -347,35 +385,35 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
           }
         }
         if (bad) atomicOr(a.status + seq, ENTRO_F_PAGE);
-        l = add32(add16(l));
-
-        // join the wavefronts
-        if (g == 0u) red_ml[wave][n] = (f32x2){m, l};
+        // join the lanes, then the wavefronts
+        const float wave_top = max32(max16(top));
+        l = add32(add16(l * exp2_fast(top - wave_top)));
+        if (g == 0u) red_ml[wave][n] = (f32x2){m, wave_top + __log2f(l)};
 #pragma unroll
         for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(&red_o[wave][n][16 * d + 4 * g]) = o[d];
         __syncthreads();
         const bool whole = t1 - t0 == all_tiles;
         for (uint32_t i = tid; i < heads * (D / 2u); i += 256u) {
           const uint32_t h = i / (D / 2u), d = i % (D / 2u) * 2u;
-          float mm = -INFINITY;
+          Joined j{-INFINITY, -INFINITY};
 #pragma unroll
-          for (uint32_t v = 0; v < kCacheWaves; ++v) mm = fmaxf(mm, red_ml[v][h].x);
-          float x = 0.0f, y = 0.0f, ll = 0.0f;
+          for (uint32_t v = 0; v < kCacheWaves; ++v) j.raise(red_ml[v][h]);
+          float x = 0.0f, y = 0.0f, sum = 0.0f;
 #pragma unroll
           for (uint32_t v = 0; v < kCacheWaves; ++v) {
-            const float k = join_factor(red_ml[v][h].x, mm);
+            const float k = join_factor(red_ml[v][h].x, j.o);
             x += k * red_o[v][h][d];
             y += k * red_o[v][h][d + 1u];
-            ll += k * red_ml[v][h].y;
+            sum += join_factor(red_ml[v][h].y, j.w);
           }
           if (whole) {
-            const float r = ll > 0.0f ? 1.0f / ll : ll == 0.0f ? 0.0f : ll;   // NaN stays
+            const Factor f(j, sum);
             *reinterpret_cast<uint32_t *>(a.out + seq * a.o_t + (int64_t)(head0 + h) * a.o_h + d * 2u) =
-                Elem<T>::pack2(x * r, y * r);
+                Elem<T>::pack2(f.of(x), f.of(y));
           } else {
             const uint64_t at = ((uint64_t)w + seq) * a.n_heads + head0 + h;
             *reinterpret_cast<f32x2 *>(a.part_o + at * D + d) = (f32x2){x, y};
-            if (d == 0u) a.part_ml[at] = (f32x2){mm, ll};
+            if (d == 0u) a.part_ml[at] = (f32x2){j.o, j.w + __log2f(sum)};
           }
         }
         __syncthreads();
@@ -408,47 +446,48 @@ __global__ __launch_bounds__(64 * G) void attn_join_kernel(CacheArg a) {
       const f32x2 *ml = a.part_ml + at;
       const float *po = a.part_o + at * D;
       const uint32_t d = min(lane * 2u, D - 2u);
-      float m = -INFINITY, x = 0.0f, y = 0.0f, l = 0.0f;
+      Joined j{-INFINITY, -INFINITY};
+      float x = 0.0f, y = 0.0f, sum = 0.0f;
       for (uint32_t i0 = group; i0 < n; i0 += 4u * G) {
         f32x2 v[4], p[4];
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-          const uint64_t i = min(i0 + (uint32_t)G * j, n - 1u);
-          v[j] = ml[i * a.n_heads];
-          p[j] = *reinterpret_cast<const f32x2 *>(po + i * a.n_heads * D + d);
+        for (uint32_t c = 0; c < 4; ++c) {
+          const uint64_t i = min(i0 + (uint32_t)G * c, n - 1u);
+          v[c] = ml[i * a.n_heads];
+          p[c] = *reinterpret_cast<const f32x2 *>(po + i * a.n_heads * D + d);
         }
-        float mn = m;
+        Joined up = j;
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) mn = fmaxf(mn, v[j].x);
-        float k = join_factor(m, mn);
+        for (uint32_t c = 0; c < 4; ++c) up.raise(v[c]);
+        const float k = join_factor(j.o, up.o);
         x *= k;
         y *= k;
-        l *= k;
-        m = mn;
+        sum *= join_factor(j.w, up.w);
+        j = up;
 #pragma unroll
-        for (uint32_t j = 0; j < 4; ++j) {
-          if (i0 + (uint32_t)G * j >= n) break;
-          k = join_factor(v[j].x, m);
-          x += k * p[j].x;
-          y += k * p[j].y;
-          l += k * v[j].y;
+        for (uint32_t c = 0; c < 4; ++c) {
+          if (i0 + (uint32_t)G * c >= n) break;
+          const float kc = join_factor(v[c].x, j.o);
+          x += kc * p[c].x;
+          y += kc * p[c].y;
+          sum += join_factor(v[c].y, j.w);
         }
       }
       if (lane * 2u < D) *reinterpret_cast<f32x2 *>(&red_o[group][d]) = (f32x2){x, y};
-      if (lane == 0u) red_ml[group] = (f32x2){m, l};
+      if (lane == 0u) red_ml[group] = (f32x2){j.o, sum == 0.0f ? -INFINITY : j.w + __log2f(sum)};   // a group without pieces
       __syncthreads();
       if (group == 0u && lane * 2u < D) {
-        m = -INFINITY;
-        x = y = l = 0.0f;
-        for (int g = 0; g < G; ++g) m = fmaxf(m, red_ml[g].x);
+        j = Joined{-INFINITY, -INFINITY};
+        x = y = sum = 0.0f;
+        for (int g = 0; g < G; ++g) j.raise(red_ml[g]);
         for (int g = 0; g < G; ++g) {
-          const float k = join_factor(red_ml[g].x, m);
+          const float k = join_factor(red_ml[g].x, j.o);
           x += k * red_o[g][d];
           y += k * red_o[g][d + 1u];
-          l += k * red_ml[g].y;
+          sum += join_factor(red_ml[g].y, j.w);
         }
-        const float r = l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l;
-        *reinterpret_cast<uint32_t *>(a.out + b * a.o_t + head * a.o_h + d * 2u) = Elem<T>::pack2(x * r, y * r);
+        const Factor f(j, sum);
+        *reinterpret_cast<uint32_t *>(a.out + b * a.o_t + head * a.o_h + d * 2u) = Elem<T>::pack2(f.of(x), f.of(y));
       }
       __syncthreads();   // red_o and red_ml are written again
     }
