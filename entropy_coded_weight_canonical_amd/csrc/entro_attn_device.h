@@ -113,20 +113,23 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
   v += dpp0<0x143, 0xC>(v);   // row_bcast:31 into rows 2 and 3
   return v;
 }
-__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+__device__ __forceinline__ uint32_t wave_max_scan(uint32_t v) {
   v = max(v, dpp0<0x111, 0xF>(v));
   v = max(v, dpp0<0x112, 0xF>(v));
   v = max(v, dpp0<0x114, 0xF>(v));
   v = max(v, dpp0<0x118, 0xF>(v));
   v = max(v, dpp0<0x142, 0xA>(v));
   v = max(v, dpp0<0x143, 0xC>(v));
-  return __builtin_amdgcn_readlane(v, 63);
+  return v;
 }
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) { return __builtin_amdgcn_readlane(wave_max_scan(v), 63); }
 
-// The sequence whose items include number `item` when the sequences' items
-// (count(b) of them) are numbered one after another, and the item's number
-// within it.  Every lane of the wavefront returns the same; seq = n_seq where
-// there are fewer items.  64 sequences a step.
+// The sequence whose items include number `item` when the sequences' items are
+// numbered one after another, and the item's number within it.  Every lane of the
+// wavefront returns the same; seq = n_seq where there are fewer items.  64
+// sequences a step: count(b0) is the number of items of sequence b0 + lane (0 past
+// the last), b0 = 0, 64, ... in turn, all lanes active; all of them together are
+// below 2^32.
 struct Found {
   uint32_t seq, local;
 };
@@ -134,8 +137,7 @@ template <typename Count>
 __device__ __forceinline__ Found find_item(uint32_t item, uint32_t n_seq, uint32_t lane, Count count) {
   uint32_t before = 0;
   for (uint32_t b0 = 0; b0 < n_seq; b0 += 64u) {
-    const uint32_t b = b0 + lane;
-    const uint32_t own = b < n_seq ? count(b) : 0u;
+    const uint32_t own = count(b0);
     const uint32_t run = wave_scan(own);
     const uint64_t past = __ballot(before + run > item);
     if (past) {
@@ -149,10 +151,9 @@ __device__ __forceinline__ Found find_item(uint32_t item, uint32_t n_seq, uint32
 
 // All sequences' items together.
 template <typename Count>
-__device__ __forceinline__ uint32_t count_items(uint32_t n_seq, uint32_t lane, Count count) {
+__device__ __forceinline__ uint32_t count_items(uint32_t n_seq, Count count) {
   uint32_t sum = 0;
-  for (uint32_t b0 = 0; b0 < n_seq; b0 += 64u)
-    sum += __builtin_amdgcn_readlane(wave_scan(b0 + lane < n_seq ? count(b0 + lane) : 0u), 63);
+  for (uint32_t b0 = 0; b0 < n_seq; b0 += 64u) sum += __builtin_amdgcn_readlane(wave_scan(count(b0)), 63);
   return sum;
 }
 
@@ -166,6 +167,29 @@ __device__ __forceinline__ Span span_of(const int32_t *cu, uint32_t b, uint32_t 
   const bool ok = lo >= 0 && hi >= lo && (uint32_t)hi <= total;
   return {ok ? (uint32_t)lo : 0u, ok ? (uint32_t)(hi - lo) : 0u, ok};
 }
+
+// Rows of the sequences b0 + lane (b0 = 0, 64, ... in turn, all lanes active) that
+// are written or taken as new: no row belongs to two sequences, so one that begins
+// before an earlier one's end is wrong, and the rows of all others together are no
+// more than there are (which bounds the items that are counted from them).
+struct Spans {
+  const int32_t *cu;
+  uint32_t total, n_seq, lane, end;   // end: the largest sum so far
+  __device__ Spans(const int32_t *sums, uint32_t rows, uint32_t n, uint32_t lane_)
+      : cu(sums), total(rows), n_seq(n), lane(lane_), end(0u) {}
+  // b0 + lane or, past the last sequence, the last: what is read of it without a
+  // branch is on its way together with what else the caller reads
+  __device__ uint32_t place(uint32_t b0) const { return min(b0 + lane, n_seq - 1u); }
+  __device__ Span at(uint32_t b0) {
+    if (b0 == 0u) end = 0u;
+    const uint32_t b = place(b0);
+    const uint32_t lo = (uint32_t)cu[b], hi = (uint32_t)cu[b + 1u];   // negative: past all rows
+    const uint32_t run = max(end, wave_max_scan(lo <= total ? lo : 0u));
+    end = __builtin_amdgcn_readlane(run, 63);
+    const bool ok = b0 + lane < n_seq && lo <= hi && hi <= total && lo >= run;
+    return {ok ? lo : 0u, ok ? hi - lo : 0u, ok};
+  }
+};
 
 // Workgroup cap of the attention's and cache's launches
 // (entro_attn_set_max_workgroups; 0: none).

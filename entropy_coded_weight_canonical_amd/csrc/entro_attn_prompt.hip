@@ -154,9 +154,12 @@ attn_prompt_kernel(PromptArg a) {
   __shared__ uint32_t lds_special[2];
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = rfl(tid >> 6), n = lane & 31u, half = lane >> 5;
   const uint32_t rows = kQueries * kWaves4 / a.heads;   // queries of a workgroup
-  if (blockIdx.x == 0u && blockIdx.y == 0u)
-    for (uint32_t b = tid; b < a.n_seq; b += 256u)
-      if (!span_of(a.cu_q, b, a.total_q).ok || !span_of(a.cu_k, b, a.total_k).ok) atomicOr(a.status + b, ENTRO_F_LENGTH);
+  Spans spans(a.cu_q, a.total_q, a.n_seq, lane);
+  if (blockIdx.x == 0u && blockIdx.y == 0u && wave == 0u)
+    for (uint32_t b0 = 0; b0 < a.n_seq; b0 += 64u) {
+      const Span k = span_of(a.cu_k, spans.place(b0), a.total_k), s = spans.at(b0);
+      if (b0 + lane < a.n_seq && !(s.ok && k.ok)) atomicOr(a.status + b0 + lane, ENTRO_F_LENGTH);
+    }
 
   // this lane's part of a tile's copies: N pieces of keys and N of values
   uint32_t k_off[N], v_off[N];
@@ -167,13 +170,13 @@ attn_prompt_kernel(PromptArg a) {
     v_off[s] = r * (uint32_t)a.v_t + value_piece<D>(r, c) * 16u;
   }
 
-  Span lq{}, lk{};                 // of the sequence this lane looked at last
-  auto items = [&](uint32_t b) {   // workgroups of sequence b for a key/value head
-    lq = span_of(a.cu_q, b, a.total_q);
-    lk = span_of(a.cu_k, b, a.total_k);
+  Span lq{}, lk{};                  // of the sequence this lane looked at last
+  auto items = [&](uint32_t b0) {   // workgroups of sequence b0 + lane for a key/value head
+    lk = span_of(a.cu_k, spans.place(b0), a.total_k);
+    lq = spans.at(b0);
     return lk.ok ? (lq.count + rows - 1u) / rows : 0u;
   };
-  const uint32_t turned = a.turned ? min(a.turned, count_items(a.n_seq, lane, items)) : 0u;
+  const uint32_t turned = a.turned ? min(a.turned, count_items(a.n_seq, items)) : 0u;
   for (uint32_t slot = blockIdx.x; slot < a.n_heads / a.heads; slot += gridDim.x)
     for (uint32_t y = blockIdx.y;; y += gridDim.y) {
       const uint32_t at = y / a.parts, share = y % a.parts;
@@ -462,9 +465,10 @@ __global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArg a) {
   constexpr uint32_t L = D / 4u, R = 256u / L, kBatch = 8u;
   const uint32_t tid = threadIdx.x, lane = tid & 63u, d = tid % L * 4u;
   Span lq{}, lk{};
-  auto items = [&](uint32_t b) {
-    lq = span_of(a.cu_q, b, a.total_q);
-    lk = span_of(a.cu_k, b, a.total_k);
+  Spans spans(a.cu_q, a.total_q, a.n_seq, lane);
+  auto items = [&](uint32_t b0) {
+    lk = span_of(a.cu_k, spans.place(b0), a.total_k);
+    lq = spans.at(b0);
     return lk.ok ? (lq.count + R - 1u) / R : 0u;
   };
   for (uint32_t head = blockIdx.x; head < a.n_heads; head += gridDim.x)

@@ -33,9 +33,10 @@ struct KvSpan {
   uint32_t begin, count, pos;
   bool ok;
 };
-__device__ __forceinline__ KvSpan kv_span(const KvArg &a, uint32_t b, uint32_t page) {
-  const Span s = span_of(a.cu, b, a.total);
-  const int32_t p = a.pos[b];
+// of sequence b0 + lane, 64 in turn
+__device__ __forceinline__ KvSpan kv_span(const KvArg &a, Spans &spans, uint32_t b0, uint32_t page) {
+  const int32_t p = a.pos[spans.place(b0)];
+  const Span s = spans.at(b0);
   const bool ok = s.ok && p >= 0 && (uint64_t)p + s.count <= (uint64_t)a.table_pages * page;
   return {s.begin, ok ? s.count : 0u, ok ? (uint32_t)p : 0u, ok};
 }
@@ -43,10 +44,14 @@ __device__ __forceinline__ uint32_t kv_pages(const KvSpan &s, uint32_t page) {
   return s.count ? (s.pos + s.count - 1u) / page - s.pos / page + 1u : 0u;
 }
 
-// Marks the sequences whose lengths do not fit (one workgroup of the call).
+// Marks the sequences whose lengths do not fit (one wavefront of the call).
 __device__ __forceinline__ void kv_check(const KvArg &a, uint32_t page) {
-  for (uint32_t b = threadIdx.x; b < a.n_seq; b += blockDim.x)
-    if (!kv_span(a, b, page).ok) atomicOr(a.status + b, ENTRO_F_LENGTH);
+  if (threadIdx.x >= 64u) return;
+  Spans spans(a.cu, a.total, a.n_seq, threadIdx.x);
+  for (uint32_t b0 = 0; b0 < a.n_seq; b0 += 64u) {
+    const bool ok = kv_span(a, spans, b0, page).ok;
+    if (b0 + threadIdx.x < a.n_seq && !ok) atomicOr(a.status + b0 + threadIdx.x, ENTRO_F_LENGTH);
+  }
 }
 
 // What a workgroup does: one page (the sequences' pages that take part are
@@ -63,8 +68,9 @@ struct KvItem {
 __device__ __forceinline__ KvItem kv_item(const KvArg &a, uint32_t page, uint32_t item, uint32_t head, uint32_t lane) {
   KvItem it{};
   KvSpan own{};   // of the sequence this lane looked at last
-  const Found f = find_item(item, a.n_seq, lane, [&](uint32_t b) {
-    own = kv_span(a, b, page);
+  Spans spans(a.cu, a.total, a.n_seq, lane);
+  const Found f = find_item(item, a.n_seq, lane, [&](uint32_t b0) {
+    own = kv_span(a, spans, b0, page);
     return kv_pages(own, page);
   });
   if (f.seq == a.n_seq) return it;

@@ -53,8 +53,10 @@ extern "C" {
 typedef enum { ENTRO_BF16 = 0, ENTRO_F16 = 1 } entro_dtype;
 
 /* Per-sequence faults OR-ed into d_status[b]. */
-#define ENTRO_F_LENGTH 0x40u /* running sums not ascending within the stated rows, a
-                                negative position, or tokens past the table's row     */
+#define ENTRO_F_LENGTH 0x40u /* running sums not ascending within the stated rows (one
+                                that begins before an earlier sequence's end among
+                                them; keys of a prompt may be shared), a negative
+                                position, or tokens past the table's row              */
 #define ENTRO_F_PAGE 0x80u   /* a page index outside the cache where tokens lie; the
                                 page is skipped                                       */
 
