@@ -20,6 +20,7 @@ struct PromptArg {
   float *part_o;                                    // parts > 1: [parts][total_q][n_heads][D]
   f32x2 *part_ml;                                   // [parts][total_q][n_heads]: maximum in powers of two, sum
   float scale;                                      // magnitude, times log2(e); 1 where the scale is 0
+  float lift;                                       // see lift_of
   uint32_t q_and, q_xor;                            // on a pair of q: the scale's sign, and 0 where the scale is 0
   uint32_t *status;
 };
@@ -27,15 +28,20 @@ struct PromptArg {
 constexpr uint32_t kTile = 64;     // keys of a step
 constexpr uint32_t kWaves4 = 4;    // wavefronts of a workgroup
 
-// Weights are held as 2^(score - maximum + kLift), the maximum being behind by
+// Weights are held as 2^(score - maximum + lift), the maximum being behind by
 // at most kLag (in powers of two): raising it means a pass over the outputs,
 // and most tiles raise it by little.  f16 has 11 bits down to 2^-14 only, and
 // many small weights can outweigh the largest together: its weights go up to
-// 2^15, so that those down to 2^-26 of the largest have all their bits.
-template <entro_dtype T>
-constexpr float kLift = T == ENTRO_F16 ? 12.0f : 0.0f;
+// 2^15, so that those down to 2^-26 of the largest have all their bits.  bf16 has
+// all its bits down to 2^-126, and values up to the 32-bit sums' own largest: its
+// weights are held so small that those of all keys are at most 1 together, and the
+// sums stay finite wherever the values are.
 template <entro_dtype T>
 constexpr float kLag = T == ENTRO_F16 ? 3.0f : 8.0f;
+template <entro_dtype T>
+static float lift_of(uint32_t total_k) {
+  return T == ENTRO_F16 ? 12.0f : -kLag<T> - std::ceil(std::log2((float)std::max(total_k, 1u)));
+}
 
 // The 16-bit values of w that are infinite or NaN: 0x8000 in their places.
 template <entro_dtype T>
@@ -312,7 +318,7 @@ attn_prompt_kernel(PromptArg a) {
       };
       // Outputs of a tile; kept(w): w, or what is left of it.
       auto outputs = [&](const f32x16 (&s)[2], const u32x4 *vt, uint32_t ln, auto kept) {
-        const float off = m == -INFINITY ? 0.0f : kLift<T> - m * a.scale;
+        const float off = m == -INFINITY ? 0.0f : a.lift - m * a.scale;
         u32x4 p[2], w[DT];
         auto pair = [&](int c, int e) {   // weights of keys 16 c + 2 e, 2 e + 1 (in the products' order)
           const float x = exp2_fast(__builtin_fmaf(s[c / 2][c % 2 * 8 + 2 * e], a.scale, off));
@@ -553,6 +559,7 @@ static PromptGrid prompt_grid(uint32_t n_seq, uint32_t total_q, uint32_t total_k
 
 template <entro_dtype T, int D>
 static entro_status launch_prompt(PromptArg &a, const PromptGrid &g, hipStream_t s) {
+  a.lift = lift_of<T>(a.total_k);
   // Where all workgroups run at once, the 256 first get a CU each and the rest
   // follow in the same order: the first ones' order is turned around, so that
   // the CUs with the least of them to do get the most of the rest.

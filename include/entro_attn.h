@@ -116,7 +116,8 @@ uint64_t entro_attn_prompt_work_bytes(uint32_t n_seq, uint32_t total_q, uint32_t
  * statistics; the weights are rounded to the element type for the product
  * with v and for their sum, the result once at the end.  An infinite value
  * that a query sees gives it an infinity or, where its weight is no longer above
- * 0, NaN.  Sequences of any length up to 2^31 - 1 rows; out must not overlap the
+ * 0, NaN.  Finite values of any size give finite results; bf16 values below
+ * 2^-118 * total_k count with fewer bits.  Sequences of any length up to 2^31 - 1 rows; out must not overlap the
  * inputs. */
 entro_status entro_attn_prompt(const entro_attn_prompt_args *a, uint32_t *d_status, hipStream_t stream);
 
