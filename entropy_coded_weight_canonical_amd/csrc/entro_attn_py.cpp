@@ -47,6 +47,16 @@ const at::Tensor &tensor(PyObject *o, const char *what) {
   return THPVariable_Unpack(o);
 }
 
+// All tensors of a call are on the device of the first one that is named (the
+// call's, which the kernels run on), also before anything is read or made.
+struct Together {
+  const at::Device device;
+  const Together &operator()(const char *what, const at::Tensor &x) const {
+    if (x.device() != device) refuse(what, ": on device ", x.device(), ", the call is on ", device);
+    return *this;
+  }
+};
+
 int type_of(const at::Tensor &x) {
   if (x.scalar_type() == at::kBFloat16) return ENTRO_BF16;
   if (x.scalar_type() == at::kHalf) return ENTRO_F16;
@@ -84,11 +94,17 @@ uint32_t small(int64_t n, const char *what) {
   return (uint32_t)n;
 }
 
-// The description of a KVCache (its attribute `desc`, made by cache_desc).
-entro_kv_cache cache_of(PyObject *cache) {
+// A KVCache's attribute `desc`, made by cache_desc: the C ABI's description and
+// the GPU that the tensors are on.
+struct CacheDesc {
+  entro_kv_cache c;
+  int64_t gpu;
+  at::Device device() const { return {at::kCUDA, (at::DeviceIndex)gpu}; }
+};
+CacheDesc cache_of(PyObject *cache) {
   PyObject *desc = PyObject_GetAttr(cache, g.desc);
   if (!desc) throw Raised();
-  entro_kv_cache c{};
+  CacheDesc c{};
   const bool ok = PyBytes_Check(desc) && PyBytes_GET_SIZE(desc) == sizeof c;
   if (ok) std::memcpy(&c, PyBytes_AS_STRING(desc), sizeof c);
   Py_DECREF(desc);
@@ -147,6 +163,11 @@ using Args = PyObject *const *;
 PyObject *prompt(Args a) {
   const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
   const at::Tensor &cu_q = tensor(a[3], "cu_q"), &cu_k = tensor(a[4], "cu_k"), &status = tensor(a[5], "status");
+  at::Tensor out, work;
+  const Together together{q.device()};
+  together("k", k)("v", v)("cu_q", cu_q)("cu_k", cu_k)("status", status);
+  if (a[7] != Py_None) together("out", out = tensor(a[7], "out"));
+  if (a[8] != Py_None) together("work", work = tensor(a[8], "work"));
   const On on{a[9] == Py_True, a[10]};
   const c10::DeviceGuard guard(q.device());
   if (cu_q.dim() != 1 || cu_q.size(0) < 1 || q.dim() != 3 || k.dim() != 3)
@@ -156,13 +177,10 @@ PyObject *prompt(Args a) {
   const at::ScalarType t = q.scalar_type();
   entro_attn_prompt_args p{};
   p.dtype = (entro_dtype)type_of(q);
-  at::Tensor out;
-  if (a[7] == Py_None) {
+  if (!out.defined())
     out = on.empty(q.sizes(), t, q);
-  } else {
-    out = tensor(a[7], "out");
-    if (out.dim() == 3 && out.size(0) != q.size(0)) refuse("out has the rows of q");
-  }
+  else if (out.dim() == 3 && out.size(0) != q.size(0))
+    refuse("out has the rows of q");
   p.out = rows(out, "out", t, heads, dim);
   p.q = rows(q, "q", t, heads, dim);
   p.k = rows(k, "k", t, kv, dim);
@@ -176,10 +194,7 @@ PyObject *prompt(Args a) {
   p.n_kv_heads = small(kv, "k");
   p.head_dim = small(dim, "q");
   p.scale = scale_of(a[6], dim);
-  at::Tensor work;
-  if (a[8] != Py_None) {
-    work = tensor(a[8], "work");
-  } else if (on.make) {   // (without workspace the keys are not split)
+  if (!work.defined() && on.make) {   // (without workspace the keys are not split)
     const uint64_t bytes = g.prompt_bytes(p.n_seq, p.total_q, p.total_k, p.n_heads, p.n_kv_heads, p.head_dim);
     if (bytes) work = on.empty({(int64_t)bytes}, at::kByte, q);
   }
@@ -202,22 +217,29 @@ void kv_call(Fn fn, A p, const char *name, const entro_kv_cache &c, const at::Te
 
 // cache, k, v, table, held, cu_new, status, make, stream
 PyObject *store(Args a) {
-  const entro_kv_cache c = cache_of(a[0]);
+  const CacheDesc desc = cache_of(a[0]);
   const at::Tensor &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &table = tensor(a[3], "table");
+  const at::Tensor &held = tensor(a[4], "held"), &cu_new = tensor(a[5], "cu_new"), &status = tensor(a[6], "status");
   if (k.dim() != 3 || v.dim() != 3 || k.size(0) != v.size(0)) refuse("k and v have the same rows");
+  if (!k.is_cuda()) refuse("k: a tensor on the GPU expected, got ", k.device());
+  Together{desc.device()}("k", k)("v", v)("table", table)("held", held)("cu_new", cu_new)("status", status);
   const int64_t n = table.dim() ? table.size(0) : 0;
   entro_kv_store_args p{};
-  p.d_held = static_cast<int32_t *>(ints(tensor(a[4], "held"), "held", n));
-  p.d_cu_new = static_cast<int32_t *>(ints(tensor(a[5], "cu_new"), "cu_new", n + 1));
+  p.d_held = static_cast<int32_t *>(ints(held, "held", n));
+  p.d_cu_new = static_cast<int32_t *>(ints(cu_new, "cu_new", n + 1));
   p.total_new = small(k.size(0), "k");
-  kv_call(g.store, p, "entro_kv_store", c, k, v, table, tensor(a[6], "status"), {a[7] == Py_True, a[8]});
+  kv_call(g.store, p, "entro_kv_store", desc.c, k, v, table, status, {a[7] == Py_True, a[8]});
   Py_RETURN_NONE;
 }
 
 // cache, table, first, cu_out, total, status, type of the results as f16 or not, k, v, make, stream -> (k, v)
 PyObject *load(Args a) {
-  const entro_kv_cache c = cache_of(a[0]);
-  const at::Tensor &table = tensor(a[1], "table"), &status = tensor(a[5], "status");
+  const CacheDesc desc = cache_of(a[0]);
+  const entro_kv_cache &c = desc.c;
+  const at::Tensor &table = tensor(a[1], "table"), &first = tensor(a[2], "first"), &cu_out = tensor(a[3], "cu_out");
+  const at::Tensor &status = tensor(a[5], "status");
+  const Together together{desc.device()};
+  together("table", table)("first", first)("cu_out", cu_out)("status", status);
   const On on{a[9] == Py_True, a[10]};
   const int64_t n = table.dim() ? table.size(0) : 0, total = PyLong_AsLongLong(a[4]);
   if (total == -1 && PyErr_Occurred()) throw Raised();
@@ -229,12 +251,11 @@ PyObject *load(Args a) {
     k = on.empty({total, c.n_kv_heads, c.head_dim}, t, table);
     v = on.empty({total, c.n_kv_heads, c.head_dim}, t, table);
   } else {
-    k = tensor(a[7], "k");
-    v = tensor(a[8], "v");
+    together("k", k = tensor(a[7], "k"))("v", v = tensor(a[8], "v"));
     if (k.dim() != 3 || v.dim() != 3 || k.size(0) != total || v.size(0) != total) refuse("the outputs have `total` rows");
   }
-  p.d_first = static_cast<int32_t *>(ints(tensor(a[2], "first"), "first", n));
-  p.d_cu_out = static_cast<int32_t *>(ints(tensor(a[3], "cu_out"), "cu_out", n + 1));
+  p.d_first = static_cast<int32_t *>(ints(first, "first", n));
+  p.d_cu_out = static_cast<int32_t *>(ints(cu_out, "cu_out", n + 1));
   kv_call(g.load, p, "entro_kv_load", c, k, v, table, status, on);
   PyObject *x = THPVariable_Wrap(std::move(k)), *y = THPVariable_Wrap(std::move(v));
   PyObject *r = x && y ? PyTuple_Pack(2, x, y) : nullptr;
@@ -245,8 +266,15 @@ PyObject *load(Args a) {
 
 // q, cache, table, lens, status, scale, out, work, make, stream -> out
 PyObject *cache(Args a) {
-  const at::Tensor &q = tensor(a[0], "q"), &lens = tensor(a[3], "lens"), &status = tensor(a[4], "status");
-  const entro_kv_cache c = cache_of(a[1]);
+  const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[2], "table"), &lens = tensor(a[3], "lens");
+  const at::Tensor &status = tensor(a[4], "status");
+  const CacheDesc desc = cache_of(a[1]);
+  const entro_kv_cache &c = desc.c;
+  at::Tensor out, work;
+  const Together together{desc.device()};
+  together("q", q)("table", table)("lens", lens)("status", status);
+  if (a[6] != Py_None) together("out", out = tensor(a[6], "out"));
+  if (a[7] != Py_None) together("work", work = tensor(a[7], "work"));
   const On on{a[8] == Py_True, a[9]};
   const c10::DeviceGuard guard(q.device());
   if (q.dim() != 3) refuse("q is [sequences][heads][dim]");
@@ -255,32 +283,26 @@ PyObject *cache(Args a) {
   const at::ScalarType t = q.scalar_type();
   entro_attn_cache_args p{};
   p.dtype = (entro_dtype)type_of(q);
-  at::Tensor out;
-  if (a[6] == Py_None) {
+  if (!out.defined())
     out = on.empty(q.sizes(), t, q);
-  } else {
-    out = tensor(a[6], "out");
-    if (out.dim() == 3 && out.size(0) != n) refuse("out has the rows of q");
-  }
+  else if (out.dim() == 3 && out.size(0) != n)
+    refuse("out has the rows of q");
   p.out = rows(out, "out", t, heads, dim);
   p.q = rows(q, "q", t, heads, dim);
   p.n_heads = small(heads, "q");
-  at::Tensor work;
-  if (a[7] == Py_None) {
+  if (!work.defined()) {
     const uint64_t bytes = g.cache_bytes(small(n, "q"), p.n_heads, c.n_kv_heads, c.head_dim);
     work = on.empty({(int64_t)std::max<uint64_t>(bytes, 16u)}, at::kByte, q);
-  } else {
-    work = tensor(a[7], "work");
   }
   std::tie(p.d_work, p.work_bytes) = workspace(work);
   p.d_lens = static_cast<int32_t *>(ints(lens, "lens", n));
   p.scale = scale_of(a[5], dim);
-  const entro_kv_table tb = table_of(tensor(a[2], "table"), n);
+  const entro_kv_table tb = table_of(table, n);
   done(g.cache(&c, &tb, &p, static_cast<uint32_t *>(ints(status, "status", n)), on.handle(q)), "entro_attn_cache");
   return THPVariable_Wrap(std::move(out));
 }
 
-// k_codes, v_codes, k_scales, v_scales -> the cache's description as bytes
+// k_codes, v_codes, k_scales, v_scales -> CacheDesc as bytes
 PyObject *cache_desc(Args a) {
   const at::Tensor &k = tensor(a[0], "k_codes"), &v = tensor(a[1], "v_codes");
   const at::Tensor &ks = tensor(a[2], "k_scales"), &vs = tensor(a[3], "v_scales");
@@ -292,9 +314,11 @@ PyObject *cache_desc(Args a) {
   for (const at::Tensor *x : {&k, &v, &ks, &vs})
     if (x->scalar_type() != (x->dim() == 4 ? at::kChar : at::kFloat) || !x->is_cuda() || !x->is_contiguous())
       refuse("int8 codes and float32 scales, contiguous and on the GPU, expected");
-  const entro_kv_cache c = {static_cast<int8_t *>(k.data_ptr()), static_cast<int8_t *>(v.data_ptr()),
-                            static_cast<float *>(ks.data_ptr()), static_cast<float *>(vs.data_ptr()),
-                            small(pages, "pages"), small(page, "page"), small(kv, "heads"), small(dim, "dim")};
+  Together{k.device()}("v_codes", v)("k_scales", ks)("v_scales", vs);
+  const CacheDesc c = {{static_cast<int8_t *>(k.data_ptr()), static_cast<int8_t *>(v.data_ptr()),
+                        static_cast<float *>(ks.data_ptr()), static_cast<float *>(vs.data_ptr()), small(pages, "pages"),
+                        small(page, "page"), small(kv, "heads"), small(dim, "dim")},
+                       k.device().index()};
   return PyBytes_FromStringAndSize(reinterpret_cast<const char *>(&c), sizeof c);
 }
 
