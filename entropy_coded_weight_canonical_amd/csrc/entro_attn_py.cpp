@@ -10,6 +10,7 @@
 
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -48,11 +49,14 @@ const at::Tensor &tensor(PyObject *o, const char *what) {
 }
 
 // All tensors of a call are on the device of the first one that is named (the
-// call's, which the kernels run on), also before anything is read or made.
+// call's, which the kernels run on), and none is one that a gradient is recorded
+// for: there is no backward pass.  Looked at before anything is read or made.
 struct Together {
   const at::Device device;
   const Together &operator()(const char *what, const at::Tensor &x) const {
     if (x.device() != device) refuse(what, ": on device ", x.device(), ", the call is on ", device);
+    if (x.requires_grad() && c10::GradMode::is_enabled())
+      refuse(what, ": requires a gradient, and there is no backward pass; call under torch.no_grad() or detach it");
     return *this;
   }
 };
@@ -165,7 +169,7 @@ PyObject *prompt(Args a) {
   const at::Tensor &cu_q = tensor(a[3], "cu_q"), &cu_k = tensor(a[4], "cu_k"), &status = tensor(a[5], "status");
   at::Tensor out, work;
   const Together together{q.device()};
-  together("k", k)("v", v)("cu_q", cu_q)("cu_k", cu_k)("status", status);
+  together("q", q)("k", k)("v", v)("cu_q", cu_q)("cu_k", cu_k)("status", status);
   if (a[7] != Py_None) together("out", out = tensor(a[7], "out"));
   if (a[8] != Py_None) together("work", work = tensor(a[8], "work"));
   const On on{a[9] == Py_True, a[10]};
@@ -314,7 +318,7 @@ PyObject *cache_desc(Args a) {
   for (const at::Tensor *x : {&k, &v, &ks, &vs})
     if (x->scalar_type() != (x->dim() == 4 ? at::kChar : at::kFloat) || !x->is_cuda() || !x->is_contiguous())
       refuse("int8 codes and float32 scales, contiguous and on the GPU, expected");
-  Together{k.device()}("v_codes", v)("k_scales", ks)("v_scales", vs);
+  Together{k.device()}("k_codes", k)("v_codes", v)("k_scales", ks)("v_scales", vs);
   const CacheDesc c = {{static_cast<int8_t *>(k.data_ptr()), static_cast<int8_t *>(v.data_ptr()),
                         static_cast<float *>(ks.data_ptr()), static_cast<float *>(vs.data_ptr()), small(pages, "pages"),
                         small(page, "page"), small(kv, "heads"), small(dim, "dim")},
