@@ -173,11 +173,15 @@ def kv_load(cache: KVCache, table, first, cu_out, total: int, status, dtype=None
     """Read tokens back as 16-bit values (``entro_kv_load``): for sequence b
     the ``cu_out[b + 1] - cu_out[b]`` tokens from position ``first[b]`` on.
     Returns ``(k, v)``, each [total][kv heads][dim], of ``dtype`` (default
-    bfloat16) or the pair ``out``."""
+    bfloat16) or the pair ``out``, whose type it then is."""
     e = _ext or _load_ext()
     k, v = (None, None) if out is None else out
-    if dtype is not None and dtype is not torch.bfloat16 and dtype is not torch.float16:
-        raise ValueError(f"element type {dtype}: bfloat16 or float16 expected")
+    if dtype is not None:
+        if dtype is not torch.bfloat16 and dtype is not torch.float16:
+            raise ValueError(f"element type {dtype}: bfloat16 or float16 expected")
+        for x in out or ():
+            if isinstance(x, torch.Tensor) and x.dtype is not dtype:
+                raise ValueError(f"element type {dtype} with outputs of type {x.dtype}")
     f16 = dtype is torch.float16
     if stream is not None:
         return _on(stream, e.kv_load, cache, table, first, cu_out, total, status, f16, k, v)
