@@ -271,11 +271,21 @@ def decode_gemm(tensors, items, n_tokens: int, d_status: int, stream=None) -> No
                                     ctypes.c_void_p(_stream_handle(stream))), "entro_decode_gemm")
 
 
+class _Caps(int):
+    """The cap of ``entro.h``'s launches, with that of ``entro_attn.h``'s."""
+
+    attn = 0
+
+
 def set_max_workgroups(n: int) -> int:
     """``entro_set_max_workgroups`` and ``entro_attn_set_max_workgroups``: cap
-    the workgroups of later launches (0: no cap); returns the previous cap."""
-    load().entro_attn_set_max_workgroups(int(n))
-    return int(load().entro_set_max_workgroups(int(n)))
+    the workgroups of later launches (0: no cap); returns the previous cap.
+    Given back what was returned, it sets both to what they were before."""
+    lib = load()
+    attn_old = lib.entro_attn_set_max_workgroups(n.attn if isinstance(n, _Caps) else int(n))
+    old = _Caps(lib.entro_set_max_workgroups(int(n)))
+    old.attn = attn_old
+    return old
 
 
 def _rans_array(tensors):
