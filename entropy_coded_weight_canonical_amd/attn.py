@@ -16,6 +16,7 @@ require a gradient are refused outside ``torch.no_grad()``.
 from __future__ import annotations
 
 import ctypes
+import operator
 
 __all__ = ["KVCache", "attn_prompt", "kv_store", "kv_load", "attn_cache", "attn_prompt_work_bytes", "attn_cache_work_bytes"]
 
@@ -94,17 +95,29 @@ def _load_ext():
     return _ext
 
 
+def _kept(slot):
+    """A KVCache's attribute, held in `slot`: it can only be set to what it is
+    (as an operation in place does)."""
+
+    def keep(self, value):
+        if value is not getattr(self, slot):
+            raise AttributeError("a KVCache keeps the tensors that it was made of: make another of the new ones")
+
+    return property(operator.attrgetter(slot), keep)
+
+
 class KVCache:
     """Pages of 8-bit keys and values: ``k_codes`` int8 [pages][kv heads][page
     tokens][dim], ``v_codes`` int8 [pages][kv heads][dim][page tokens],
     ``k_scales`` / ``v_scales`` float32 [pages][kv heads].  Holds the tensors,
-    so that the device memory outlives the calls."""
+    so that the device memory outlives the calls; they cannot be replaced."""
 
-    __slots__ = ("k_codes", "v_codes", "k_scales", "v_scales", "desc")
+    __slots__ = ("_k_codes", "_v_codes", "_k_scales", "_v_scales", "_desc")
+    k_codes, v_codes, k_scales, v_scales, desc = (_kept(s) for s in __slots__)
 
     def __init__(self, k_codes, v_codes, k_scales, v_scales):
-        self.desc = (_ext or _load_ext()).cache_desc(k_codes, v_codes, k_scales, v_scales)
-        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self._desc = (_ext or _load_ext()).cache_desc(k_codes, v_codes, k_scales, v_scales)
+        self._k_codes, self._v_codes, self._k_scales, self._v_scales = k_codes, v_codes, k_scales, v_scales
 
     @property
     def tensors(self):
