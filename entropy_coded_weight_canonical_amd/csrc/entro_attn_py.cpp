@@ -11,6 +11,7 @@
 #include <ATen/ATen.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -338,10 +339,8 @@ PyObject *entry(PyObject *, Args a, Py_ssize_t n) {
     return nullptr;
   } catch (const std::invalid_argument &e) {
     PyErr_SetString(PyExc_ValueError, e.what());
-  } catch (const c10::OutOfMemoryError &e) {
-    PyErr_SetString(PyExc_MemoryError, e.what_without_backtrace());
-  } catch (const std::exception &e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
+  } catch (const std::exception &) {   // torch's own, as torch raises them
+    torch::translate_exception_to_python(std::current_exception());
   }
   return nullptr;
 }
