@@ -123,6 +123,8 @@ __device__ __forceinline__ uint32_t top_of(uint32_t w, uint32_t top) {
   return max(top, max(a, b));
 }
 
+constexpr uint32_t kWavesMost = 8;   // wavefronts of a workgroup, at most
+
 // Largest of v over the workgroup.
 __device__ __forceinline__ uint32_t wg_max(uint32_t v, uint32_t *red) {
   v = wave_max(v);
@@ -171,10 +173,10 @@ __device__ __forceinline__ Grow grow(float before, float top) {
 template <entro_dtype T, int D>
 __global__ __launch_bounds__(512, 5) void kv_store_kernel(KvArg a, uint32_t page) {
   constexpr uint32_t C = D / 8;           // column groups of eight
-  __shared__ uint32_t red[8];
   uint8_t *vt = reinterpret_cast<uint8_t *>(dyn_lds);   // [D][page + 4]
   const uint32_t tid = threadIdx.x, lane = tid & 63u;
   const uint32_t vs = page + 4u, c = tid % C, quad = tid / C;
+  uint32_t *red = reinterpret_cast<uint32_t *>(vt + D * vs);   // [kWavesMost]
   if (blockIdx.x == 0u && blockIdx.y == 0u) kv_check(a, page);
   for (uint32_t head = blockIdx.y; head < a.n_kv; head += gridDim.y)
     for (uint64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
@@ -366,7 +368,7 @@ static entro_status launch_kv(KvArg &a, uint32_t page, hipStream_t s) {
   const uint64_t items = std::min<uint64_t>(a.total, (uint64_t)a.total / page + 2ull * a.n_seq);
   a.items = items;
   const uint32_t threads = (D / 8u * (page / 4u) + 63u) & ~63u;
-  const size_t lds = (size_t)D * (page + 4u);
+  const size_t lds = (size_t)D * (page + 4u) + (STORE ? 4u * kWavesMost : 0u);
   (void)hipGetLastError();
   hipLaunchKernelGGL((STORE ? kv_store_kernel<T, D> : kv_load_kernel<T, D>), grid2(items, a.n_kv), dim3(threads), lds, s,
                      a, page);
