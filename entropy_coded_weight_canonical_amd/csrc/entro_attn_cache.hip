@@ -174,10 +174,10 @@ __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
 // tile.  Lanes, wavefronts and pieces are joined by the logarithms of their sums.
 //
 // Bound by the reading of the cache: 131072 tokens of one sequence (32 / 8 heads
-// of 128) 44 us, 6.1 TB/s, which is what a kernel that only reads reaches; 64
-// ragged sequences of up to 16384 tokens 120 us, 5.2 TB/s; 8 of up to 4099 (32
-// heads of 96) 16 us, 3.7 TB/s, a third of it the way to the first key and the
-// wavefronts' join.  90 tokens: 4.8 us.  At head dimension 128 registers for a
+// of 128) 43 us, 6.2 TB/s, where a kernel that only reads reaches 6.4; 64 ragged
+// sequences of up to 16384 tokens 116 us, 5.4 TB/s; 8 of up to 4099 (32 heads of
+// 96) 16 us, 3.7 TB/s, a third of it the way to the first key and the wavefronts'
+// join.  90 tokens: 5.0 us.  At head dimension 128 registers for a
 // third workgroup a CU would take spills: 120 -> 135 us.
 // ---------------------------------------------------------------------------
 template <entro_dtype T, int D>
@@ -506,10 +506,11 @@ template <entro_dtype T, int D>
 static entro_status launch_cache(CacheArg &a, hipStream_t s) {
   // Where no sequence can be long, a workgroup each and nothing to join: the
   // second kernel and its launch cost more than some rounds of the wavefronts
-  // (12 sequences of up to 393 tokens, 32 / 8 heads of 128, 16 us with and 8 us
-  // without; one of 1000 14 and 10; 16 of up to 1000 17 and 12; one of 2000 14 and
-  // 16).  With more workgroups than run at once the longest come on top: 64 of up
-  // to 800 tokens, 32 heads of 96, 39 and 37, up to 1000 35 and 46.
+  // (32 / 8 heads of 128: 12 sequences of up to 393 tokens 16 us with and 7 us
+  // without, 16 of up to 1000 15 and 11, one of 1000 11 and 10, one of 1536 11 and
+  // 13).  With more workgroups than run at once the longest come on top: 64 of up
+  // to 768 tokens, 32 heads of 96, 41 and 35; of up to 1000 35 and 46 in an earlier
+  // state of the kernel.
   const uint64_t tiles = (((uint64_t)a.table_pages << a.page_log2) + kTile - 1u) / kTile;
   const bool split = tiles > ((uint64_t)a.n_seq * a.n_kv * a.parts <= shares_at(D) ? 24u : 12u);
   a.part_ml = reinterpret_cast<f32x2 *>(a.part_o + ((uint64_t)a.n_seq + a.shares) * a.n_heads * D);

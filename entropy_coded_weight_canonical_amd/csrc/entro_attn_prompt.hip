@@ -119,6 +119,10 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 // product is element r of a half; the values' tokens are read in that order).
 // Values are turned on the way from LDS to registers.
 //
+// Weights are rounded to the element type, that of the values, which is what the
+// matrix cores multiply; their sum is taken of the rounded ones, so that an output
+// is a mean of values whose weights are each off by half a step and sum to 1.
+//
 // Values that a query must not see have weight 0, and 0 times an infinity
 // would reach it: a tile that some queries see in part is looked over by the
 // wavefronts that copied it, and where it holds infinities or NaN these are
@@ -131,12 +135,12 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 //
 // Bound by the matrix cores, and on them by the card's power: 16384 tokens of
 // 32 / 8 heads of 128 (bf16, normal values) take 2.0 ms, 1080 TFLOP/s, at a
-// clock of 1.5 to 1.7 GHz with the matrix cores busy 63% of it; with all values
+// clock of 1.5 to 1.7 GHz with the matrix cores busy 61% of it; with all values
 // zero the same work runs at 1480 TFLOP/s (a library product of 8192^3: 1150 and
-// 1690).  8192 tokens of 32 heads: of 96 447 us, 920 TFLOP/s; of 64 305 us, 900, with
-// 6 vector instructions (the exponentials at a quarter of the rate among
-// them) a matrix product at 96.  4096 tokens (32 / 8 heads of 128) 146 us, 2048
-// 48 us, 8 sequences of 512 42 us.  37 tokens 6.6 us, which is latency: sums,
+// 1690).  8192 tokens of 32 heads: of 96 462 us, 890 TFLOP/s; of 64 306 us, 900, with
+// 7.5 vector instructions (the exponentials at a quarter of the rate among
+// them) a matrix product at 96.  4096 tokens (32 / 8 heads of 128) 148 us, 2048
+// 47 us, 8 sequences of 512 40 us.  37 tokens 6.5 us a call, which is latency: sums,
 // the first tile, the queries, one tile's work, the outputs.
 //
 // Measured and not taken: the scores of the next tile between the exponentials
@@ -545,10 +549,11 @@ static PromptGrid prompt_grid(uint32_t n_seq, uint32_t total_q, uint32_t total_k
   // times (about 6 bytes a picosecond), and the second kernel takes some 6 us.
   // The n with the least of both, from 4 tiles a part and 32 parts (the second
   // kernel's own way) on down.  32 / 8 heads of 128, split and not: one query,
-  // 16000 keys 30 and 218 us, 1100 keys 17 and 24; 128 queries behind 4000 keys 30
-  // and 64; 9 x 13 behind 3506 37 and 57; 512 behind 4000 55 and 75, behind 1000
-  // (not split) 38 and 33; 6 of up to 45 queries behind up to 3664 keys 27 and 57.
-  // The guess is off for 12 x 20 behind 1300: 30 and 27.
+  // 16000 keys 30 and 216 us, 1100 keys 17 and 23; 128 queries behind 4000 keys 30
+  // and 64; 9 x 13 with 3506 keys each 44 and 71; 512 behind 4000 54 and 70; 6 of up
+  // to 45 queries with up to 3664 keys 27 and 57; one query of 16000 keys beside 15 of
+  // 200 83 and 271 (all get the parts of their average).  The guess is off for 12 x 20
+  // behind 1300: 31 and 29.
   const double way = (0.3 + 0.005 * head_dim) * (n_seq > 1u ? 1.5 : 1.0) * (double)tiles;
   const double sums = (double)total_q * n_heads * head_dim * 8.0 / 6e6;
   uint64_t parts = std::min<uint64_t>({512u / all, tiles / 4u, 32u, (uint64_t)std::sqrt(way / sums)});

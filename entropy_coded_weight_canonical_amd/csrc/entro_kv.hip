@@ -163,10 +163,10 @@ __device__ __forceinline__ Grow grow(float before, float top) {
 // registers to four tokens a word and collected in LDS, from where a thread
 // writes 16 tokens of one dimension.  Pieces of 16 tokens that are not all new
 // are merged with what the page holds.  Memory bound: 2 bytes in and 1 out per
-// value.  32768 tokens of 8 heads of 128: 44 us, 4.6 TB/s of both together (a
-// large copy reaches 4.8); 4522 tokens of 12 sequences, 32 heads of 96 in pages
-// of 32: 25 us, 3.4 TB/s.  One token for each of 16 sequences: 7.0 us, 7.3 where
-// the range grows: a chain of reads (sums, page, rows and scale, codes held).
+// value.  32768 tokens of 8 heads of 128: 46 us, 4.4 TB/s of both together (a copy
+// in that proportion reaches 5.6); 4522 tokens of 12 sequences, 32 heads of 96 in
+// pages of 32: 24 us, 3.5 TB/s.  One token for each of 16 sequences: 7.4 us, 0.3 more
+// where the range grows: a chain of reads (sums, page, rows and scale, codes held).
 // Reading the codes held with the rows takes registers: it spills and costs the
 // large calls 10%.
 // ---------------------------------------------------------------------------
@@ -296,8 +296,8 @@ __global__ __launch_bounds__(512, 5) void kv_store_kernel(KvArg a, uint32_t page
 // load: the same four rows x eight columns a thread, keys and values of a head
 // on their way together.  Value codes come in as 16 tokens of one dimension and
 // are turned over LDS.  Memory bound, 1 byte in and 2 out: 58371 tokens of 8
-// heads of 128 (24 sequences) 72 us, 5.0 TB/s; 700 tokens of 32 heads of 64 in
-// pages of 16 5.5 us.
+// heads of 128 (24 sequences) 71 us, 5.05 TB/s (a copy in that proportion: 5.2); 700 tokens of 32 heads of 64 in
+// pages of 16 5.2 us.
 // ---------------------------------------------------------------------------
 template <entro_dtype T>
 __device__ __forceinline__ u32x4 values8(uint32_t lo, uint32_t hi, float s) {
