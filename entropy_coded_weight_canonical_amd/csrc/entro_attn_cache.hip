@@ -35,7 +35,7 @@ struct CacheArg {
   uint32_t shares;              // that the tokens of a key/value head are split into at most; 0: one sequence each
   float scale;                  // times log2(e)
   float *part_o;                // [n_seq + shares][n_heads][D]
-  f32x2 *part_ml;               // [n_seq + shares][n_heads]: the output's exponent, the weights' sum (logarithms)
+  f32x2 *part_ml;               // [n_seq + shares][n_heads]: Piece's o and gap
   uint32_t *status;
 };
 
@@ -112,30 +112,40 @@ __device__ __forceinline__ f16v8 half8(uint32_t w0, uint32_t w1) {
   return __builtin_bit_cast(f16v8, (u32x4){a.x, a.y, b.x, b.y});
 }
 
-// A piece of a head's tokens, or several, in powers of two: `o`, the exponent of
-// its outputs (times 2^15, see below), and `w`, the logarithm of its softmax's
-// sum.  Both -inf without tokens (o also where all values are zero); w is NaN
-// where the result is.  The two are apart by the values' size, which may be
-// anything: neither is taken relative to the other before the end.
+// What is known of a piece of a head's tokens beside its outputs, in powers of
+// two: `o`, the exponent of the outputs (times 2^15, see below), and `gap`, how far
+// the logarithm of its softmax's sum lies below o.  o goes with the scores and may
+// be large; the gap goes with the values' size, and is held by itself because it is
+// what the result's size follows from.  Without tokens o is -inf and the gap inf; the
+// gap is NaN where the result is.
+typedef f32x2 Piece;
+__device__ __forceinline__ float above(float o, float ref) { return o == ref ? 0.0f : o - ref; }
+
+// Pieces joined: outputs relative to the largest o, their weights' sum relative
+// to 2^(o + w).
 struct Joined {
   float o, w;
-  __device__ void raise(f32x2 part) {
-    o = fmaxf(o, part.x);
-    w = fmaxf(w, part.y);
-  }
+  __device__ float of(Piece p) const { return above(p.x, o) - p.y; }   // logarithm of a piece's sum, less o
 };
-// What outputs relative to 2^o, with weights that sum to `sum` relative to 2^w,
-// are multiplied by.
+// What the joined outputs are multiplied by.
 struct Factor {
   float r;
   int e;
   __device__ Factor(Joined j, float sum) {
-    const float up = fminf(fmaxf(j.o - j.w, -512.0f), 512.0f), whole = floorf(up);
+    const float up = fminf(fmaxf(-j.w, -512.0f), 512.0f), whole = floorf(up);
     r = j.w == -INFINITY && sum == sum ? 0.0f : exp2_fast(up - whole) / sum;
     e = (int)whole - 15;
   }
   __device__ float of(float x) const { return ldexpf(x * r, e); }
 };
+// The gap of pieces whose weights sum to `sum` relative to 2^(o + w).
+__device__ __forceinline__ float gap_of(float w, float sum) { return sum == 0.0f ? INFINITY : -(w + __log2f(sum)); }
+
+// a b, rounded, whatever follows.
+__device__ __forceinline__ float rounded(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
 
 __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -163,15 +173,15 @@ __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
 // product as 2^(t - M + 15): the scale of a page's values rides in the exponent,
 // and f16 covers weights down to 2^-29 of the largest with 11 bits.
 //
-// A page's scale may be anything from 0 (values all zero) to the type's largest,
-// so the softmax's sum has a maximum of its own, of the scores s alone, for each
-// lane (16 tokens of a tile, all of one page).  A lane's weights of a tile are
-// computed once, as 2^(s - base): base = M - log2(scale) - 15 makes them those of
-// the product; where the page's scale is so small against M that they would be
-// below 2^-64, base = (largest s) + 64 keeps them for the sum, and f16 takes them
-// as the zeros they are in the product.  The sum is of the weights before
-// rounding, in 32 bits, brought from base to the lane's maximum by one factor a
-// tile.  Lanes, wavefronts and pieces are joined by the logarithms of their sums.
+// A page's scale may be anything from 0 (values all zero; taken as 2^-200) to the
+// type's largest, so the softmax's sum has a maximum of its own, of the scores
+// alone, and one for each lane, whose 16 tokens of a tile are all of one page:
+// weights are computed less the largest of the 16, added up in 32 bits, and brought
+// to the product's by one factor of the lane.  Scores may be far from 0, where a
+// scale's logarithm added to them is lost: M is held less an anchor, the score whose
+// t was the largest when M last rose, and only differences of scores meet
+// anything else (the scores are rounded first: a fused difference would have the
+// rounding left over).
 //
 // Bound by the reading of the cache: 131072 tokens of one sequence (32 / 8 heads
 // of 128) 43 us, 6.2 TB/s, where a kernel that only reads reaches 6.4; 64 ragged
@@ -281,8 +291,8 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
         f32x4 o[DT];
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-        float m = -INFINITY;                     // of score + log2(value scale)
-        float top = -kFloatMax, l = 0.0f;        // of the scores, and the weights' sum: this lane's tokens only
+        float anchor = 0.0f, m = -INFINITY;   // M is their sum
+        float top = -kFloatMax, l = 0.0f;     // of the scores, and the weights' sum: this lane's tokens only
         bool bad = false;
 
         // Pages of the 16-token blocks that this lane reads keys of (n / 4) and
@@ -340,27 +350,29 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
           }
           if (more) keys(tile + kCacheWaves, next.k);
           now = next;
-          // scores in powers of two; tokens that are not seen are of value scale 0
+          // scores in powers of two
           const uint32_t seen = v_bad || tv >= len ? 0u : min(16u, len - tv);
-          const float vs = seen ? v_scale : 0.0f, lv = __log2f(vs);
-          float mx = -INFINITY;
+          const float vs = seen ? v_scale : 0.0f;
+          const float lv = seen ? fmaxf(__log2f(vs), -200.0f) : -INFINITY;
+          float mx = -kFloatMax;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             for (int r = 0; r < 4; ++r) {
-              const float t = (uint32_t)(4 * i + r) < seen ? s4[i][r] * ks : -INFINITY;
+              const float t = (uint32_t)(4 * i + r) < seen ? rounded(s4[i][r], ks) : -INFINITY;
               s4[i][r] = t;
               mx = fmaxf(mx, t);
             }
-          const float mt = max32(max16(mx + lv));
+          const float t = mx - anchor + lv, mt = max32(max16(t));
           if (__any(mt > m)) {
-            const float mn = fmaxf(m, mt);
-            const float k = mn == -INFINITY ? 1.0f : exp2_fast(m - mn);
-            m = mn;
+            const bool rise = mt > m;
+            const float next = rise ? max32(max16(t == mt ? mx : -INFINITY)) : anchor;
+            const float mn = max32(max16(mx - next + lv)), k = rise ? exp2_fast(m - (next - anchor) - mn) : 1.0f;
+            anchor = next;
+            m = rise ? mn : m;
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[d] *= k;
           }
-          mx = fmaxf(mx, -kFloatMax);
-          const float base = fminf(m - lv - 15.0f, mx + 64.0f);   // (inf - inf counts as no limit)
+          const float f = exp2_fast(fminf(mx - anchor + lv - m + 15.0f, 15.0f));   // (inf - inf counts as 15: all is 0)
           float sum = 0.0f;
           u32x4 pw[2];
 #pragma unroll
@@ -368,14 +380,14 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
             float p[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              p[r] = exp2_fast(s4[i][r] - base);
+              p[r] = exp2_fast(s4[i][r] - mx);
               sum += p[r];
             }
-            pw[i >> 1][2 * (i & 1)] = Elem<ENTRO_F16>::pack2(p[0], p[1]);
-            pw[i >> 1][2 * (i & 1) + 1] = Elem<ENTRO_F16>::pack2(p[2], p[3]);
+            pw[i >> 1][2 * (i & 1)] = Elem<ENTRO_F16>::pack2(p[0] * f, p[1] * f);
+            pw[i >> 1][2 * (i & 1) + 1] = Elem<ENTRO_F16>::pack2(p[2] * f, p[3] * f);
           }
           const float up = fmaxf(top, mx);
-          l = l * exp2_fast(top - up) + sum * exp2_fast(base - up) + vs * 0.0f;   // NaN where the scale is no number
+          l = l * exp2_fast(top - up) + sum * exp2_fast(mx - up) + vs * 0.0f;   // NaN where the scale is no number
           top = up;
           const f16v8 p0 = __builtin_bit_cast(f16v8, pw[0]), p1 = __builtin_bit_cast(f16v8, pw[1]);
 #pragma unroll
@@ -388,7 +400,7 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
         // join the lanes, then the wavefronts
         const float wave_top = max32(max16(top));
         l = add32(add16(l * exp2_fast(top - wave_top)));
-        if (g == 0u) red_ml[wave][n] = (f32x2){m, wave_top + __log2f(l)};
+        if (g == 0u) red_ml[wave][n] = (Piece){anchor + m, gap_of(wave_top - anchor - m, l)};
 #pragma unroll
         for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(&red_o[wave][n][16 * d + 4 * g]) = o[d];
         __syncthreads();
@@ -397,14 +409,16 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
           const uint32_t h = i / (D / 2u), d = i % (D / 2u) * 2u;
           Joined j{-INFINITY, -INFINITY};
 #pragma unroll
-          for (uint32_t v = 0; v < kCacheWaves; ++v) j.raise(red_ml[v][h]);
+          for (uint32_t v = 0; v < kCacheWaves; ++v) j.o = fmaxf(j.o, red_ml[v][h].x);
+#pragma unroll
+          for (uint32_t v = 0; v < kCacheWaves; ++v) j.w = fmaxf(j.w, j.of(red_ml[v][h]));
           float x = 0.0f, y = 0.0f, sum = 0.0f;
 #pragma unroll
           for (uint32_t v = 0; v < kCacheWaves; ++v) {
-            const float k = join_factor(red_ml[v][h].x, j.o);
+            const float k = exp2_fast(above(red_ml[v][h].x, j.o));
             x += k * red_o[v][h][d];
             y += k * red_o[v][h][d + 1u];
-            sum += join_factor(red_ml[v][h].y, j.w);
+            sum += join_factor(j.of(red_ml[v][h]), j.w);
           }
           if (whole) {
             const Factor f(j, sum);
@@ -413,7 +427,7 @@ __global__ __launch_bounds__(256, 2) void attn_cache_kernel(CacheArg a) {
           } else {
             const uint64_t at = ((uint64_t)w + seq) * a.n_heads + head0 + h;
             *reinterpret_cast<f32x2 *>(a.part_o + at * D + d) = (f32x2){x, y};
-            if (d == 0u) a.part_ml[at] = (f32x2){j.o, j.w + __log2f(sum)};
+            if (d == 0u) a.part_ml[at] = (Piece){j.o, gap_of(j.w, sum)};
           }
         }
         __syncthreads();
@@ -458,8 +472,12 @@ __global__ __launch_bounds__(64 * G) void attn_join_kernel(CacheArg a) {
         }
         Joined up = j;
 #pragma unroll
-        for (uint32_t c = 0; c < 4; ++c) up.raise(v[c]);
-        const float k = join_factor(j.o, up.o);
+        for (uint32_t c = 0; c < 4; ++c) up.o = fmaxf(up.o, v[c].x);
+        const float by = above(j.o, up.o), k = exp2_fast(by);
+        j.w += by;
+        up.w = j.w;
+#pragma unroll
+        for (uint32_t c = 0; c < 4; ++c) up.w = fmaxf(up.w, up.of(v[c]));
         x *= k;
         y *= k;
         sum *= join_factor(j.w, up.w);
@@ -467,24 +485,25 @@ __global__ __launch_bounds__(64 * G) void attn_join_kernel(CacheArg a) {
 #pragma unroll
         for (uint32_t c = 0; c < 4; ++c) {
           if (i0 + (uint32_t)G * c >= n) break;
-          const float kc = join_factor(v[c].x, j.o);
+          const float kc = exp2_fast(above(v[c].x, j.o));
           x += kc * p[c].x;
           y += kc * p[c].y;
-          sum += join_factor(v[c].y, j.w);
+          sum += join_factor(j.of(v[c]), j.w);
         }
       }
       if (lane * 2u < D) *reinterpret_cast<f32x2 *>(&red_o[group][d]) = (f32x2){x, y};
-      if (lane == 0u) red_ml[group] = (f32x2){j.o, sum == 0.0f ? -INFINITY : j.w + __log2f(sum)};   // a group without pieces
+      if (lane == 0u) red_ml[group] = (Piece){j.o, gap_of(j.w, sum)};
       __syncthreads();
       if (group == 0u && lane * 2u < D) {
         j = Joined{-INFINITY, -INFINITY};
         x = y = sum = 0.0f;
-        for (int g = 0; g < G; ++g) j.raise(red_ml[g]);
+        for (int g = 0; g < G; ++g) j.o = fmaxf(j.o, red_ml[g].x);
+        for (int g = 0; g < G; ++g) j.w = fmaxf(j.w, j.of(red_ml[g]));
         for (int g = 0; g < G; ++g) {
-          const float k = join_factor(red_ml[g].x, j.o);
+          const float k = exp2_fast(above(red_ml[g].x, j.o));
           x += k * red_o[g][d];
           y += k * red_o[g][d + 1u];
-          sum += join_factor(red_ml[g].y, j.w);
+          sum += join_factor(j.of(red_ml[g]), j.w);
         }
         const Factor f(j, sum);
         *reinterpret_cast<uint32_t *>(a.out + b * a.o_t + head * a.o_h + d * 2u) = Elem<T>::pack2(f.of(x), f.of(y));
