@@ -18,7 +18,7 @@ struct PromptArg {
   uint32_t heads;                                   // query heads of a workgroup: 1, 2 or 4 of one key/value head
   uint32_t parts;                                   // workgroups that share an item's keys
   float *part_o;                                    // parts > 1: [parts][total_q][n_heads][D]
-  f32x2 *part_ml;                                   // [parts][total_q][n_heads]: maximum in powers of two, sum
+  f32x2 *part_ml;                                   // [parts][total_q][n_heads]: maximum (of q . k), sum
   float scale;                                      // magnitude, times log2(e); 1 where the scale is 0
   float lift;                                       // see lift_of
   uint32_t q_and, q_xor;                            // on a pair of q: the scale's sign, and 0 where the scale is 0
@@ -58,6 +58,12 @@ __device__ __forceinline__ u32x4 without_special(u32x4 w) {
   return w;
 }
 
+// Weights are 2^(s scale + (lift - maximum scale)), one instruction before the
+// exponential, and what the second term is rounded by is the same for all keys of a
+// maximum.  With maxima above this (in powers of two) it would show between tiles,
+// or push weights out of their type: the maximum then is taken from the scores first.
+constexpr float kFar = 256.0f;
+
 // LDS place (16-byte piece) of piece c of row r of a tile of keys or values.
 // Rows are 2 D bytes, and 256 bytes are read at once: one piece of 16 rows
 // (keys), or four neighbouring pieces of 4 rows (values).  The pieces' order
@@ -83,6 +89,16 @@ __device__ __forceinline__ void scale_in_place(f32x16 &o, float k) {
     float x = o[r];
     asm volatile("v_mul_f32 %0, %1, %0" : "+v"(x) : "v"(k));
     o[r] = x;
+  }
+}
+
+// s -= x likewise.
+__device__ __forceinline__ void less_in_place(f32x16 &s, float x) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    float y = s[r];
+    asm volatile("v_sub_f32 %0, %0, %1" : "+v"(y) : "v"(x));
+    s[r] = y;
   }
 }
 
@@ -207,6 +223,7 @@ attn_prompt_kernel(PromptArg a) {
 
       f32x16 o[DT];
       float m = -INFINITY, l = 0.0f;   // l: this lane's keys only
+      bool far = false;                // some of the wavefront's maxima are, see kFar
 #pragma unroll
       for (int d = 0; d < DT; ++d)
         for (int r = 0; r < 16; ++r) o[d][r] = 0.0f;
@@ -294,19 +311,25 @@ attn_prompt_kernel(PromptArg a) {
         }
       };
       // Maximum of the lane's query up to this tile.
-      auto raise_to = [&](const f32x16 (&s)[2]) {
+      auto raise_to = [&](f32x16 (&s)[2]) {
         float mx = -INFINITY;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[i][r]);
-        if (__any(mx * a.scale > m * a.scale + kLag<T>)) {
+        if (far || __any((mx - m) * a.scale > kLag<T>)) {
           mx = max32(mx);
-          const float mn = mx * a.scale > m * a.scale + kLag<T> ? mx : m;
+          const float mn = (mx - m) * a.scale > kLag<T> ? mx : m;
           const float k = mn == -INFINITY ? 1.0f : exp2_fast((m - mn) * a.scale);
           m = mn;
           l *= k;
 #pragma unroll
           for (int d = 0; d < DT; ++d) scale_in_place(o[d], k);
+          far = __any(m != -INFINITY && fabsf(m) * a.scale > kFar);
+          if (far) {
+            const float less = m == -INFINITY ? 0.0f : m;
+            less_in_place(s[0], less);
+            less_in_place(s[1], less);
+          }
         }
       };
       // Values of 16 tokens from 16 c on, of dimensions 32 d on: the lane gives
@@ -322,7 +345,7 @@ attn_prompt_kernel(PromptArg a) {
       };
       // Outputs of a tile; kept(w): w, or what is left of it.
       auto outputs = [&](const f32x16 (&s)[2], const u32x4 *vt, uint32_t ln, auto kept) {
-        const float off = m == -INFINITY ? 0.0f : a.lift - m * a.scale;
+        const float off = m == -INFINITY ? 0.0f : far ? a.lift : a.lift - m * a.scale;
         u32x4 p[2], w[DT];
         auto pair = [&](int c, int e) {   // weights of keys 16 c + 2 e, 2 e + 1 (in the products' order)
           const float x = exp2_fast(__builtin_fmaf(s[c / 2][c % 2 * 8 + 2 * e], a.scale, off));
@@ -442,7 +465,7 @@ attn_prompt_kernel(PromptArg a) {
 #pragma unroll
             for (int r = 0; r < 16; r += 4)
               *reinterpret_cast<f32x4 *>(to + 32 * d + 2 * r) = (f32x4){o[d][r], o[d][r + 1], o[d][r + 2], o[d][r + 3]};
-          if (ln < 32u) a.part_ml[row] = (f32x2){m * a.scale, sum};
+          if (ln < 32u) a.part_ml[row] = (f32x2){m, sum};
         }
         continue;
       }
@@ -474,6 +497,7 @@ template <entro_dtype T, int D>
 __global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArg a) {
   constexpr uint32_t L = D / 4u, R = 256u / L, kBatch = 8u;
   const uint32_t tid = threadIdx.x, lane = tid & 63u, d = tid % L * 4u;
+  const auto factor = [&](float m, float all) { return m == all ? 1.0f : exp2_fast((m - all) * a.scale); };   // as join_factor
   Span lq{}, lk{};
   Spans spans(a.cu_q, a.total_q, a.n_seq, lane);
   auto items = [&](uint32_t b0) {
@@ -504,14 +528,14 @@ __global__ __launch_bounds__(256) void attn_prompt_join_kernel(PromptArg a) {
           float mn = m;
 #pragma unroll
           for (uint32_t j = 0; j < kBatch; ++j) mn = fmaxf(mn, ml[j].x);
-          const float k = join_factor(m, mn);
+          const float k = factor(m, mn);
           x *= k;
           l *= k;
           m = mn;
 #pragma unroll
           for (uint32_t j = 0; j < kBatch; ++j) {
             if (p0 + j >= a.parts) break;
-            const float kj = join_factor(ml[j].x, m);
+            const float kj = factor(ml[j].x, m);
             x += kj * o[j];
             l += kj * ml[j].y;
           }
