@@ -185,9 +185,9 @@ __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
 //
 // Bound by the reading of the cache: 131072 tokens of one sequence (32 / 8 heads
 // of 128) 43 us, 6.2 TB/s, where a kernel that only reads reaches 6.4; 64 ragged
-// sequences of up to 16384 tokens 116 us, 5.4 TB/s; 8 of up to 4099 (32 heads of
+// sequences of up to 16384 tokens 119 us, 5.3 TB/s; 8 of up to 4099 (32 heads of
 // 96) 16 us, 3.7 TB/s, a third of it the way to the first key and the wavefronts'
-// join.  90 tokens: 5.0 us.  At head dimension 128 registers for a
+// join.  90 tokens: 4.8 us.  At head dimension 128 registers for a
 // third workgroup a CU would take spills: 120 -> 135 us.
 // ---------------------------------------------------------------------------
 template <entro_dtype T, int D>

@@ -150,11 +150,11 @@ __device__ __forceinline__ u32x2 read_turned(const void *at) {
 // joins.
 //
 // Bound by the matrix cores, and on them by the card's power: 16384 tokens of
-// 32 / 8 heads of 128 (bf16, normal values) take 2.0 ms, 1080 TFLOP/s, at a
-// clock of 1.5 to 1.7 GHz with the matrix cores busy 61% of it; with all values
+// 32 / 8 heads of 128 (bf16, normal values) take 2.0 to 2.1 ms by the card, 1080
+// TFLOP/s, at a clock of 1.5 to 1.7 GHz with the matrix cores busy 61% of it; with all values
 // zero the same work runs at 1480 TFLOP/s (a library product of 8192^3: 1150 and
 // 1690).  8192 tokens of 32 heads: of 96 462 us, 890 TFLOP/s; of 64 306 us, 900, with
-// 7.5 vector instructions (the exponentials at a quarter of the rate among
+// 7.7 vector instructions (the exponentials at a quarter of the rate among
 // them) a matrix product at 96.  4096 tokens (32 / 8 heads of 128) 148 us, 2048
 // 47 us, 8 sequences of 512 40 us.  37 tokens 6.5 us a call, which is latency: sums,
 // the first tile, the queries, one tile's work, the outputs.
