@@ -25,10 +25,12 @@ __all__ = [
     "SCHEME_ASYMMETRIC", "SCHEME_UNSIGNED", "SCHEME_MIXED",
     "KVCache", "attn_prompt", "kv_store", "kv_load", "attn_cache", "attn_prompt_work_bytes",
     "attn_cache_work_bytes",
+    "Rotary", "rope", "kv_append", "attn_chunk", "attn_chunk_work_bytes",
 ]
 
 from . import attn
-from .attn import KVCache, attn_cache, attn_cache_work_bytes, attn_prompt, attn_prompt_work_bytes, kv_load, kv_store
+from .attn import (KVCache, Rotary, attn_cache, attn_cache_work_bytes, attn_chunk, attn_chunk_work_bytes, attn_prompt,
+                   attn_prompt_work_bytes, kv_append, kv_load, kv_store, rope)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libentro.so")

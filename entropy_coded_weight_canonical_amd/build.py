@@ -19,7 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libentro.so")
 BINDING = os.path.join(HERE, "_attn.so")
-SOURCES = ["entro_decode.hip", "entro_rans.hip", "entro_attn_prompt.hip", "entro_kv.hip", "entro_attn_cache.hip",
+SOURCES = ["entro_decode.hip", "entro_rans.hip", "entro_attn_prompt.hip", "entro_kv.hip", "entro_rope.hip", "entro_attn_cache.hip",
+           "entro_attn_chunk.hip",
            "entro_lut.cpp", "entro_encode.cpp", "entro_rans.cpp"]
 ARCH = os.environ.get("ENTRO_OFFLOAD_ARCH", "gfx950")
 

@@ -97,21 +97,6 @@ __device__ __forceinline__ Shares shares_of(const CacheArg &a, const Lens &lens)
   return s;
 }
 
-// Four codes of a word as two pairs of f16: the code plus 128 in the low byte
-// of 1024's bits, less 1152 (exact).
-__device__ __forceinline__ u32x2 half4(uint32_t w) {
-  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
-  const uint32_t u = w ^ 0x80808080u;
-  const h2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
-  const uint32_t lo = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u), hi = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
-  return (u32x2){__builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, lo) - off),
-                 __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, hi) - off)};
-}
-__device__ __forceinline__ f16v8 half8(uint32_t w0, uint32_t w1) {
-  const u32x2 a = half4(w0), b = half4(w1);
-  return __builtin_bit_cast(f16v8, (u32x4){a.x, a.y, b.x, b.y});
-}
-
 // What is known of a piece of a head's tokens beside its outputs, in powers of
 // two: `o`, the exponent of the outputs (times 2^15, see below), and `gap`, how far
 // the logarithm of its softmax's sum lies below o.  o goes with the scores and may
@@ -140,12 +125,6 @@ struct Factor {
 };
 // The gap of pieces whose weights sum to `sum` relative to 2^(o + w).
 __device__ __forceinline__ float gap_of(float w, float sum) { return sum == 0.0f ? INFINITY : -(w + __log2f(sum)); }
-
-// a b, rounded, whatever follows.
-__device__ __forceinline__ float rounded(float a, float b) {
-#pragma clang fp contract(off)
-  return a * b;
-}
 
 __device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);

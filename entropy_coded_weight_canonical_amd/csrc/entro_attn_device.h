@@ -1,5 +1,6 @@
 // Device and host helpers shared by the attention and cache kernels
-// (entro_attn_prompt.hip, entro_kv.hip, entro_attn_cache.hip): element types,
+// (entro_attn_prompt.hip, entro_kv.hip, entro_rope.hip, entro_attn_cache.hip,
+// entro_attn_chunk.hip): element types,
 // matrix-core fragments, reductions, and the search that turns a workgroup's
 // number into a place in one of the call's sequences.
 #pragma once
@@ -91,6 +92,27 @@ __device__ __forceinline__ float add16(float v) {
   const uint32_t u = __builtin_bit_cast(uint32_t, v);
   const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
   return __builtin_bit_cast(float, (uint32_t)r[0]) + __builtin_bit_cast(float, (uint32_t)r[1]);
+}
+
+// Four codes of a word as two pairs of f16: the code plus 128 in the low byte
+// of 1024's bits, less 1152 (exact).
+__device__ __forceinline__ u32x2 half4(uint32_t w) {
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  const uint32_t u = w ^ 0x80808080u;
+  const h2 off = {(_Float16)1152.0f, (_Float16)1152.0f};
+  const uint32_t lo = __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u), hi = __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u);
+  return (u32x2){__builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, lo) - off),
+                 __builtin_bit_cast(uint32_t, __builtin_bit_cast(h2, hi) - off)};
+}
+__device__ __forceinline__ f16v8 half8(uint32_t w0, uint32_t w1) {
+  const u32x2 a = half4(w0), b = half4(w1);
+  return __builtin_bit_cast(f16v8, (u32x4){a.x, a.y, b.x, b.y});
+}
+
+// a b, rounded, whatever follows.
+__device__ __forceinline__ float rounded(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
 }
 
 // Factor of a part with maximum m where the parts' is `all`: parts without

@@ -32,6 +32,10 @@ struct {
   decltype(&entro_kv_load) load;
   decltype(&entro_attn_cache) cache;
   decltype(&entro_attn_cache_work_bytes) cache_bytes;
+  decltype(&entro_rope) rope;
+  decltype(&entro_kv_append) append;
+  decltype(&entro_attn_chunk) chunk;
+  decltype(&entro_attn_chunk_work_bytes) chunk_bytes;
   PyObject *raw_stream, *check, *desc;
 } g;
 
@@ -106,16 +110,24 @@ struct CacheDesc {
   int64_t gpu;
   at::Device device() const { return {at::kCUDA, (at::DeviceIndex)gpu}; }
 };
-CacheDesc cache_of(PyObject *cache) {
-  PyObject *desc = PyObject_GetAttr(cache, g.desc);
+// A Rotary's, made by rotary_desc.
+struct RotaryDesc {
+  entro_rotary r;
+  int64_t gpu;
+  at::Device device() const { return {at::kCUDA, (at::DeviceIndex)gpu}; }
+};
+template <typename Desc>
+Desc desc_of(PyObject *of, const char *expected) {
+  PyObject *desc = PyObject_GetAttr(of, g.desc);
   if (!desc) throw Raised();
-  CacheDesc c{};
+  Desc c{};
   const bool ok = PyBytes_Check(desc) && PyBytes_GET_SIZE(desc) == sizeof c;
   if (ok) std::memcpy(&c, PyBytes_AS_STRING(desc), sizeof c);
   Py_DECREF(desc);
-  if (!ok) refuse("cache: a KVCache expected");
+  if (!ok) refuse(expected);
   return c;
 }
+CacheDesc cache_of(PyObject *cache) { return desc_of<CacheDesc>(cache, "cache: a KVCache expected"); }
 
 struct On {
   bool make;          // memory may be made for the call
@@ -307,6 +319,206 @@ PyObject *cache(Args a) {
   return THPVariable_Wrap(std::move(out));
 }
 
+// q, cache, table, lens, cu_q, status, scale, out, work, make, stream -> out
+PyObject *chunk(Args a) {
+  const at::Tensor &q = tensor(a[0], "q"), &table = tensor(a[2], "table"), &lens = tensor(a[3], "lens");
+  const at::Tensor &cu_q = tensor(a[4], "cu_q"), &status = tensor(a[5], "status");
+  const CacheDesc desc = cache_of(a[1]);
+  const entro_kv_cache &c = desc.c;
+  at::Tensor out, work;
+  const Together together{desc.device()};
+  together("q", q)("table", table)("lens", lens)("cu_q", cu_q)("status", status);
+  if (a[7] != Py_None) together("out", out = tensor(a[7], "out"));
+  if (a[8] != Py_None) together("work", work = tensor(a[8], "work"));
+  const On on{a[9] == Py_True, a[10]};
+  if (q.dim() != 3) refuse("q is [rows][heads][dim]");
+  const int64_t n = table.dim() ? table.size(0) : 0, heads = q.size(1), dim = q.size(2);
+  if (dim != c.head_dim) refuse("q has head dimension ", dim, ", the cache ", c.head_dim);
+  const at::ScalarType t = q.scalar_type();
+  entro_attn_chunk_args p{};
+  p.dtype = (entro_dtype)type_of(q);
+  if (!out.defined())
+    out = on.empty(q.sizes(), t, q);
+  else if (out.dim() == 3 && out.size(0) != q.size(0))
+    refuse("out has the rows of q");
+  p.out = rows(out, "out", t, heads, dim);
+  p.q = rows(q, "q", t, heads, dim);
+  p.total_q = small(q.size(0), "q");
+  p.n_heads = small(heads, "q");
+  p.d_lens = static_cast<int32_t *>(ints(lens, "lens", n));
+  p.d_cu_q = static_cast<int32_t *>(ints(cu_q, "cu_q", n + 1));
+  p.scale = scale_of(a[6], dim);
+  if (!work.defined()) {
+    const uint64_t bytes = g.chunk_bytes(small(n, "table"), p.total_q, p.n_heads, c.n_kv_heads, c.head_dim);
+    if (bytes) work = on.empty({(int64_t)bytes}, at::kByte, q);
+  }
+  if (work.defined()) std::tie(p.d_work, p.work_bytes) = workspace(work);
+  const entro_kv_table tb = table_of(table, n);
+  uint32_t *const flags = static_cast<uint32_t *>(ints(status, "status", n));
+  const c10::DeviceGuard guard(q.device());
+  done(g.chunk(&c, &tb, &p, flags, on.handle(q)), "entro_attn_chunk");
+  return THPVariable_Wrap(std::move(out));
+}
+
+// Positions of a call's rows on the axes of r; a tensor of one dimension is one axis.
+const int32_t *positions_of(const at::Tensor &x, const entro_rotary &r, int64_t rows, int64_t *stride) {
+  const bool flat = x.dim() == 1 && r.n_axes == 1;
+  if (x.scalar_type() != at::kInt || !x.is_cuda() || !(flat || (x.dim() == 2 && x.size(0) == r.n_axes)) || x.size(-1) != rows)
+    refuse("positions: int32 [", r.n_axes, "][", rows, "] on the GPU expected, got ", x.scalar_type(), " ", x.sizes(), " on ",
+           x.device());
+  if (rows > 1 && x.stride(-1) != 1) refuse("positions: those of an axis have to lie side by side");
+  *stride = r.n_axes > 1 ? x.stride(0) : 0;
+  return static_cast<const int32_t *>(x.data_ptr());
+}
+
+// An operand of 32 or 16 bits, and the type of what it becomes: float16 or bfloat16.
+entro_dtype in_type(const at::Tensor &x) {
+  if (x.scalar_type() == at::kFloat) return ENTRO_F32;
+  if (x.scalar_type() == at::kBFloat16) return ENTRO_BF16;
+  if (x.scalar_type() == at::kHalf) return ENTRO_F16;
+  refuse("element type ", x.scalar_type(), ": float32, bfloat16 or float16 expected");
+}
+
+// rotary, q, k, positions, type of the results as bf16 (False) or f16 (True), q_out, k_out, make, stream -> (q, k)
+PyObject *rope(Args a) {
+  const RotaryDesc r = desc_of<RotaryDesc>(a[0], "rotary: a Rotary expected");
+  const at::Tensor &positions = tensor(a[3], "positions");
+  const Together together{r.device()};
+  at::Tensor x[2], out[2];
+  static const char *const kNames[2] = {"q", "k"}, *const kOuts[2] = {"q_out", "k_out"};
+  for (int i = 0; i < 2; ++i) {
+    if (a[1 + i] != Py_None) together(kNames[i], x[i] = tensor(a[1 + i], kNames[i]));
+    if (a[5 + i] == Py_None) continue;
+    if (!x[i].defined()) refuse(kOuts[i], ": there is no ", kNames[i]);
+    together(kOuts[i], out[i] = tensor(a[5 + i], kOuts[i]));
+  }
+  together("positions", positions);
+  const On on{a[7] == Py_True, a[8]};
+  const at::Tensor &first = x[0].defined() ? x[0] : x[1];
+  if (!first.defined()) refuse("q or k expected");
+  if (first.dim() != 3) refuse("q and k are [rows][heads][dim]");
+  const int64_t n = first.size(0), dim = first.size(2);
+  entro_rope_args p{};
+  p.in = in_type(first);
+  const at::ScalarType t = a[4] == Py_True ? at::kHalf : at::kBFloat16;
+  p.out = t == at::kHalf ? ENTRO_F16 : ENTRO_BF16;
+  p.rows = small(n, "rows");
+  p.head_dim = small(dim, "dim");
+  p.d_pos = positions_of(positions, r.r, n, &p.pos_stride);
+  for (int i = 0; i < 2; ++i) {
+    if (!x[i].defined()) continue;
+    if (x[i].dim() != 3 || x[i].size(0) != n) refuse("q and k have the same rows");
+    const int64_t heads = x[i].size(1);
+    (i ? p.k : p.q) = rows(x[i], kNames[i], first.scalar_type(), heads, dim);
+    if (!out[i].defined()) out[i] = on.empty(x[i].sizes(), t, x[i]);
+    if (out[i].dim() == 3 && out[i].size(0) != n) refuse(kOuts[i], " has the rows of ", kNames[i]);
+    (i ? p.k_out : p.q_out) = rows(out[i], kOuts[i], t, heads, dim);
+    (i ? p.n_kv_heads : p.n_heads) = small(heads, kNames[i]);
+  }
+  const c10::DeviceGuard guard(first.device());
+  done(g.rope(&r.r, &p, on.handle(first)), "entro_rope");
+  PyObject *y[2];
+  for (int i = 0; i < 2; ++i) {
+    if (out[i].defined()) {
+      y[i] = THPVariable_Wrap(std::move(out[i]));
+    } else {
+      Py_INCREF(Py_None);
+      y[i] = Py_None;
+    }
+  }
+  PyObject *both = y[0] && y[1] ? PyTuple_Pack(2, y[0], y[1]) : nullptr;
+  Py_XDECREF(y[0]);
+  Py_XDECREF(y[1]);
+  return both;
+}
+
+// cache, rotary, k, v, table, held, cu_new, status, positions, q, type of its result as in rope, q_out, make, stream -> q_out
+PyObject *append(Args a) {
+  const CacheDesc desc = cache_of(a[0]);
+  const RotaryDesc r = desc_of<RotaryDesc>(a[1], "rotary: a Rotary expected");
+  const entro_kv_cache &c = desc.c;
+  const at::Tensor &k = tensor(a[2], "k"), &v = tensor(a[3], "v"), &table = tensor(a[4], "table");
+  const at::Tensor &held = tensor(a[5], "held"), &cu_new = tensor(a[6], "cu_new"), &status = tensor(a[7], "status");
+  at::Tensor positions, q, out;
+  const Together together{desc.device()};
+  if (r.device() != desc.device()) refuse("rotary: on device ", r.device(), ", the call is on ", desc.device());
+  together("k", k)("v", v)("table", table)("held", held)("cu_new", cu_new)("status", status);
+  if (a[8] != Py_None) together("positions", positions = tensor(a[8], "positions"));
+  if (a[9] != Py_None) together("q", q = tensor(a[9], "q"));
+  if (a[11] != Py_None) {
+    if (!q.defined()) refuse("q_out: there is no q");
+    together("q_out", out = tensor(a[11], "q_out"));
+  }
+  const On on{a[12] == Py_True, a[13]};
+  if (k.dim() != 3 || v.dim() != 3 || k.size(0) != v.size(0)) refuse("k and v have the same rows");
+  const int64_t n = table.dim() ? table.size(0) : 0, total = k.size(0);
+  entro_kv_append_args p{};
+  p.in = in_type(k);
+  const at::ScalarType t = a[10] == Py_True ? at::kHalf : at::kBFloat16;
+  p.out = t == at::kHalf ? ENTRO_F16 : ENTRO_BF16;
+  p.k = rows(k, "k", k.scalar_type(), c.n_kv_heads, c.head_dim);
+  p.v = rows(v, "v", k.scalar_type(), c.n_kv_heads, c.head_dim);
+  p.d_held = static_cast<int32_t *>(ints(held, "held", n));
+  p.d_cu_new = static_cast<int32_t *>(ints(cu_new, "cu_new", n + 1));
+  p.total_new = small(total, "k");
+  if (positions.defined()) p.d_pos = positions_of(positions, r.r, total, &p.pos_stride);
+  if (q.defined()) {
+    if (q.dim() != 3 || q.size(0) != total) refuse("q has the rows of k");
+    const int64_t heads = q.size(1);
+    p.q = rows(q, "q", k.scalar_type(), heads, c.head_dim);
+    if (!out.defined()) out = on.empty(q.sizes(), t, q);
+    if (out.dim() == 3 && out.size(0) != total) refuse("q_out has the rows of q");
+    p.q_out = rows(out, "q_out", t, heads, c.head_dim);
+    p.n_heads = small(heads, "q");
+  }
+  const entro_kv_table tb = table_of(table, n);
+  uint32_t *const flags = static_cast<uint32_t *>(ints(status, "status", n));
+  const c10::DeviceGuard guard(k.device());
+  done(g.append(&c, &tb, &r.r, &p, flags, on.handle(k)), "entro_kv_append");
+  if (!out.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(std::move(out));
+}
+
+// freqs, axes (a sequence of the pairs' axes, or None), interleaved, gain -> RotaryDesc as bytes
+PyObject *rotary_desc(Args a) {
+  const at::Tensor &freqs = tensor(a[0], "freqs");
+  if (freqs.scalar_type() != at::kFloat || freqs.dim() != 1 || !freqs.is_cuda() || !freqs.is_contiguous())
+    refuse("freqs: contiguous float32 [pairs] on the GPU expected, got ", freqs.scalar_type(), " ", freqs.sizes(), " on ",
+           freqs.device());
+  Together{freqs.device()}("freqs", freqs);
+  RotaryDesc d{};
+  d.gpu = freqs.device().index();
+  d.r.d_freqs = static_cast<const float *>(freqs.data_ptr());
+  const int64_t pairs = freqs.size(0);
+  if (pairs < 1 || pairs > 64 || pairs % 8) refuse("freqs: 8, 16, .. 64 pairs expected, got ", pairs);
+  d.r.pairs = (uint32_t)pairs;
+  d.r.n_axes = 1;
+  if (a[1] != Py_None) {
+    PyObject *axes = PySequence_Fast(a[1], "axes: a sequence expected");
+    if (!axes) throw Raised();
+    const bool fits = PySequence_Fast_GET_SIZE(axes) == pairs;
+    bool fine = true;
+    for (int64_t i = 0; fits && i < pairs; ++i) {
+      const long x = PyLong_AsLong(PySequence_Fast_GET_ITEM(axes, i));
+      if (x == -1 && PyErr_Occurred()) {
+        Py_DECREF(axes);
+        throw Raised();
+      }
+      if (x < 0 || x > 3) fine = false;
+      d.r.axes[i / 16] |= (uint32_t)(x & 3) << (2 * (i % 16));
+      d.r.n_axes = std::max<uint32_t>(d.r.n_axes, (uint32_t)(x & 3) + 1);
+    }
+    Py_DECREF(axes);
+    if (!fits || !fine) refuse("axes: the axis, 0 to 3, of each of the ", pairs, " pairs expected");
+  }
+  d.r.interleaved = PyObject_IsTrue(a[2]) == 1;
+  const double gain = PyFloat_AsDouble(a[3]);
+  if (PyErr_Occurred()) throw Raised();
+  d.r.gain = (float)gain;
+  if (!std::isfinite(d.r.gain)) refuse("gain: ", gain, " is not a finite 32-bit number");
+  return PyBytes_FromStringAndSize(reinterpret_cast<const char *>(&d), sizeof d);
+}
+
 // k_codes, v_codes, k_scales, v_scales -> CacheDesc as bytes
 PyObject *cache_desc(Args a) {
   const at::Tensor &k = tensor(a[0], "k_codes"), &v = tensor(a[1], "v_codes");
@@ -345,17 +557,23 @@ PyObject *entry(PyObject *, Args a, Py_ssize_t n) {
   return nullptr;
 }
 
-// The addresses of the library's six functions, raw_stream, check.
+// The addresses of the library's ten functions, raw_stream, check.
 PyObject *bind(PyObject *, PyObject *args) {
-  unsigned long long f[6];
+  unsigned long long f[10];
   PyObject *raw_stream, *check;
-  if (!PyArg_ParseTuple(args, "KKKKKKOO", f, f + 1, f + 2, f + 3, f + 4, f + 5, &raw_stream, &check)) return nullptr;
+  if (!PyArg_ParseTuple(args, "KKKKKKKKKKOO", f, f + 1, f + 2, f + 3, f + 4, f + 5, f + 6, f + 7, f + 8, f + 9, &raw_stream,
+                        &check))
+    return nullptr;
   g.prompt = reinterpret_cast<decltype(g.prompt)>(f[0]);
   g.prompt_bytes = reinterpret_cast<decltype(g.prompt_bytes)>(f[1]);
   g.store = reinterpret_cast<decltype(g.store)>(f[2]);
   g.load = reinterpret_cast<decltype(g.load)>(f[3]);
   g.cache = reinterpret_cast<decltype(g.cache)>(f[4]);
   g.cache_bytes = reinterpret_cast<decltype(g.cache_bytes)>(f[5]);
+  g.rope = reinterpret_cast<decltype(g.rope)>(f[6]);
+  g.append = reinterpret_cast<decltype(g.append)>(f[7]);
+  g.chunk = reinterpret_cast<decltype(g.chunk)>(f[8]);
+  g.chunk_bytes = reinterpret_cast<decltype(g.chunk_bytes)>(f[9]);
   Py_INCREF(raw_stream);
   Py_INCREF(check);
   Py_XSETREF(g.raw_stream, raw_stream);
@@ -370,8 +588,16 @@ PyMethodDef method(const char *name) {
 }
 
 PyMethodDef methods[] = {
-    method<prompt, 11>("attn_prompt"), method<store, 9>("kv_store"),        method<load, 11>("kv_load"),
-    method<cache, 10>("attn_cache"),   method<cache_desc, 4>("cache_desc"), {"bind", bind, METH_VARARGS, nullptr},
+    method<prompt, 11>("attn_prompt"),
+    method<store, 9>("kv_store"),
+    method<load, 11>("kv_load"),
+    method<cache, 10>("attn_cache"),
+    method<rope, 9>("rope"),
+    method<append, 14>("kv_append"),
+    method<chunk, 11>("attn_chunk"),
+    method<cache_desc, 4>("cache_desc"),
+    method<rotary_desc, 4>("rotary_desc"),
+    {"bind", bind, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,19 +1,20 @@
 /*
- * entro_attn.h - attention and the 8-bit key/value cache beside the coded
- * weight products of entro.h (MI355X, gfx950).
+ * entro_attn.h - attention, rotary positions and the 8-bit key/value cache
+ * beside the coded weight products of entro.h (MI355X, gfx950).
  *
  * The fused products turn activations into queries, keys and values and take
- * the attention's output back; the four entry points here do what lies
- * between: causal attention of packed prompts (entro_attn_prompt), keys and
- * values into a paged 8-bit cache (entro_kv_store) and back to 16 bits
- * (entro_kv_load), and attention of one new token per sequence over the cache
- * (entro_attn_cache).
+ * the attention's output back; the entry points here do what lies between:
+ * rotary positions (entro_rope), causal attention of packed prompts
+ * (entro_attn_prompt), keys and values into a paged 8-bit cache as they are
+ * (entro_kv_store) or with the rotation applied on the way (entro_kv_append) and
+ * back to 16 bits (entro_kv_load), and attention over the cache, of one new token
+ * per sequence (entro_attn_cache) or of a chunk of them (entro_attn_chunk).
  *
  * Heads.  n_heads query heads, n_kv_heads key/value heads; n_kv_heads divides
  * n_heads and query head h reads key/value head h / (n_heads / n_kv_heads).
  * head_dim is 64, 96 or 128.
  *
- * 16-bit operands (q, k, v, out) are indexed [token][head][dim]: element
+ * Operands (q, k, v, out; 16 bits but where said otherwise) are indexed [token][head][dim]: element
  * (t, h, d) at t * stride_t + h * stride_h + d, strides in elements, so that
  * slices of a joint projection need no copy.  Pointers are 16-byte aligned and
  * strides multiples of 8 (ENTRO_E_INVAL otherwise).  entro_attn_prompt takes
@@ -52,8 +53,9 @@
 extern "C" {
 #endif
 
-/* Element type of q, k, v and out. */
-typedef enum { ENTRO_BF16 = 0, ENTRO_F16 = 1 } entro_dtype;
+/* Element type of q, k, v and out.  ENTRO_F32, what the fused products write, is
+ * taken by entro_rope and entro_kv_append for their inputs. */
+typedef enum { ENTRO_BF16 = 0, ENTRO_F16 = 1, ENTRO_F32 = 2 } entro_dtype;
 
 /* Per-sequence faults OR-ed into d_status[b]. */
 #define ENTRO_F_LENGTH 0x40u /* running sums not ascending within the stated rows (one
@@ -63,7 +65,7 @@ typedef enum { ENTRO_BF16 = 0, ENTRO_F16 = 1 } entro_dtype;
 #define ENTRO_F_PAGE 0x80u   /* a page index outside the cache where tokens lie; the
                                 page is skipped                                       */
 
-/* A 16-bit operand's place and strides (elements). */
+/* An operand's place and strides (elements). */
 typedef struct {
   void *d;
   int64_t stride_t, stride_h;
@@ -185,6 +187,90 @@ uint64_t entro_attn_cache_work_bytes(uint32_t n_seq, uint32_t n_heads, uint32_t 
  * pages). */
 entro_status entro_attn_cache(const entro_kv_cache *c, const entro_kv_table *t, const entro_attn_cache_args *a,
                               uint32_t *d_status, hipStream_t stream);
+
+/* Attention of a chunk of new tokens per sequence over the cache, in which the
+ * chunk's own keys and values are already (entro_kv_append, entro_kv_store). */
+typedef struct {
+  entro_rows q, out;       /* the chunks of all sequences, packed */
+  const int32_t *d_cu_q;   /* [n_seq + 1] */
+  const int32_t *d_lens;   /* [n_seq] tokens of sequence b in the cache, its chunk's among them */
+  uint32_t total_q;        /* rows at q and out */
+  uint32_t n_heads;
+  entro_dtype dtype;
+  float scale;             /* factor of q . k, finite */
+  void *d_work;            /* entro_attn_chunk_work_bytes, 16-byte aligned; contents irrelevant */
+  uint64_t work_bytes;
+} entro_attn_chunk_args;
+
+/* Bytes of workspace that entro_attn_chunk needs (0 where an argument is out of
+ * its range): the partial results of chunks whose tokens are split over
+ * workgroups. */
+uint64_t entro_attn_chunk_work_bytes(uint32_t n_seq, uint32_t total_q, uint32_t n_heads, uint32_t n_kv_heads,
+                                     uint32_t head_dim);
+
+/* For sequence b with Lq queries and L = d_lens[b] tokens in the cache, the last Lq
+ * of them the queries' own: as entro_attn_prompt with the cache's values, query i
+ * sees tokens 0 .. i + L - Lq; a query with no token (L < Lq, or L = 0) gives 0.
+ * Tokens outside a query's range have no influence on it, but for page 0 and for
+ * its scales as said above.  Codes are taken exactly; q is held in 16 bits after a
+ * power of two per query and head (exact but for values below 2^-17 of the row's
+ * largest, which are rounded at 2^-25 of it), the weights in f16 for the product
+ * with the values, everything else in 32 bits.  The result does not depend on
+ * timing.  Row strides up to 2^31 - 1 elements; at most 2^31 - 1 rows. */
+entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv_table *t, const entro_attn_chunk_args *a,
+                              uint32_t *d_status, hipStream_t stream);
+
+/* Rotary positions.  The first 2 * pairs elements of a head are pairs, (i, i + pairs)
+ * or, interleaved, (2 i, 2 i + 1); pair i's angle is position * d_freqs[i], and
+ *   (x, y) -> gain * (x cos - y sin, y cos + x sin).
+ * Further elements are left as they are.  A token has a position on each of n_axes
+ * axes (1 for text; time, height and width of an image's or video's patches, for
+ * one) and each pair belongs to one of them.  Positions are any 32-bit integers:
+ * angles are computed in 64 bits and brought to one turn there, cosine and sine are
+ * then taken in 32 bits (off by at most 2^-21). */
+typedef struct {
+  const float *d_freqs;    /* [pairs] radians per position */
+  uint32_t pairs;          /* a multiple of 8, at most head_dim / 2 */
+  uint32_t n_axes;         /* 1 to 4 */
+  uint32_t axes[4];        /* pair i's axis: two bits of axes[i / 16] from bit 2 (i % 16) on, below n_axes */
+  uint32_t interleaved;    /* 0 or 1 */
+  float gain;              /* finite */
+} entro_rotary;
+
+typedef struct {
+  entro_rows q, q_out;     /* [rows][n_heads][head_dim] */
+  entro_rows k, k_out;     /* [rows][n_kv_heads][head_dim] */
+  const int32_t *d_pos;    /* position of row t on axis a at a * pos_stride + t */
+  int64_t pos_stride;      /* 0 or more; any with one axis */
+  uint32_t rows;
+  uint32_t n_heads, n_kv_heads;   /* either may be 0: no such operand */
+  uint32_t head_dim;
+  entro_dtype in, out;     /* of q and k, and (16 bits) of the outputs */
+} entro_rope_args;
+
+/* Rotate rows of queries and keys in one launch, rounded once.  An output may be
+ * its own input (the same place, type and strides); they must not overlap
+ * otherwise. */
+entro_status entro_rope(const entro_rotary *r, const entro_rope_args *a, hipStream_t stream);
+
+typedef struct {
+  entro_rows k, v;         /* the new tokens of all sequences, packed; k not rotated yet */
+  entro_rows q, q_out;     /* their queries, and where they go rotated */
+  const int32_t *d_held;   /* [n_seq] tokens that sequence b has in the cache before the call */
+  const int32_t *d_cu_new; /* [n_seq + 1] */
+  const int32_t *d_pos;    /* as in entro_rope_args, or NULL: a token's position is its place in its
+                              sequence (d_held[b] for the first new one), on every axis */
+  int64_t pos_stride;
+  uint32_t total_new;      /* rows at k, v, q and q_out */
+  uint32_t n_heads;        /* 0: no queries */
+  entro_dtype in, out;     /* of k, v and q, and (16 bits) of q_out */
+} entro_kv_append_args;
+
+/* entro_kv_store with the keys rotated on the way, in 32 bits (they are not rounded
+ * to 16 bits in between, nor are 32-bit values), and the queries of the same tokens
+ * rotated in the same launch as by entro_rope. */
+entro_status entro_kv_append(const entro_kv_cache *c, const entro_kv_table *t, const entro_rotary *r,
+                             const entro_kv_append_args *a, uint32_t *d_status, hipStream_t stream);
 
 /* entro_set_max_workgroups for the launches of this header: at most n
  * workgroups each from now on (0, the default: no cap); returns the cap before. */

@@ -93,3 +93,39 @@ def rows_of(k_codes, v_codes, k_scales, v_scales, table, first, count):
         k[i] = k_codes[p, :, r].astype(np.float32) * k_scales[p][:, None]
         v[i] = v_codes[p, :, :, r].astype(np.float32) * v_scales[p][:, None]
     return k, v
+
+
+def rotate(x, positions, freqs, axes=None, interleaved=False, gain=1.0):
+    """Rotary positions: x [rows][heads][dim], positions [axes][rows], freqs
+    [pairs] -> (rotated x, and for each element the sum |x| + |y| of its pair that
+    errors go by; elements that stay as they are: 0)."""
+    x = np.asarray(x, np.float64)
+    n = len(freqs)
+    axes = [0] * n if axes is None else axes
+    out, size = x.copy(), np.zeros_like(x)
+    for i in range(n):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + n)
+        # the product of two 32-bit numbers is exact in 64 bits up to 2^53
+        angle = np.asarray(positions[axes[i]], np.float64) * np.float64(np.float32(freqs[i]))
+        c, s = np.cos(angle)[:, None] * gain, np.sin(angle)[:, None] * gain
+        out[..., a] = x[..., a] * c - x[..., b] * s
+        out[..., b] = x[..., b] * c + x[..., a] * s
+        size[..., a] = size[..., b] = abs(gain) * (np.abs(x[..., a]) + np.abs(x[..., b]))
+    return out, size
+
+
+def chunk(q, keys, values, lens, cu_q, scale):
+    """Attention of chunks: q [rows][heads][dim], keys[b] and values[b] [tokens][kv
+    heads][dim] of sequence b, the last of its lens[b] tokens the chunk's own ->
+    (outputs, weighted means of |v|, largest |score|) as from prompt()."""
+    rows, heads, dim = q.shape
+    out, mean, top = np.zeros((rows, heads, dim)), np.zeros((rows, heads, dim)), np.zeros((rows, heads))
+    for b in range(len(lens)):
+        group = heads // keys[b].shape[1]
+        count = int(cu_q[b + 1] - cu_q[b])
+        for i in range(count):
+            n = max(0, int(lens[b]) - count + i + 1)
+            for h in range(heads):
+                r = int(cu_q[b]) + i
+                out[r, h], mean[r, h], top[r, h] = attend(q[r, h], keys[b][:n, h // group], values[b][:n, h // group], scale)
+    return out, mean, top
