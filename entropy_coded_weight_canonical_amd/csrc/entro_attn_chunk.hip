@@ -195,7 +195,7 @@ __device__ __forceinline__ Shares shares_of(const ChunkArg &a, uint64_t tiles) {
 struct State {
   float m, l, g, top;
 };
-constexpr float kUnit = 9.0f;    // the unit lies by about as much below top
+constexpr float kUnit = 11.5f;   // the unit lies by about as much below top
 
 // log2 of a page's value scale (below 2^-126: 0)
 struct Scale {
@@ -209,12 +209,240 @@ struct Scale {
   }
 };
 
+// A value of each four lanes in another order (0: the first one's), and the largest.
+template <int CTRL>
+__device__ __forceinline__ float quad(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, quad<0xB1>(v));      // 1, 0, 3, 2
+  return fmaxf(v, quad<0x4E>(v));   // 2, 3, 0, 1
+}
+
+// Instructions stay on their side of this place.
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+// The value, computed anew from here on: what follows from it is not kept in
+// registers from before.
+__device__ __forceinline__ uint32_t fresh(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// Changes in the registers that hold the value: written as an expression, the two
+// ways through a (rare) branch around it get registers of their own, and the common
+// way copies all of them every tile.  The matrix instructions' results are waited for
+// first.
+__device__ __forceinline__ void results_there() { asm volatile("s_nop 15\n\ts_nop 15"); }
+__device__ __forceinline__ void scale_in_place(f32x16 &o, float k) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    float x = o[r];
+    asm volatile("v_mul_f32 %0, %1, %0" : "+v"(x) : "v"(k));
+    o[r] = x;
+  }
+}
+// o = o k + z
+__device__ __forceinline__ void add_in_place(f32x16 &o, float k, const f32x16 &z) {
+#pragma unroll
+  for (int r = 0; r < 16; ++r) {
+    float x = o[r];
+    asm volatile("v_fma_f32 %0, %0, %1, %2" : "+v"(x) : "v"(k), "v"(z[r]));
+    o[r] = x;
+  }
+}
+// -infinity where token 16 b + j is not seen (16 b + j >= seen)
+__device__ __forceinline__ void hide_in_place(f32x16 &x, int b, int32_t seen) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float y = x[8 * (b & 1) + j];
+    asm volatile("v_cmp_lt_i32 vcc, %1, %2\n\ts_nop 1\n\tv_cndmask_b32 %0, %3, %0, vcc"
+                 : "+v"(y) : "n"(16 * b + j), "v"(seen), "v"(-INFINITY) : "vcc");
+    x[8 * (b & 1) + j] = y;
+  }
+}
+
+__device__ __forceinline__ f32x16 mfma(f16v8 a, f16v8 b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
 template <int D, int W>
 struct Lds {
   static constexpr uint32_t kRow = D * 2 + 16;          // bytes of a key's row and
   static constexpr uint32_t vRow = kTile * 2 + 16;      // of a dimension's: rows begin four banks further
   static constexpr uint32_t kBytes = kTile * kRow, vBytes = D * vRow, bytes = 2 * (kBytes + vBytes);
 };
+
+// A tile as a lane sees it.
+template <typename L>
+struct Tile {
+  const char *k, *v;   // the key that is its row of the first product, the dimension that is its row of the second
+  int32_t base;        // first token
+  float ks, vs, log;   // scales of block lane % 4, log2 of the value's
+  float most, least;   // of the four logarithms
+  __device__ f16v8 key(int half, int step) const {
+    return *reinterpret_cast<const f16v8 *>(k + 32 * half * (int)L::kRow + 32 * step);
+  }
+  __device__ f16v8 value(int d, int block) const {
+    return *reinterpret_cast<const f16v8 *>(v + 32 * d * (int)L::vRow + 16 * block);
+  }
+};
+
+// Products of H halves of the tile's keys, from half `from` on, with the queries;
+// between(i) goes between them.
+template <int H, typename L, int KS, typename Between>
+__device__ __forceinline__ void products(f32x16 *x, const Tile<L> &tile, int from, const f16v8 (&q)[KS], Between between) {
+  constexpr int N = H * KS, kAhead = N < 6 ? N : 6;   // reads ahead of their products
+  f16v8 w[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) w[i] = tile.key(from + i / KS, i % KS);
+  in_order();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i % KS == 0)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) x[i / KS][r] = 0.0f;
+    x[i / KS] = mfma(w[i % kAhead], q[i % KS], x[i / KS]);
+    if (i + kAhead < N) w[i % kAhead] = tile.key(from + (i + kAhead) / KS, (i + kAhead) % KS);
+    between(i);
+    in_order();
+  }
+}
+
+// A tile whose scales and scores are ordinary ones: weights go into the product with
+// their page's value scale, as 2^(t - m + log2(scale) - g), where g is held such that
+// the largest are 2^10 to 2^(15.9) (f16 has 11 bits from 2^-14 on), and come out of
+// its rounded weights for the sum.  m is raised only where it lags by more than kLag:
+// that is one pass over the outputs.  False, and nothing done, for tiles that are not
+// ordinary: values' scales more than a factor of 2^kSpread from one another or near the
+// ends of the range, keys' not finite or close to 0 (a hidden score is -infinity times
+// them), scores so far from 0 that a fused difference
+// would have a rounding of the score left over, values so far from the unit that moving
+// it could lose them.  (NaN fails.)
+constexpr float kLag = 3.0f, kSpread = 2.75f, kRoom = 12.875f;
+template <typename L, int DT>
+__device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x16 (&x)[2], const Tile<L> &tile, float c) {
+  float mx = -INFINITY;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    float most = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) most = fmaxf(most, x[b >> 1][8 * (b & 1) + j]);
+    mx = fmaxf(mx, most * (lane_of(tile.ks, b) * c));
+  }
+  mx = max32(mx);
+  const bool move = !(tile.most - st.g <= kRoom + 0.025f && tile.least - st.g >= 10.0f);
+  const float g = move ? tile.most - kRoom : st.g;
+  const auto near = [](float y) { return (fabsf(y) < 32768.0f) | (y == -INFINITY); };
+  const bool fine = (tile.ks < INFINITY) & (tile.ks >= 0x1p-60f) & (c >= 0x1p-60f) & (fabsf(tile.log) < 100.0f) & (tile.most - tile.least <= kSpread) & near(mx) & near(st.m) &
+                    (!move | (st.top == -INFINITY) | (fabsf(g - st.g) <= 60.0f));
+  if (!__all(fine)) return false;
+  if (__any(move | (mx > st.m + kLag))) {
+    const float m = fmaxf(st.m, mx), up = m == -INFINITY ? 0.0f : m - st.m, k = exp2_fast(-up);
+    const float ko = st.top == -INFINITY ? 0.0f : k * exp2_fast(st.g - g);
+    st.l *= k;
+    st.top -= up;
+    st.m = m;
+    st.g = g;
+    results_there();
+#pragma unroll
+    for (int d = 0; d < DT; ++d) scale_in_place(o[d], ko);
+  }
+  const float m = st.m == -INFINITY ? 0.0f : st.m, off = -st.g - m;
+  st.top = fmaxf(st.top, mx - m + tile.least);
+  const float unit = exp2_fast(st.g), rcp = __builtin_amdgcn_rcpf(tile.vs);
+  // the weights of the next 16 tokens between the products of these
+  u32x4 p[2];
+  float part = 0.0f, sum = 0.0f;
+  const auto pair = [&](int b, int j) {
+    const float sc = lane_of(tile.ks, b) * c, by = lane_of(tile.log, b) + off;
+    const float y0 = __builtin_fmaf(x[b >> 1][8 * (b & 1) + 2 * j], sc, by);
+    const float y1 = __builtin_fmaf(x[b >> 1][8 * (b & 1) + 2 * j + 1], sc, by);
+    p[b & 1][j] = Elem<ENTRO_F16>::pack2(exp2_fast(y0), exp2_fast(y1));
+    part = Elem<ENTRO_F16>::add2(p[b & 1][j], j ? part : 0.0f);
+    if (j == 3) sum = __builtin_fmaf(part, lane_of(rcp, b), sum);
+  };
+  f16v8 w[DT];
+#pragma unroll
+  for (int d = 0; d < DT; ++d) w[d] = tile.value(d, 0);
+  in_order();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) pair(0, j);
+#pragma unroll
+  for (int b = 0; b < 4; ++b)
+#pragma unroll
+    for (int d = 0; d < DT; ++d) {
+      o[d] = mfma(w[d], __builtin_bit_cast(f16v8, p[b & 1]), o[d]);
+      if (b < 3) {
+        w[d] = tile.value(d, b + 1);
+#pragma unroll
+        for (int j = 4 * d / DT; j < 4 * (d + 1) / DT; ++j) pair(b + 1, j);
+      }
+      in_order();
+    }
+  st.l = __builtin_fmaf(sum, unit, st.l);
+  return true;
+}
+
+// Any tile: 16 tokens at a time, the weights relative to their own largest and their
+// product's part brought to the outputs' unit in 32 bits, the unit to the values'.  A
+// block that a row does not see has no influence on it, whatever its scales are.
+template <typename L, int DT, int KS>
+__device__ __forceinline__ void slow_tile(State &st, f32x16 (&o)[DT], const f16v8 (&q)[KS], const Tile<L> &tile, float c,
+                                          int32_t seen) {
+#pragma unroll 1
+  for (int hh = 0; hh < 2; ++hh) {
+    f32x16 x;
+    products<1>(&x, tile, hh, q, [](int) {});
+#pragma unroll
+    for (int cc = 0; cc < 2; ++cc) {
+      const int blk = 2 * hh + cc;
+      const float sc = lane_of(tile.ks, blk) * c;
+      const Scale vs(lane_of(tile.vs, blk));
+      float mx = -kFloatMax, y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        y[j] = 16 * blk + j < seen ? rounded(x[8 * cc + j], sc) : -INFINITY;
+        mx = fmaxf(mx, y[j]);
+      }
+      const bool any = max32(16 * blk < seen ? 1.0f : 0.0f) != 0.0f;   // (the row's other lane may see one)
+      mx = max32(mx);
+      float sum = 0.0f;
+      u32x4 pw;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p0 = exp2_fast(y[2 * j] - mx), p1 = exp2_fast(y[2 * j + 1] - mx);
+        sum += p0 + p1;
+        pw[j] = Elem<ENTRO_F16>::pack2(p0 * 32768.0f, p1 * 32768.0f);
+      }
+      // the row's state with the block
+      const float m = fmaxf(st.m, mx), up = m - st.m, down = mx - m;
+      const float top = fmaxf(st.top - up, down + vs.log);
+      float g = st.g;
+      if (top > -kFloatMax && !(fabsf(top - kUnit - g) <= 30.0f)) g = top - kUnit;
+      const float keep = any ? exp2_fast(st.g - g - up) : 1.0f;
+      const float f = any && vs.part != 0.0f ? vs.part * exp2_fast(down + vs.whole - g - 15.0f) : 0.0f;
+      if (any) {
+        st.l = st.l * exp2_fast(-up) + sum * exp2_fast(down);
+        st.m = m;
+        st.g = g;
+        st.top = top;
+      }
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        in_order();   // one part of the outputs after another: registers
+        f32x16 z;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = 0.0f;
+        z = mfma(tile.value(d, blk), __builtin_bit_cast(f16v8, pw), z);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) z[i] = any ? z[i] * f : 0.0f;
+        results_there();
+        add_in_place(o[d], keep, z);
+      }
+      in_order();
+    }
+  }
+}
 
 // ---------------------------------------------------------------------------
 // One workgroup takes pieces of blocks for one key/value head.  A block's rows are
@@ -234,11 +462,10 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
   typedef Lds<D, W> L;
   constexpr int KS = D / 16;                       // products over the dimensions
   constexpr int DT = D / 32;                       // 32-dimension parts of the output
-  constexpr uint32_t kPieces = kTile * D / 16;     // 16-byte pieces of a tile's keys, and of its values
-  constexpr int PT = (kPieces + 64 * W - 1) / (64 * W);
+  constexpr int PT = 8 / W;                        // 16-byte pieces of a tile's keys, and of its values, for a thread
   constexpr uint32_t kRows = 32 * W;
   char *lds = reinterpret_cast<char *>(dyn_lds);
-  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = rfl(tid >> 6), col = lane & 31u, half = lane >> 5;
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = rfl(tid >> 6);
   const uint32_t page = 1u << a.page_log2;
   Place at(a, lane);
   if (blockIdx.x == 0u && blockIdx.y == 0u && wave == 0u) {
@@ -255,6 +482,8 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
     for (uint32_t w = blockIdx.y; w < sh.n; w += gridDim.y) {
       const uint32_t kvh = head_part / a.parts, h0 = head_part % a.parts * a.heads;
       const uint32_t heads = min(a.heads, a.group - h0), head0 = kvh * a.group + h0;
+      const uint32_t page_bytes = a.n_kv * page * D;   // from one page's codes to the next's, below 2^30
+      const int8_t *const kb = a.k_codes + (uint64_t)kvh * page * D, *const vb = a.v_codes + (uint64_t)kvh * page * D;
       uint64_t now = sh.begin(w);
       const uint64_t end = sh.begin(w + 1u);
       at.find(now);
@@ -265,22 +494,31 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
         const uint32_t t0 = (uint32_t)(now - at.before), t1 = (uint32_t)min((uint64_t)all_tiles, end - at.before);
         now = at.before + t1;
         const int32_t *row = a.table + (uint64_t)at.seq * a.table_stride;
-        // this lane's row; past the last, the last
         const uint32_t token0 = at.block << a.block_log2;
         const uint32_t rows = min(1u << a.block_log2, s.count - token0) * heads;
-        const uint32_t r = wave * 32u + col, rr = min(r, rows - 1u);
-        const uint32_t token = token0 + rr / heads, head = head0 + rr % heads;
         const bool active = wave * 32u < rows;
-        const int32_t limit = (int32_t)max((int64_t)0, blocks.ahead + token + 1);   // tokens that it sees
-        const int32_t most = __builtin_amdgcn_readlane(limit, 31);                   // and that the wavefront's last does
-
-        // the query as f16 times 2^-e, piece 2 s + half of its dimensions in the
-        // order in which the keys lie in LDS
-        f16v8 qf[KS];
-        float c = 0.0f;   // score = c * key scale * product
-        if (active) {
+        // a lane's row; past the last, the last
+        struct Row {
+          uint32_t token, head;
+        };
+        const auto row_of = [&](uint32_t ln) {
+          const uint32_t r = min(wave * 32u + (ln & 31u), rows - 1u);
+          return (Row){token0 + r / heads, head0 + r % heads};
+        };
+        // tokens that the lane's row sees, less the first one of the lane's eight
+        int32_t limit;
+        int32_t least, most;   // tokens that the wavefront's rows see
+        f16v8 qf[KS];          // the query as f16 times 2^-e, piece 2 i + lane / 32 of its dimensions as the keys lie in LDS
+        float c = 0.0f;        // score = c * key scale * product
+        {
+          const uint32_t ln = fresh(lane), half = ln >> 5;
+          const Row mine = row_of(ln);
+          limit = (int32_t)max((int64_t)0, blocks.ahead + mine.token + 1);
+          least = __builtin_amdgcn_readlane(limit, 0);
+          most = __builtin_amdgcn_readlane(limit, 31);
+          limit -= 8 * (int32_t)half;
           u32x4 raw[KS];
-          const char *q = a.q + ((int64_t)s.begin + token) * a.q_t + (int64_t)head * a.q_h;
+          const char *q = a.q + ((int64_t)s.begin + mine.token) * a.q_t + (int64_t)mine.head * a.q_h;
 #pragma unroll
           for (int i = 0; i < KS; ++i) {
             const uint32_t p = 2u * i + half;
@@ -293,7 +531,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
             for (int i = 0; i < KS; ++i)
               for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(Elem<T>::lo(raw[i][e])), fabsf(Elem<T>::hi(raw[i][e]))));
             top = max32(top);
-            e2 = (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;   // bf16 denormals: -127
+            e2 = top == 0.0f ? 0 : (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;   // bf16 denormals: -127
           }
           c = ldexpf(a.scale, e2);
 #pragma unroll
@@ -315,126 +553,137 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
           for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
         State st = {-INFINITY, 0.0f, 0.0f, -INFINITY};
 
-        // The page of 16-token block `lane % 4` of a tile, and its scales.  A block past
-        // the end, or of a page that does not exist, takes page 0.
+        // A tile's way: page numbers three tiles ahead, codes and scales two, f16 in LDS
+        // one.  (Past the piece's last tile the last is fetched again: no branches.)  A
+        // block past the sequence's end, or of a page that does not exist, takes page 0.
         bool bad = false;
-        const auto page_of = [&](uint32_t tile) {
-          const uint32_t t = tile * kTile + (lane & 3u) * 16u;
-          int32_t p = t < s.len ? row[t >> a.page_log2] : 0;
-          if ((uint32_t)p >= a.n_pages) {
-            bad = true;
-            p = 0;
-          }
-          return (uint32_t)p;
+        const uint32_t last = t1 - 1u;
+        const auto fetch_page = [&](uint32_t tile) {
+          return (uint32_t)row[min(min(tile, last) * kTile + (fresh(lane) & 3u) * 16u, max(s.len, 1u) - 1u) >> a.page_log2];
         };
+        const auto page_ok = [&](uint32_t p, uint32_t tile) {
+          const bool there = min(tile, last) * kTile + (fresh(lane) & 3u) * 16u < s.len;
+          bad |= there && p >= a.n_pages;
+          return there && p < a.n_pages ? p : 0u;
+        };
+        // A thread's pieces: 16 dimensions of a key, eight threads a key (all of a
+        // wavefront's eight keys on one page); 16 tokens of a dimension, four threads a
+        // dimension where a tile lies in one page, or all of a wavefront's 64 dimensions of
+        // one block, which lie side by side where pages are small.  In LDS a key's piece lies
+        // in two halves, D / 2 apart; a dimension's in two halves, 32 tokens apart.
+        const bool wide = page >= kTile;
+        const uint32_t k_block = wave / 2u, v_block = wide ? 0u : wave & 3u;   // of a wavefront's page
+        uint32_t k_from, k_to, v_from, v_to;
+        bool k_mine, v_mine[PT];
+        {
+          const uint32_t ln = fresh(lane), key = wave * 8u + ln / 8u, piece = ln % 8u;
+          k_mine = piece < D / 16u;
+          k_from = (key & (page - 1u)) * D + min(piece, D / 16u - 1u) * 16u;
+          k_to = key * L::kRow + piece * 16u;
+          const uint32_t dim = wide ? wave * 16u + ln / 4u : (wave / 4u) * 64u + ln, block = wide ? ln & 3u : wave & 3u;
+#pragma unroll
+          for (int i = 0; i < PT; ++i) v_mine[i] = dim + 64u * i < D;
+          v_from = (dim << a.page_log2) + (block * 16u & (page - 1u));
+          v_to = L::kBytes + dim * L::vRow + block * 16u;
+        }
         u32x4 kq[PT], vq[PT];
-        float ks = 0.0f, vs = 0.0f;
-        const auto fetch = [&](uint32_t tile, uint32_t pages) {
-          const uint64_t mine = (uint64_t)pages * a.n_kv + kvh;
-          ks = a.k_scales[mine];
-          vs = a.v_scales[mine];
-#pragma unroll
-          for (int i = 0; i < PT; ++i) {
-            const uint32_t p = min(tid + 64u * W * i, kPieces - 1u);
-            const uint32_t tk = p / (D / 16u), dv = p / 4u, tv = p % 4u * 16u;
-            const uint64_t pk = (uint64_t)(uint32_t)__shfl((int)pages, (int)(tk / 16u)) * a.n_kv + kvh;
-            const uint64_t pv = (uint64_t)(uint32_t)__shfl((int)pages, (int)(p % 4u)) * a.n_kv + kvh;
-            const uint32_t in_k = (tile * kTile + tk) & (page - 1u), in_v = (tile * kTile + tv) & (page - 1u);
-            kq[i] = *reinterpret_cast<const u32x4 *>(a.k_codes + ((pk << a.page_log2) + in_k) * D + p % (D / 16u) * 16u);
-            vq[i] = *reinterpret_cast<const u32x4 *>(a.v_codes + ((pv * D + dv) << a.page_log2) + in_v);
-          }
+        const auto fetch_keys = [&](uint32_t tile, uint32_t pages, int i) {
+          const uint32_t p = lane_of(pages, k_block + 2u * i), in = (min(tile, last) * kTile + 32u * i) & (page - 1u);
+          kq[i] = *reinterpret_cast<const u32x4 *>(kb + ((uint64_t)p * page_bytes + in * D) + k_from);
         };
-        uint32_t pages = page_of(t0);
-        fetch(t0, pages);
-        if (t0 + 1u < t1) pages = page_of(t0 + 1u);
+        const auto fetch_values = [&](uint32_t tile, uint32_t pages, int i) {
+          const uint32_t p = lane_of(pages, v_block), in = (min(tile, last) * kTile) & (page - 1u);
+          const uint32_t further = v_mine[i] ? v_from + (64u * i << a.page_log2) : 0u;
+          vq[i] = *reinterpret_cast<const u32x4 *>(vb + ((uint64_t)p * page_bytes + in) + further);
+        };
+        const auto put = [&](uint32_t tile, int i, int which) {
+          char *to = lds + (tile & 1u) * (L::kBytes + L::vBytes);
+          if (which < 2 ? D < 128 && !k_mine : D < 64 * W / 4 * PT && !v_mine[i]) return;
+          char *kp = to + k_to + 32 * i * (int)L::kRow, *vp = to + v_to + 64 * i * (int)L::vRow;
+          if (which == 0) *reinterpret_cast<f16v8 *>(kp) = half8(kq[i].x, kq[i].y);
+          if (which == 1) *reinterpret_cast<f16v8 *>(kp + D) = half8(kq[i].z, kq[i].w);
+          if (which == 2) *reinterpret_cast<f16v8 *>(vp) = half8(vq[i].x, vq[i].y);
+          if (which == 3) *reinterpret_cast<f16v8 *>(vp + kTile) = half8(vq[i].z, vq[i].w);
+        };
+        uint32_t pages = page_ok(fetch_page(t0), t0);
+#pragma unroll
+        for (int i = 0; i < PT; ++i) {
+          fetch_keys(t0, pages, i);
+          fetch_values(t0, pages, i);
+        }
+        float ks0 = a.k_scales[(uint64_t)pages * a.n_kv + kvh], vs0 = a.v_scales[(uint64_t)pages * a.n_kv + kvh];
+        pages = page_ok(fetch_page(t0 + 1u), t0 + 1u);
+        uint32_t pages_raw = fetch_page(t0 + 2u);
+        float ks1 = a.k_scales[(uint64_t)pages * a.n_kv + kvh], vs1 = a.v_scales[(uint64_t)pages * a.n_kv + kvh];
+#pragma unroll
+        for (int i = 0; i < 4 * PT; ++i) put(t0, i / 4, i % 4);
+#pragma unroll
+        for (int i = 0; i < PT; ++i) {
+          fetch_keys(t0 + 1u, pages, i);
+          fetch_values(t0 + 1u, pages, i);
+        }
         for (uint32_t t = t0; t < t1; ++t) {
-          char *kt = lds + (t & 1u) * (L::kBytes + L::vBytes), *vt = kt + L::kBytes;
-          // the tile's codes as f16: a key's piece of 16 dimensions in two halves, D / 2
-          // apart; a dimension's 16 tokens in two halves, 32 apart
-#pragma unroll
-          for (int i = 0; i < PT; ++i) {
-            const uint32_t p = tid + 64u * W * i;
-            if (kPieces % (64u * W) && p >= kPieces) break;
-            char *kp = kt + p / (D / 16u) * L::kRow + p % (D / 16u) * 16u, *vp = vt + p / 4u * L::vRow + p % 4u * 16u;
-            *reinterpret_cast<f16v8 *>(kp) = half8(kq[i].x, kq[i].y);
-            *reinterpret_cast<f16v8 *>(kp + D) = half8(kq[i].z, kq[i].w);
-            *reinterpret_cast<f16v8 *>(vp) = half8(vq[i].x, vq[i].y);
-            *reinterpret_cast<f16v8 *>(vp + kTile) = half8(vq[i].z, vq[i].w);
-          }
-          const float ks_now = ks, vs_now = vs;
-          if (t + 1u < t1) {
-            fetch(t + 1u, pages);
-            if (t + 2u < t1) pages = page_of(t + 2u);
-          }
-          __syncthreads();
-          if (!active || (int64_t)t * kTile >= most) continue;
-#pragma unroll 1
-          for (int hh = 0; hh < 2; ++hh) {
-            f32x16 x;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-            const uint32_t kr = 32u * hh + ((col & 0x13u) | ((col & 4u) << 1) | ((col & 8u) >> 1));
-#pragma unroll
-            for (int i = 0; i < KS; ++i) {
-              const f16v8 kf = *reinterpret_cast<const f16v8 *>(kt + kr * L::kRow + (2 * i + half) * 16u);
-              x = __builtin_amdgcn_mfma_f32_32x32x16_f16(kf, qf[i], x, 0, 0, 0);
+          __syncthreads();   // tile t is there; the other buffer has been read
+          // the next tiles' way, one step after another
+          constexpr int kSteps = 6 * PT + 2;
+          float ks2, vs2;
+          const auto ahead = [&](int i) {
+            if (i < 4 * PT) {
+              put(t + 1u, i / 4, i % 4);
+            } else if (i == 4 * PT) {
+              pages = page_ok(pages_raw, t + 2u);
+              pages_raw = fetch_page(t + 3u);
+            } else if (i <= 5 * PT) {
+              fetch_keys(t + 2u, pages, i - 4 * PT - 1);
+            } else if (i <= 6 * PT) {
+              fetch_values(t + 2u, pages, i - 5 * PT - 1);
+            } else {
+              const uint64_t mine = (uint64_t)pages * a.n_kv + kvh;
+              ks2 = a.k_scales[mine];
+              vs2 = a.v_scales[mine];
             }
+          };
+          if (!active || (int64_t)t * kTile >= most) {
 #pragma unroll
-            for (int cc = 0; cc < 2; ++cc) {
-              const uint32_t blk = 2u * hh + cc;
-              const float sc = lane_of(ks_now, blk) * c;
-              const Scale vsc(lane_of(vs_now, blk));
-              const int32_t first = (int32_t)(t * kTile + 16u * blk), own = first + 8 * (int32_t)half;
-              const bool any = first < limit;
-              float mx = -kFloatMax, y[8];
+            for (int i = 0; i < kSteps; ++i) ahead(i);
+          } else {
+            const uint32_t ln = fresh(lane), col = ln & 31u, half = ln >> 5;
+            const char *kt = lds + (t & 1u) * (L::kBytes + L::vBytes), *vt = kt + L::kBytes;
+            const uint32_t kr = (col & 0x13u) | ((col & 4u) << 1) | ((col & 8u) >> 1);   // the token of row `col`
+            // (blocks past the end take the first one's scales)
+            const bool past = t * kTile + (ln & 3u) * 16u >= s.len;
+            const float k_first = quad<0x00>(ks0), v_first = quad<0x00>(vs0);
+            const float v_scale = past ? v_first : vs0, log = __log2f(v_scale);
+            const Tile<L> tile{kt + kr * L::kRow + half * 16u, vt + col * L::vRow + half * 64u, (int32_t)(t * kTile),
+                               past ? k_first : ks0, v_scale, log, quad_max(log), -quad_max(-log)};
+            f32x16 x[2];
+            products<2>(x, tile, 0, qf, [&](int i) {   // kSteps steps among 2 KS products
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                y[j] = own + j < limit ? rounded(x[8 * cc + j], sc) : -INFINITY;
-                mx = fmaxf(mx, y[j]);
-              }
-              mx = max32(mx);
-              float sum = 0.0f;
-              u32x4 pw;
+              for (int j = kSteps * i / (2 * KS); j < kSteps * (i + 1) / (2 * KS); ++j) ahead(j);
+            });
+            const int32_t seen = limit - tile.base;
+            if (tile.base + (int32_t)kTile > least) {
+              results_there();
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float p0 = exp2_fast(y[2 * j] - mx), p1 = exp2_fast(y[2 * j + 1] - mx);
-                sum += p0 + p1;
-                pw[j] = Elem<ENTRO_F16>::pack2(p0 * 32768.0f, p1 * 32768.0f);
-              }
-              // the row's state with the block
-              const float m = fmaxf(st.m, mx), up = m - st.m, down = mx - m;
-              const float top = fmaxf(st.top - up, down + vsc.log);
-              float g = st.g;
-              if (top > -kFloatMax && !(fabsf(top - kUnit - g) <= 30.0f)) g = top - kUnit;
-              const float keep = any ? exp2_fast(st.g - g - up) : 1.0f;
-              const float f = any && vsc.part != 0.0f ? vsc.part * exp2_fast(down + vsc.whole - g - 15.0f) : 0.0f;
-              if (any) {
-                st.l = st.l * exp2_fast(-up) + sum * exp2_fast(down);
-                st.m = m;
-                st.g = g;
-                st.top = top;
-              }
-#pragma unroll
-              for (int d = 0; d < DT; ++d) {
-                const f16v8 vf = *reinterpret_cast<const f16v8 *>(vt + (32u * d + col) * L::vRow + (blk + 4u * half) * 16u);
-                f32x16 z;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = 0.0f;
-                z = __builtin_amdgcn_mfma_f32_32x32x16_f16(vf, __builtin_bit_cast(f16v8, pw), z, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[d][i] = any ? o[d][i] * keep + z[i] * f : o[d][i];
-              }
+              for (int b = 0; b < 4; ++b) hide_in_place(x[b >> 1], b, seen);
             }
+            if (!fast_tile(st, o, x, tile, c)) slow_tile(st, o, qf, tile, c, seen);
           }
+          ks0 = ks1;
+          vs0 = vs1;
+          ks1 = ks2;
+          vs1 = vs2;
         }
         if (bad) atomicOr(a.status + at.seq, ENTRO_F_PAGE);
         __syncthreads();   // the tiles' places are written again
-        if (!active || r >= rows) continue;
+        const uint32_t ln = fresh(lane), half = ln >> 5, r = wave * 32u + (ln & 31u);
+        if (r >= rows) continue;
+        const Row mine = row_of(ln);
         const float l = add32(st.l);
         if (t1 - t0 == all_tiles) {
           const float whole = floorf(fminf(fmaxf(st.g, -400.0f), 400.0f));
           const float k = l == 0.0f ? 0.0f : exp2_fast(st.g - whole) / l;
-          char *to = a.out + ((int64_t)s.begin + token) * a.o_t + (int64_t)head * a.o_h;
+          char *to = a.out + ((int64_t)s.begin + mine.token) * a.o_t + (int64_t)mine.head * a.o_h;
 #pragma unroll
           for (int d = 0; d < DT; ++d)
 #pragma unroll

@@ -204,9 +204,17 @@ def test_chunk_hidden_places(ent, dtype):
         clean = torch.ones(76, dtype=torch.bool)
         clean[first[0]: 40] = False
         clean[43 + first[2]: 76] = False
-        b = g[clean].double() - a[clean].double()
-        assert (b.abs() <= 2 * ROUND[dtype] * a[clean].double().abs() + 2.0 ** -18).all()
+        assert alike(g[clean], a[clean], dtype)
         assert not torch.isfinite(g[~clean]).all(-1).any()
+
+
+def alike(x, y, dtype, vmax=0.04 * 127):
+    """Two results of one row over the cache of filled_cache(), by the operator's
+    ways for ordinary and for other tiles: each is off by its own rounding, and by the
+    weights' to f16, 2^-12 of a weighted mean of |v| (which is at most vmax; scores
+    and sums in 32 bits: within a tenth of that)."""
+    x, y = x.double(), y.double()
+    return bool(((x - y).abs() <= 2 * ROUND[dtype] * torch.maximum(x.abs(), y.abs()) + 2 * 1.1 * 2.0 ** -12 * vmax).all())
 
 
 def raw(ent, heads, dtype, page, new, lens, seed, edit, scale=None):
@@ -305,7 +313,7 @@ def test_chunk_queries_that_are_no_numbers(ent):
     bad = torch.zeros(43, 4, dtype=torch.bool, device="cuda")
     bad[3, 1] = bad[41, 0] = True
     assert not torch.isfinite(got[bad]).any() and torch.isfinite(got[~bad]).all()
-    assert ((got[~bad].double() - a[~bad].double()).abs() <= 2.0 ** -7 * a[~bad].double().abs() + 2.0 ** -18).all()
+    assert alike(got[~bad], a[~bad], "bf16")
 
 
 def test_chunk_flags(ent):
