@@ -9,7 +9,7 @@
 namespace entro {
 
 constexpr uint32_t kTile = 64;          // tokens of a step
-constexpr uint32_t kShareTiles = 4;     // least tiles of a workgroup's share
+constexpr uint32_t kShareTiles = 6;     // least work of a workgroup's share, in tiles
 constexpr float kFloatMax = 3.40282347e38f;
 
 struct ChunkArg {
@@ -32,6 +32,7 @@ struct ChunkArg {
   uint32_t q_xor;               // on a pair of q: the scale's sign
   float *part_o;                // [n_kv parts][shares][2][rows][D]
   f32x4 *part_s;                // [n_kv parts][shares][2][rows]: a row's State
+  u32x4 *cuts;                  // [shares]: see Cut
   uint32_t *status;
 };
 
@@ -50,17 +51,20 @@ __device__ __forceinline__ Seq chunk_seq(const ChunkArg &a, Spans &spans, uint32
 }
 
 // The blocks of a sequence: 2^L tokens each, the last one maybe fewer.  A block
-// has the tiles that its last token sees, and one at least.  L is a whole number so
-// that the tiles of a sequence's first blocks can be written down.
+// has the tiles that its last token sees, and one at least; its work is counted in
+// tiles, with kBegin for its queries' way in and its results' way out.  L is a whole
+// number so that the work of a sequence's first blocks can be written down.
+constexpr uint32_t kBegin = 2;
 struct Blocks {
   uint32_t L, n, count;
   int64_t ahead;   // tokens in front of the first query; below 0 where the first ones see none
   __device__ Blocks(uint32_t log2, const Seq &s)
       : L(log2), n((uint32_t)(((uint64_t)s.count + (1ull << log2) - 1u) >> log2)), count(s.count),
         ahead((int64_t)s.len - (int64_t)s.count) {}
-  // tiles of the first x blocks, all of them full: the sum over y = 1 .. x of
-  // max(1, ceil((ahead + 2^L y) / 64))
-  __device__ uint64_t full(uint32_t blocks) const {
+  // the work of the first x blocks, all of them full
+  __device__ uint64_t full(uint32_t x) const { return (uint64_t)x * kBegin + full_tiles(x); }
+  // their tiles: the sum over y = 1 .. x of max(1, ceil((ahead + 2^L y) / 64))
+  __device__ uint64_t full_tiles(uint32_t blocks) const {
     const int64_t x = blocks;
     if (L <= 6u) {   // ceil(ceil((ahead + 2^L y) / 2^L) / 2^(6 - L))
       const uint32_t j = 6u - L;
@@ -80,8 +84,9 @@ struct Blocks {
     const int64_t end = ahead + (int64_t)min(((uint64_t)b + 1u) << L, (uint64_t)count);
     return end > 0 ? (uint32_t)((end + kTile - 1) / kTile) : 1u;
   }
-  __device__ uint64_t all() const { return n ? full(n - 1u) + tiles(n - 1u) : 0u; }
-  // the block of tile t
+  __device__ uint32_t work(uint32_t b) const { return kBegin + tiles(b); }
+  __device__ uint64_t all() const { return n ? full(n - 1u) + work(n - 1u) : 0u; }
+  // the block of piece t of the work
   __device__ uint32_t of(uint64_t t) const {
     uint32_t lo = 0, hi = n - 1u;
     while (lo < hi) {
@@ -115,38 +120,48 @@ __device__ __forceinline__ float lane_of(float v, uint32_t lane) {
   return __builtin_bit_cast(float, lane_of(__builtin_bit_cast(uint32_t, v), lane));
 }
 
-// A place among the tiles of all sequences' blocks, one after another.
+// A place in the work of all sequences' blocks, one after another.
 struct Place {
   const ChunkArg &a;
   uint32_t lane;
   Spans spans;
-  uint32_t b0;       // own: of sequence b0 + lane
+  uint32_t b0;          // own: of sequence b0 + lane
   Seq own;
-  uint32_t seq;      // n_seq: past the last
+  uint64_t mine, run;   // its work, and with that of the lanes before
+  bool loaded;          // whether the first 64 sequences are there
+  uint32_t seq;         // n_seq: past the last
   uint32_t block;
-  uint64_t before;   // tiles before the block
+  uint64_t before;      // work before the block
   __device__ Place(const ChunkArg &arg, uint32_t lane_)
-      : a(arg), lane(lane_), spans(arg.cu, arg.total_q, arg.n_seq, lane_) {}
-  __device__ uint64_t count_all() {
-    uint64_t sum = 0;
-    for (b0 = 0; b0 < a.n_seq; b0 += 64u) {
-      own = chunk_seq(a, spans, b0);
-      sum += lane_of(wave_scan64(Blocks(a.block_log2, own).all()), 63u);
-    }
-    return sum;
+      : a(arg), lane(lane_), spans(arg.cu, arg.total_q, arg.n_seq, lane_), loaded(false) {}
+  __device__ void load(uint32_t at) {
+    b0 = at;
+    own = chunk_seq(a, spans, b0);
+    mine = Blocks(a.block_log2, own).all();
+    run = wave_scan64(mine);
   }
-  __device__ void find(uint64_t tile) {
+  __device__ uint64_t count_all() {
+    load(0u);
+    uint64_t sum = lane_of(run, 63u);
+    loaded = a.n_seq <= 64u;
+    for (uint32_t at = 64u; at < a.n_seq; at += 64u) {
+      load(at);
+      sum += lane_of(run, 63u);
+    }
+    return rfl64(sum);
+  }
+  __device__ void find(uint64_t place) {
     uint64_t sum = 0;
-    for (b0 = 0; b0 < a.n_seq; b0 += 64u) {
-      own = chunk_seq(a, spans, b0);
-      const uint64_t mine = Blocks(a.block_log2, own).all(), run = wave_scan64(mine);
-      const uint64_t past = __ballot(sum + run > tile);
+    for (uint32_t at = 0; at < a.n_seq; at += 64u) {
+      if (!loaded) load(at);   // (a chain of reads: 1 us)
+      loaded = false;
+      const uint64_t past = __ballot(sum + run > place);
       if (past) {
-        const uint32_t at = (uint32_t)__builtin_ctzll(past);
-        seq = rfl(b0 + at);
-        sum += lane_of(run - mine, at);
+        const uint32_t l = (uint32_t)__builtin_ctzll(past);
+        seq = rfl(at + l);
+        sum += lane_of(run - mine, l);
         const Blocks b(a.block_log2, here());
-        block = rfl(b.of(tile - sum));
+        block = rfl(b.of(place - sum));
         before = rfl64(sum + b.full(block));
         return;
       }
@@ -161,7 +176,7 @@ struct Place {
   // to the next block
   __device__ void next() {
     const Blocks b(a.block_log2, here());
-    before += b.tiles(block);
+    before += b.work(block);
     if (++block < b.n) return;
     block = 0u;
     while (++seq < a.n_seq) {
@@ -171,21 +186,42 @@ struct Place {
   }
 };
 
-// All tiles of a key/value head in equal shares (to one tile), one workgroup each and
-// as many as the GPU holds at once: share w has tiles begin(w) .. begin(w + 1) - 1.  A
-// share's part of one block is a piece; a block in one piece is finished by its
-// workgroup, the others' pieces are joined by the second kernel.  A share has at most
-// two pieces of blocks that it does not finish: one that lacks the block's first
-// tile, always the share's first (place 0), and one that has it, always its last
-// (place 1).
+// The work of a key/value head in equal shares (to one tile), one workgroup each and as
+// many as the GPU holds at once: share w is begin(w) .. begin(w + 1) - 1.  A share's
+// tiles of one block are a piece; a block in one piece is finished by its workgroup, the
+// others' pieces are joined by the second kernel.  A share has at most two pieces of
+// blocks that it does not finish: one that lacks the block's first tile, always the
+// share's first (place 0), and one that has it, always its last (place 1).
 struct Shares {
-  uint64_t tiles;
-  uint32_t n;
-  __device__ uint64_t begin(uint32_t w) const { return w * tiles / n; }
+  uint64_t work, each;   // of a share; the first `more` have one more
+  uint32_t n, more;
+  __device__ uint64_t begin(uint32_t w) const { return w * each + min(w, more); }
+  // the share of place t
+  __device__ uint32_t of(uint64_t t) const {
+    const uint64_t longer = more * (each + 1u);
+    const bool first = t < longer;
+    const uint64_t x = first ? t : t - longer, y = first ? each + 1u : each;
+    const uint32_t q = (x | y) >> 32 ? (uint32_t)(x / y) : (uint32_t)x / (uint32_t)y;
+    return first ? q : more + q;
+  }
 };
-__device__ __forceinline__ Shares shares_of(const ChunkArg &a, uint64_t tiles) {
-  return {tiles, (uint32_t)min((uint64_t)a.shares, max((uint64_t)1, tiles / kShareTiles))};
+__device__ __forceinline__ Shares shares_of(const ChunkArg &a, uint64_t work) {
+  Shares s;
+  s.work = work;
+  s.n = (uint32_t)min((uint64_t)a.shares, max((uint64_t)1, work / kShareTiles));
+  s.each = work >> 32 ? work / s.n : (uint32_t)work / s.n;
+  s.more = (uint32_t)(work - s.each * s.n);
+  return s;
 }
+// The tile of a block before which a share's begin or end cuts it; 0: before all.
+__device__ __forceinline__ uint32_t cut_at(uint64_t place, uint64_t before) {
+  return place > before + kBegin ? (uint32_t)(place - before - kBegin) : 0u;
+}
+
+// What the first kernel tells the second of each share's begin: where it is the first
+// cut in a block, the block's first row of q, its tokens, and its last share; else
+// (and for shares that there are not) no tokens.
+typedef u32x4 Cut;   // row, tokens, share, 0
 
 // What is known of a row (one query of one head) beside its outputs, in powers of
 // two: the largest score m, the weights' sum l relative to 2^m, and the exponent g
@@ -194,8 +230,15 @@ __device__ __forceinline__ Shares shares_of(const ChunkArg &a, uint64_t tiles) {
 // near it, so that outputs keep their bits whatever the pages' scales are.
 struct State {
   float m, l, g, top;
+  // of the weights: -g - m (m: 0 where nothing was seen), and 2^g
+  float off, unit;
+  __device__ void settle() {
+    off = -g - (m == -INFINITY ? 0.0f : m);
+    unit = exp2_fast(g);
+  }
 };
 constexpr float kUnit = 11.5f;   // the unit lies by about as much below top
+constexpr float kSpread = 2.75f; // and a tile's scales that are ordinary by as much from one another at most
 
 // log2 of a page's value scale (below 2^-126: 0)
 struct Scale {
@@ -272,13 +315,29 @@ struct Lds {
   static constexpr uint32_t kBytes = kTile * kRow, vBytes = D * vRow, bytes = 2 * (kBytes + vBytes);
 };
 
+// The scales of 16 blocks of 16 tokens, four tiles, in each 16 lanes.  Blocks past the
+// sequence's end have those of their tile's first.
+struct Scales {
+  float k, v, log, rcp;   // log2 and reciprocal of v
+  float most, least;      // of a tile's logarithms
+  uint64_t fine;          // lanes whose tile can be an ordinary one, see fast_tile
+  __device__ Scales(float ks, float vs, bool past) {
+    const float k0 = quad<0x00>(ks), v0 = quad<0x00>(vs);
+    k = past ? k0 : ks;
+    v = past ? v0 : vs;
+    log = __log2f(v);
+    rcp = __builtin_amdgcn_rcpf(v);
+    most = quad_max(log);
+    least = -quad_max(-log);
+    fine = __ballot(k < INFINITY && k >= 0x1p-60f && fabsf(log) < 100.0f && most - least <= kSpread);
+  }
+};
+
 // A tile as a lane sees it.
 template <typename L>
 struct Tile {
   const char *k, *v;   // the key that is its row of the first product, the dimension that is its row of the second
-  int32_t base;        // first token
-  float ks, vs, log;   // scales of block lane % 4, log2 of the value's
-  float most, least;   // of the four logarithms
+  uint32_t at;         // the lane that has its first block's scales
   __device__ f16v8 key(int half, int step) const {
     return *reinterpret_cast<const f16v8 *>(k + 32 * half * (int)L::kRow + 32 * step);
   }
@@ -318,48 +377,48 @@ __device__ __forceinline__ void products(f32x16 *x, const Tile<L> &tile, int fro
 // them), scores so far from 0 that a fused difference
 // would have a rounding of the score left over, values so far from the unit that moving
 // it could lose them.  (NaN fails.)
-constexpr float kLag = 3.0f, kSpread = 2.75f, kRoom = 12.875f;
+constexpr float kLag = 3.0f, kRoom = 12.875f;
 template <typename L, int DT>
-__device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x16 (&x)[2], const Tile<L> &tile, float c) {
-  float mx = -INFINITY;
+__device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x16 (&x)[2], const Tile<L> &tile,
+                                          const Scales &scales, float c) {
+  float sc[4], mx = -INFINITY;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {
+    sc[b] = lane_of(scales.k, tile.at + b) * c;
     float most = -INFINITY;
 #pragma unroll
     for (int j = 0; j < 8; ++j) most = fmaxf(most, x[b >> 1][8 * (b & 1) + j]);
-    mx = fmaxf(mx, most * (lane_of(tile.ks, b) * c));
+    mx = fmaxf(mx, most * sc[b]);
   }
   mx = max32(mx);
-  const bool move = !(tile.most - st.g <= kRoom + 0.025f && tile.least - st.g >= 10.0f);
-  const float g = move ? tile.most - kRoom : st.g;
-  const auto near = [](float y) { return (fabsf(y) < 32768.0f) | (y == -INFINITY); };
-  const bool fine = (tile.ks < INFINITY) & (tile.ks >= 0x1p-60f) & (c >= 0x1p-60f) & (fabsf(tile.log) < 100.0f) & (tile.most - tile.least <= kSpread) & near(mx) & near(st.m) &
-                    (!move | (st.top == -INFINITY) | (fabsf(g - st.g) <= 60.0f));
-  if (!__all(fine)) return false;
-  if (__any(move | (mx > st.m + kLag))) {
-    const float m = fmaxf(st.m, mx), up = m == -INFINITY ? 0.0f : m - st.m, k = exp2_fast(-up);
-    const float ko = st.top == -INFINITY ? 0.0f : k * exp2_fast(st.g - g);
+  const float most = lane_of(scales.most, tile.at), least = lane_of(scales.least, tile.at);
+  const bool move = !(most - st.g <= kRoom + 0.025f && least - st.g >= 10.0f), none = st.top == -INFINITY;
+  const bool rise = move || mx > st.m + kLag || none;
+  const float g = move ? most - kRoom : st.g, m = fmaxf(st.m, mx);
+  // (all of it before the outputs are touched: with ways out in between they are copied)
+  const bool near = (fabsf(m) < 32768.0f || m == -INFINITY) && (none || fabsf(g - st.g) <= 60.0f);
+  if ((scales.fine >> tile.at & 15u) != 15u || __any(rise && !near)) return false;
+  if (__any(rise)) {
+    const float up = m == -INFINITY ? 0.0f : m - st.m, k = exp2_fast(-up), ko = none ? 0.0f : k * exp2_fast(st.g - g);
     st.l *= k;
-    st.top -= up;
+    st.top = m == -INFINITY ? -INFINITY : fmaxf(st.top - up, g + kUnit);
     st.m = m;
     st.g = g;
+    st.settle();
     results_there();
 #pragma unroll
     for (int d = 0; d < DT; ++d) scale_in_place(o[d], ko);
   }
-  const float m = st.m == -INFINITY ? 0.0f : st.m, off = -st.g - m;
-  st.top = fmaxf(st.top, mx - m + tile.least);
-  const float unit = exp2_fast(st.g), rcp = __builtin_amdgcn_rcpf(tile.vs);
   // the weights of the next 16 tokens between the products of these
   u32x4 p[2];
   float part = 0.0f, sum = 0.0f;
   const auto pair = [&](int b, int j) {
-    const float sc = lane_of(tile.ks, b) * c, by = lane_of(tile.log, b) + off;
-    const float y0 = __builtin_fmaf(x[b >> 1][8 * (b & 1) + 2 * j], sc, by);
-    const float y1 = __builtin_fmaf(x[b >> 1][8 * (b & 1) + 2 * j + 1], sc, by);
+    const float by = lane_of(scales.log, tile.at + b) + st.off;
+    const float y0 = __builtin_fmaf(x[b >> 1][8 * (b & 1) + 2 * j], sc[b], by);
+    const float y1 = __builtin_fmaf(x[b >> 1][8 * (b & 1) + 2 * j + 1], sc[b], by);
     p[b & 1][j] = Elem<ENTRO_F16>::pack2(exp2_fast(y0), exp2_fast(y1));
     part = Elem<ENTRO_F16>::add2(p[b & 1][j], j ? part : 0.0f);
-    if (j == 3) sum = __builtin_fmaf(part, lane_of(rcp, b), sum);
+    if (j == 3) sum = __builtin_fmaf(part, lane_of(scales.rcp, tile.at + b), sum);
   };
   f16v8 w[DT];
 #pragma unroll
@@ -379,7 +438,7 @@ __device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x
       }
       in_order();
     }
-  st.l = __builtin_fmaf(sum, unit, st.l);
+  st.l = __builtin_fmaf(sum, st.unit, st.l);
   return true;
 }
 
@@ -388,7 +447,7 @@ __device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x
 // block that a row does not see has no influence on it, whatever its scales are.
 template <typename L, int DT, int KS>
 __device__ __forceinline__ void slow_tile(State &st, f32x16 (&o)[DT], const f16v8 (&q)[KS], const Tile<L> &tile, float c,
-                                          int32_t seen) {
+                                          int32_t seen, const Scales &scales) {
 #pragma unroll 1
   for (int hh = 0; hh < 2; ++hh) {
     f32x16 x;
@@ -396,8 +455,8 @@ __device__ __forceinline__ void slow_tile(State &st, f32x16 (&o)[DT], const f16v
 #pragma unroll
     for (int cc = 0; cc < 2; ++cc) {
       const int blk = 2 * hh + cc;
-      const float sc = lane_of(tile.ks, blk) * c;
-      const Scale vs(lane_of(tile.vs, blk));
+      const float sc = lane_of(scales.k, tile.at + blk) * c;
+      const Scale vs(lane_of(scales.v, tile.at + blk));
       float mx = -kFloatMax, y[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -442,6 +501,7 @@ __device__ __forceinline__ void slow_tile(State &st, f32x16 (&o)[DT], const f16v
       in_order();
     }
   }
+  st.settle();
 }
 
 // ---------------------------------------------------------------------------
@@ -476,10 +536,13 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
       if (b0 + lane < a.n_seq && !ok) atomicOr(a.status + b0 + lane, ENTRO_F_LENGTH);
     }
   }
-  const Shares sh = shares_of(a, rfl64(at.count_all()));
-  if (sh.tiles == 0u) return;
+  const Shares sh = shares_of(a, at.count_all());
+  const uint32_t units = sh.work ? sh.n : 0u;
+  if (blockIdx.x == 0u && tid == 0u && a.total_q)   // (without rows there is no workspace)
+    for (uint32_t w = blockIdx.y; w < a.shares; w += gridDim.y)
+      if (w >= units) a.cuts[w] = (Cut){0u, 0u, 0u, 0u};
   for (uint32_t head_part = blockIdx.x; head_part < a.n_kv * a.parts; head_part += gridDim.x)
-    for (uint32_t w = blockIdx.y; w < sh.n; w += gridDim.y) {
+    for (uint32_t w = blockIdx.y; w < units; w += gridDim.y) {
       const uint32_t kvh = head_part / a.parts, h0 = head_part % a.parts * a.heads;
       const uint32_t heads = min(a.heads, a.group - h0), head0 = kvh * a.group + h0;
       const uint32_t page_bytes = a.n_kv * page * D;   // from one page's codes to the next's, below 2^30
@@ -487,12 +550,22 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
       uint64_t now = sh.begin(w);
       const uint64_t end = sh.begin(w + 1u);
       at.find(now);
+      if (head_part == 0u) {
+        const Seq s = at.here();
+        const Blocks blocks(a.block_log2, s);
+        const uint32_t token0 = at.block << a.block_log2;
+        Cut cut = {s.begin + token0, min(1u << a.block_log2, s.count - token0), 0u, 0u};
+        if (!cut_at(now, at.before) || cut_at(sh.begin(w - 1u), at.before)) cut.y = 0u;   // none, or not the block's first
+        if (cut.y) cut.z = sh.of(at.before + blocks.work(at.block) - 1u);
+        if (tid == 0u) a.cuts[w] = cut;
+      }
       for (; now < end; at.next()) {
         const Seq s = at.here();
         const Blocks blocks(a.block_log2, s);
         const uint32_t all_tiles = blocks.tiles(at.block);
-        const uint32_t t0 = (uint32_t)(now - at.before), t1 = (uint32_t)min((uint64_t)all_tiles, end - at.before);
-        now = at.before + t1;
+        const uint32_t t0 = cut_at(now, at.before), t1 = min(all_tiles, cut_at(end, at.before));
+        now = at.before + blocks.work(at.block);
+        if (t0 == t1) continue;
         const int32_t *row = a.table + (uint64_t)at.seq * a.table_stride;
         const uint32_t token0 = at.block << a.block_log2;
         const uint32_t rows = min(1u << a.block_log2, s.count - token0) * heads;
@@ -547,25 +620,30 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
           }
         }
 
+        const bool plain = __all(c >= 0x1p-60f);   // see fast_tile
+
         f32x16 o[DT];
 #pragma unroll
         for (int d = 0; d < DT; ++d)
           for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
-        State st = {-INFINITY, 0.0f, 0.0f, -INFINITY};
+        State st = {-INFINITY, 0.0f, 0.0f, -INFINITY, 0.0f, 1.0f};
 
-        // A tile's way: page numbers three tiles ahead, codes and scales two, f16 in LDS
-        // one.  (Past the piece's last tile the last is fetched again: no branches.)  A
-        // block past the sequence's end, or of a page that does not exist, takes page 0.
+        // A tile's way: page numbers eight tiles ahead and scales four (of four tiles at
+        // once, 16 blocks in each 16 lanes), codes two, f16 in LDS one.  (Past the piece's
+        // last tile the last is fetched again: no branches.)  A block past the sequence's
+        // end, or of a page that does not exist, takes page 0.
         bool bad = false;
         const uint32_t last = t1 - 1u;
-        const auto fetch_page = [&](uint32_t tile) {
-          return (uint32_t)row[min(min(tile, last) * kTile + (fresh(lane) & 3u) * 16u, max(s.len, 1u) - 1u) >> a.page_log2];
+        const auto token_of = [&](uint32_t four) { return min(four, s.len / 256u) * 256u + (fresh(lane) & 15u) * 16u; };
+        const auto fetch_page = [&](uint32_t four) {
+          return (uint32_t)row[min(token_of(four), max(s.len, 1u) - 1u) >> a.page_log2];
         };
-        const auto page_ok = [&](uint32_t p, uint32_t tile) {
-          const bool there = min(tile, last) * kTile + (fresh(lane) & 3u) * 16u < s.len;
+        const auto page_ok = [&](uint32_t p, uint32_t four) {
+          const bool there = token_of(four) < s.len && four * 4u < t1;
           bad |= there && p >= a.n_pages;
           return there && p < a.n_pages ? p : 0u;
         };
+        const auto scale_at = [&](const float *scales, uint32_t p) { return scales[(uint64_t)p * a.n_kv + kvh]; };
         // A thread's pieces: 16 dimensions of a key, eight threads a key (all of a
         // wavefront's eight keys on one page); 16 tokens of a dimension, four threads a
         // dimension where a tile lies in one page, or all of a wavefront's 64 dimensions of
@@ -588,11 +666,11 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
         }
         u32x4 kq[PT], vq[PT];
         const auto fetch_keys = [&](uint32_t tile, uint32_t pages, int i) {
-          const uint32_t p = lane_of(pages, k_block + 2u * i), in = (min(tile, last) * kTile + 32u * i) & (page - 1u);
+          const uint32_t p = lane_of(pages, min(tile, last) % 4u * 4u + k_block + 2u * i), in = (min(tile, last) * kTile + 32u * i) & (page - 1u);
           kq[i] = *reinterpret_cast<const u32x4 *>(kb + ((uint64_t)p * page_bytes + in * D) + k_from);
         };
         const auto fetch_values = [&](uint32_t tile, uint32_t pages, int i) {
-          const uint32_t p = lane_of(pages, v_block), in = (min(tile, last) * kTile) & (page - 1u);
+          const uint32_t p = lane_of(pages, min(tile, last) % 4u * 4u + v_block), in = (min(tile, last) * kTile) & (page - 1u);
           const uint32_t further = v_mine[i] ? v_from + (64u * i << a.page_log2) : 0u;
           vq[i] = *reinterpret_cast<const u32x4 *>(vb + ((uint64_t)p * page_bytes + in) + further);
         };
@@ -605,74 +683,59 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
           if (which == 2) *reinterpret_cast<f16v8 *>(vp) = half8(vq[i].x, vq[i].y);
           if (which == 3) *reinterpret_cast<f16v8 *>(vp + kTile) = half8(vq[i].z, vq[i].w);
         };
-        uint32_t pages = page_ok(fetch_page(t0), t0);
+        uint32_t four = t0 / 4u, pages = page_ok(fetch_page(four), four);
+        const auto fetch = [&](uint32_t tile, uint32_t p) {
 #pragma unroll
-        for (int i = 0; i < PT; ++i) {
-          fetch_keys(t0, pages, i);
-          fetch_values(t0, pages, i);
-        }
-        float ks0 = a.k_scales[(uint64_t)pages * a.n_kv + kvh], vs0 = a.v_scales[(uint64_t)pages * a.n_kv + kvh];
-        pages = page_ok(fetch_page(t0 + 1u), t0 + 1u);
-        uint32_t pages_raw = fetch_page(t0 + 2u);
-        float ks1 = a.k_scales[(uint64_t)pages * a.n_kv + kvh], vs1 = a.v_scales[(uint64_t)pages * a.n_kv + kvh];
+          for (int i = 0; i < PT; ++i) {
+            fetch_keys(tile, p, i);
+            fetch_values(tile, p, i);
+          }
+        };
+        fetch(t0, pages);
+        float ks = scale_at(a.k_scales, pages), vs = scale_at(a.v_scales, pages);
+        uint32_t pages_next = page_ok(fetch_page(four + 1u), four + 1u), pages_raw = fetch_page(four + 2u);
 #pragma unroll
         for (int i = 0; i < 4 * PT; ++i) put(t0, i / 4, i % 4);
+        fetch(t0 + 1u, min(t0 + 1u, last) / 4u == four ? pages : pages_next);
+        for (uint32_t t = t0; t < t1; ++four) {
+          const Scales scales(ks, vs, token_of(four) >= s.len);
+          ks = scale_at(a.k_scales, pages_next);
+          vs = scale_at(a.v_scales, pages_next);
+          for (const uint32_t end4 = min(t1, 4u * four + 4u); t < end4; ++t) {
+            __syncthreads();   // tile t is there; the other buffer has been read
+            // the next tiles' way, one step after another
+            constexpr int kSteps = 6 * PT;
+            const uint32_t p2 = min(t + 2u, last) / 4u == four ? pages : pages_next;
+            const auto ahead = [&](int i) {
+              if (i < 4 * PT) put(t + 1u, i / 4, i % 4);
+              else if (i < 5 * PT) fetch_keys(t + 2u, p2, i - 4 * PT);
+              else fetch_values(t + 2u, p2, i - 5 * PT);
+            };
+            if (!active || (int64_t)t * kTile >= most) {
 #pragma unroll
-        for (int i = 0; i < PT; ++i) {
-          fetch_keys(t0 + 1u, pages, i);
-          fetch_values(t0 + 1u, pages, i);
-        }
-        for (uint32_t t = t0; t < t1; ++t) {
-          __syncthreads();   // tile t is there; the other buffer has been read
-          // the next tiles' way, one step after another
-          constexpr int kSteps = 6 * PT + 2;
-          float ks2, vs2;
-          const auto ahead = [&](int i) {
-            if (i < 4 * PT) {
-              put(t + 1u, i / 4, i % 4);
-            } else if (i == 4 * PT) {
-              pages = page_ok(pages_raw, t + 2u);
-              pages_raw = fetch_page(t + 3u);
-            } else if (i <= 5 * PT) {
-              fetch_keys(t + 2u, pages, i - 4 * PT - 1);
-            } else if (i <= 6 * PT) {
-              fetch_values(t + 2u, pages, i - 5 * PT - 1);
-            } else {
-              const uint64_t mine = (uint64_t)pages * a.n_kv + kvh;
-              ks2 = a.k_scales[mine];
-              vs2 = a.v_scales[mine];
+              for (int i = 0; i < kSteps; ++i) ahead(i);
+              continue;
             }
-          };
-          if (!active || (int64_t)t * kTile >= most) {
-#pragma unroll
-            for (int i = 0; i < kSteps; ++i) ahead(i);
-          } else {
             const uint32_t ln = fresh(lane), col = ln & 31u, half = ln >> 5;
             const char *kt = lds + (t & 1u) * (L::kBytes + L::vBytes), *vt = kt + L::kBytes;
             const uint32_t kr = (col & 0x13u) | ((col & 4u) << 1) | ((col & 8u) >> 1);   // the token of row `col`
-            // (blocks past the end take the first one's scales)
-            const bool past = t * kTile + (ln & 3u) * 16u >= s.len;
-            const float k_first = quad<0x00>(ks0), v_first = quad<0x00>(vs0);
-            const float v_scale = past ? v_first : vs0, log = __log2f(v_scale);
-            const Tile<L> tile{kt + kr * L::kRow + half * 16u, vt + col * L::vRow + half * 64u, (int32_t)(t * kTile),
-                               past ? k_first : ks0, v_scale, log, quad_max(log), -quad_max(-log)};
+            const Tile<L> tile{kt + kr * L::kRow + half * 16u, vt + col * L::vRow + half * 64u, t % 4u * 4u};
             f32x16 x[2];
             products<2>(x, tile, 0, qf, [&](int i) {   // kSteps steps among 2 KS products
 #pragma unroll
               for (int j = kSteps * i / (2 * KS); j < kSteps * (i + 1) / (2 * KS); ++j) ahead(j);
             });
-            const int32_t seen = limit - tile.base;
-            if (tile.base + (int32_t)kTile > least) {
+            const int32_t seen = limit - (int32_t)(t * kTile);
+            if ((int32_t)(t * kTile + kTile) > least) {
               results_there();
 #pragma unroll
               for (int b = 0; b < 4; ++b) hide_in_place(x[b >> 1], b, seen);
             }
-            if (!fast_tile(st, o, x, tile, c)) slow_tile(st, o, qf, tile, c, seen);
+            if (!plain || !fast_tile(st, o, x, tile, scales, c)) slow_tile(st, o, qf, tile, c, seen, scales);
           }
-          ks0 = ks1;
-          vs0 = vs1;
-          ks1 = ks2;
-          vs1 = vs2;
+          pages = pages_next;
+          pages_next = page_ok(pages_raw, four + 2u);
+          pages_raw = fetch_page(four + 3u);
         }
         if (bad) atomicOr(a.status + at.seq, ENTRO_F_PAGE);
         __syncthreads();   // the tiles' places are written again
@@ -708,54 +771,77 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
     }
 }
 
-// Joins the pieces of a split block: one workgroup for the first share that begins
-// inside the block and kJoinRows of its rows.  A thread has four dimensions of a row
-// and takes the pieces in the tokens' order.
-constexpr uint32_t kJoinRows = 8;
+// Joins the pieces of the blocks that were cut: kJoinSlots slots of D / 4 threads, four
+// dimensions each, for the first cut in a block.  A slot takes whole rows; where there
+// are many pieces the slots take every kJoinSlots-th piece of one row and are joined
+// over LDS.  Four pieces' reads at once; the order is the same in every call.
+constexpr uint32_t kJoinSlots = 8;
+struct Joined {
+  float m, l, g;   // of the pieces so far: as in State; g: -infinity where no value was added
+  f32x4 o;
+  // two of them, or one and a piece; factors from differences only
+  __device__ void add(float m1, float l1, float g1, f32x4 o1) {
+    if (m1 == -INFINITY && l1 == 0.0f) return;   // saw no token (a sum that is no number stays)
+    const float up = fmaxf(m, m1), d0 = m - up, d1 = m1 - up;
+    l = (m == -INFINITY ? 0.0f : l * exp2_fast(d0)) + l1 * exp2_fast(d1);
+    const float u0 = g == -INFINITY ? -INFINITY : g + d0, u1 = g1 + d1, unit = fmaxf(u0, u1);
+    if (unit != -INFINITY)   // (NaN passes)
+      o = o * (u0 == -INFINITY ? 0.0f : exp2_fast(u0 - unit)) + o1 * (u1 == -INFINITY ? 0.0f : exp2_fast(u1 - unit));
+    g = unit;
+    m = up;
+  }
+};
 template <entro_dtype T, int D, int W>
-__global__ __launch_bounds__(kJoinRows * D / 4) void attn_chunk_join_kernel(ChunkArg a) {
-  constexpr uint32_t kRows = 32 * W, kGroups = kRows / kJoinRows;
-  const uint32_t tid = threadIdx.x, lane = tid & 63u;
-  Place at(a, lane);
-  const Shares sh = shares_of(a, rfl64(at.count_all()));
-  for (uint32_t w = 1u + blockIdx.y; w < sh.n; w += gridDim.y) {
-    const uint64_t cut = sh.begin(w);
-    at.find(cut);
-    if (cut == at.before || sh.begin(w - 1u) > at.before) continue;
-    const Seq s = at.here();
-    const Blocks blocks(a.block_log2, s);
-    const uint64_t end = at.before + blocks.tiles(at.block);
-    const uint32_t token0 = at.block << a.block_log2, tokens = min(1u << a.block_log2, s.count - token0);
+__global__ __launch_bounds__(kJoinSlots * D / 4) void attn_chunk_join_kernel(ChunkArg a) {
+  constexpr uint32_t kRows = 32 * W, kGroups = kRows / kJoinSlots;
+  __shared__ Joined red[kJoinSlots][D / 4];
+  const uint32_t slot = threadIdx.x / (D / 4u), dq = threadIdx.x % (D / 4u);
+  for (uint32_t w = 1u + blockIdx.y; w < a.shares; w += gridDim.y) {
+    const Cut cut = a.cuts[w];
+    if (cut.y == 0u) continue;
+    const uint32_t pieces = rfl(cut.z) - w + 2u;
     for (uint64_t y = blockIdx.x; y < (uint64_t)a.n_kv * a.parts * kGroups; y += gridDim.x) {
-      const uint32_t head_part = (uint32_t)(y / kGroups), r = (uint32_t)(y % kGroups) * kJoinRows + tid / (D / 4u);
+      const uint32_t head_part = (uint32_t)(y / kGroups), group = (uint32_t)(y % kGroups);
       const uint32_t kvh = head_part / a.parts, h0 = head_part % a.parts * a.heads;
-      const uint32_t heads = min(a.heads, a.group - h0), head0 = kvh * a.group + h0;
-      if (r >= tokens * heads) continue;
-      const uint32_t d = tid % (D / 4u) * 4u;
-      float m = -INFINITY, l = 0.0f, g = -INFINITY;   // of the pieces so far: as in State
-      f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (uint32_t p = w - 1u; p < sh.n && (p < w || sh.begin(p) < end); ++p) {
-        const uint64_t place = (((uint64_t)head_part * a.shares + p) * 2u + (p < w)) * kRows + r;
-        const f32x4 q = a.part_s[place];
-        const f32x4 x = *reinterpret_cast<const f32x4 *>(a.part_o + place * D + d);
-        if (q.x == -INFINITY) continue;   // saw no token
-        const float up = fmaxf(m, q.x), mine = g + (m - up), its = q.z + (q.x - up);
-        l = (m == -INFINITY ? 0.0f : l * exp2_fast(m - up)) + q.y * exp2_fast(q.x - up);
-        const float unit = fmaxf(g == -INFINITY ? -INFINITY : mine, its);
-        if (unit != -INFINITY) {   // (NaN passes)
-          const float k0 = g == -INFINITY ? 0.0f : exp2_fast(mine - unit), k1 = q.z == -INFINITY ? 0.0f : exp2_fast(its - unit);
-          o = o * k0 + x * k1;
-        }
-        g = unit;
-        m = up;
-      }
-      const float whole = floorf(fminf(fmaxf(g, -400.0f), 400.0f));
-      const float k = l == 0.0f || g == -INFINITY ? l * 0.0f : exp2_fast(g - whole) / l;
-      float v[4];
+      const uint32_t heads = min(a.heads, a.group - h0), head0 = kvh * a.group + h0, rows = rfl(cut.y) * heads;
+      const uint64_t base = ((uint64_t)head_part * a.shares + w) * 2u * kRows;
+      // (steps of four pieces, one row after another in the first case)
+      const bool many = (rows + kGroups - 1u) / kGroups * ((pieces + 4u * kJoinSlots - 1u) / (4u * kJoinSlots)) < (pieces + 3u) / 4u;
+      for (uint32_t r0 = many ? group : group * kJoinSlots; r0 < rows; r0 += many ? kGroups : kRows) {
+        const uint32_t r = many ? r0 : min(r0 + slot, rows - 1u), step = many ? kJoinSlots : 1u;
+        Joined j = {-INFINITY, 0.0f, -INFINITY, {0.0f, 0.0f, 0.0f, 0.0f}};
+        for (uint32_t p0 = many ? slot : 0u; p0 < pieces; p0 += 4u * step) {
+          f32x4 q[4], x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = ldexpf(o[j] * k, (int)whole);
-      *reinterpret_cast<u32x2 *>(a.out + ((int64_t)s.begin + token0 + r / heads) * a.o_t + (int64_t)(head0 + r % heads) * a.o_h + d * 2u) =
-          (u32x2){Elem<T>::pack2(v[0], v[1]), Elem<T>::pack2(v[2], v[3])};
+          for (uint32_t i = 0; i < 4; ++i) {
+            // the first piece is share w - 1's last, the others are first ones
+            const uint32_t p = min(p0 + i * step, pieces - 1u);
+            const uint64_t place = p ? base + (uint64_t)(p - 1u) * 2u * kRows + r : base - kRows + r;
+            q[i] = a.part_s[place];
+            x[i] = *reinterpret_cast<const f32x4 *>(a.part_o + place * D + 4u * dq);
+          }
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i)
+            if (p0 + i * step < pieces) j.add(q[i].x, q[i].y, q[i].z, x[i]);
+        }
+        if (many) {
+          red[slot][dq] = j;
+          __syncthreads();
+          if (slot == 0u)
+            for (uint32_t i = 1; i < kJoinSlots; ++i) j.add(red[i][dq].m, red[i][dq].l, red[i][dq].g, red[i][dq].o);
+          __syncthreads();
+          if (slot) continue;
+        } else if (r0 + slot >= rows) {
+          continue;
+        }
+        const float whole = floorf(fminf(fmaxf(j.g, -400.0f), 400.0f));
+        const float k = j.l == 0.0f || j.g == -INFINITY ? j.l * 0.0f : exp2_fast(j.g - whole) / j.l;
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = ldexpf(j.o[i] * k, (int)whole);
+        *reinterpret_cast<u32x2 *>(a.out + ((int64_t)cut.x + r / heads) * a.o_t + (int64_t)(head0 + r % heads) * a.o_h + dq * 8u) =
+            (u32x2){Elem<T>::pack2(v[0], v[1]), Elem<T>::pack2(v[2], v[3])};
+      }
     }
   }
 }
@@ -769,14 +855,14 @@ struct Plan {
   uint32_t waves, heads, parts, block_log2, shares;
   uint64_t rows() const { return 32u * waves; }
 };
-static Plan plan_of(uint32_t n_seq, uint32_t total_q, uint32_t n_heads, uint32_t n_kv) {
+static Plan plan_of(uint32_t n_seq, uint32_t total_q, uint32_t n_heads, uint32_t n_kv, uint32_t head_dim) {
   Plan p{};
   const uint32_t group = n_heads / n_kv;
   p.waves = (uint64_t)total_q * group > 128ull * n_seq ? 8u : 4u;
   p.heads = std::min<uint32_t>(group, (uint32_t)p.rows());
   p.parts = (group + p.heads - 1u) / p.heads;
   while ((2u << p.block_log2) * p.heads <= p.rows()) ++p.block_log2;
-  p.shares = std::max(1u, (p.waves == 8u ? 256u : 512u) / (n_kv * p.parts));
+  p.shares = std::max(1u, (p.waves == 8u ? 256u : head_dim == 64u ? 768u : 512u) / (n_kv * p.parts));
   return p;
 }
 
@@ -786,9 +872,9 @@ static entro_status launch_chunk(const ChunkArg &a, hipStream_t s) {
   (void)hipGetLastError();
   hipLaunchKernelGGL((attn_chunk_kernel<T, D, W>), grid2(heads, a.shares), dim3(64 * W), lds, s, a);
   if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
-  if (a.shares > 1u) {
-    hipLaunchKernelGGL((attn_chunk_join_kernel<T, D, W>), grid2((uint64_t)heads * (32u * W / kJoinRows), a.shares - 1u),
-                       dim3(kJoinRows * D / 4), 0, s, a);
+  if (a.shares > 1u && a.total_q) {
+    hipLaunchKernelGGL((attn_chunk_join_kernel<T, D, W>), grid2((uint64_t)heads * (32u * W / kJoinSlots), a.shares - 1u),
+                       dim3(kJoinSlots * D / 4), 0, s, a);
     if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
   }
   return ENTRO_OK;
@@ -802,8 +888,8 @@ extern "C" uint64_t entro_attn_chunk_work_bytes(uint32_t n_seq, uint32_t total_q
                                                 uint32_t head_dim) {
   if (n_seq == 0 || total_q == 0 || total_q > 0x7FFFFFFFu || check_heads(n_heads, n_kv_heads, head_dim, ENTRO_BF16) != ENTRO_OK)
     return 0;
-  const Plan p = plan_of(n_seq, total_q, n_heads, n_kv_heads);
-  return (uint64_t)n_kv_heads * p.parts * p.shares * 2u * p.rows() * (head_dim + 4u) * 4u;
+  const Plan p = plan_of(n_seq, total_q, n_heads, n_kv_heads, head_dim);
+  return (uint64_t)n_kv_heads * p.parts * p.shares * 2u * p.rows() * (head_dim + 4u) * 4u + 16u * p.shares;
 }
 
 extern "C" entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv_table *t, const entro_attn_chunk_args *a,
@@ -822,7 +908,7 @@ extern "C" entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv
   }
   const uint64_t need = entro_attn_chunk_work_bytes(t->n_seq, a->total_q, a->n_heads, c->n_kv_heads, c->head_dim);
   if (need && (!a->d_work || (reinterpret_cast<uintptr_t>(a->d_work) & 15u) || a->work_bytes < need)) return ENTRO_E_INVAL;
-  const Plan p = plan_of(t->n_seq, a->total_q, a->n_heads, c->n_kv_heads);
+  const Plan p = plan_of(t->n_seq, a->total_q, a->n_heads, c->n_kv_heads, c->head_dim);
   ChunkArg k{};
   k.k_codes = c->d_k_codes;
   k.v_codes = c->d_v_codes;
@@ -852,7 +938,8 @@ extern "C" entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv
   k.shares = p.shares;
   k.scale = std::fabs(a->scale) * kLog2e;
   k.q_xor = std::signbit(a->scale) ? 0x80008000u : 0u;
-  k.part_s = static_cast<f32x4 *>(a->d_work);
+  k.cuts = static_cast<u32x4 *>(a->d_work);
+  k.part_s = reinterpret_cast<f32x4 *>(k.cuts + p.shares);
   k.part_o = reinterpret_cast<float *>(k.part_s + (uint64_t)k.n_kv * k.parts * k.shares * 2u * p.rows());
   k.status = d_status;
   const auto waves = [&](auto type, auto dim) {

@@ -314,6 +314,9 @@ def test_chunk_queries_that_are_no_numbers(ent):
     bad[3, 1] = bad[41, 0] = True
     assert not torch.isfinite(got[bad]).any() and torch.isfinite(got[~bad]).all()
     assert alike(got[~bad], a[~bad], "bf16")
+    # over tokens that are split over workgroups
+    g2 = raw(ent, (4, 2, 64), "bf16", 16, [4], [3000], 0, lambda q, c, t: q[1, 2].fill_(math.nan))
+    assert torch.isnan(g2[1, 2]).all() and torch.isfinite(g2[0]).all() and torch.isfinite(g2[2:]).all()
 
 
 def test_chunk_flags(ent):
