@@ -27,6 +27,7 @@ struct ChunkArg {
   uint32_t n_heads, group;      // group: query heads per key/value head
   uint32_t heads, parts;        // query heads of a workgroup, workgroups per key/value head for all of them
   uint32_t block_log2;          // tokens of a workgroup
+  uint32_t rows;                // rows (queries of a head) of a workgroup, at most
   uint32_t shares;              // that the tiles of a key/value head are split into at most
   float scale;                  // magnitude, times log2(e)
   uint32_t q_xor;               // on a pair of q: the scale's sign
@@ -223,6 +224,33 @@ __device__ __forceinline__ uint32_t cut_at(uint64_t place, uint64_t before) {
 // (and for shares that there are not) no tokens.
 typedef u32x4 Cut;   // row, tokens, share, 0
 
+// Marks the sequences whose lengths do not fit (one wavefront of the call).
+__device__ __forceinline__ void flag_lengths(const ChunkArg &a, uint32_t lane) {
+  Spans spans(a.cu, a.total_q, a.n_seq, lane);
+  for (uint32_t b0 = 0; b0 < a.n_seq; b0 += 64u) {
+    bool ok;
+    chunk_seq(a, spans, b0, &ok);
+    if (b0 + lane < a.n_seq && !ok) atomicOr(a.status + b0 + lane, ENTRO_F_LENGTH);
+  }
+}
+// The shares that there are; the others' cuts are none.
+__device__ __forceinline__ uint32_t no_cuts(const ChunkArg &a, const Shares &sh, uint32_t tid) {
+  const uint32_t units = sh.work ? sh.n : 0u;
+  if (blockIdx.x == 0u && tid == 0u && a.total_q)   // (without rows there is no workspace)
+    for (uint32_t w = blockIdx.y; w < a.shares; w += gridDim.y)
+      if (w >= units) a.cuts[w] = (Cut){0u, 0u, 0u, 0u};
+  return units;
+}
+__device__ __forceinline__ Cut cut_of(const ChunkArg &a, const Place &at, const Shares &sh, uint32_t w) {
+  const Seq s = at.here();
+  const Blocks blocks(a.block_log2, s);
+  const uint32_t token0 = at.block << a.block_log2;
+  Cut cut = {s.begin + token0, min(1u << a.block_log2, s.count - token0), 0u, 0u};
+  if (!cut_at(sh.begin(w), at.before) || cut_at(sh.begin(w - 1u), at.before)) cut.y = 0u;   // none, or not the block's first
+  if (cut.y) cut.z = sh.of(at.before + blocks.work(at.block) - 1u);
+  return cut;
+}
+
 // What is known of a row (one query of one head) beside its outputs, in powers of
 // two: the largest score m, the weights' sum l relative to 2^m, and the exponent g
 // of the outputs' unit, relative to 2^m too.  top: the largest exponent, less m, with
@@ -276,22 +304,31 @@ __device__ __forceinline__ uint32_t fresh(uint32_t v) {
 // way copies all of them every tile.  The matrix instructions' results are waited for
 // first.
 __device__ __forceinline__ void results_there() { asm volatile("s_nop 15\n\ts_nop 15"); }
-__device__ __forceinline__ void scale_in_place(f32x16 &o, float k) {
+template <typename V>
+__device__ __forceinline__ void scale_in_place(V &o, float k) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
+  for (int r = 0; r < (int)(sizeof(V) / 4); ++r) {
     float x = o[r];
     asm volatile("v_mul_f32 %0, %1, %0" : "+v"(x) : "v"(k));
     o[r] = x;
   }
 }
 // o = o k + z
-__device__ __forceinline__ void add_in_place(f32x16 &o, float k, const f32x16 &z) {
+template <typename V>
+__device__ __forceinline__ void add_in_place(V &o, float k, const V &z) {
 #pragma unroll
-  for (int r = 0; r < 16; ++r) {
+  for (int r = 0; r < (int)(sizeof(V) / 4); ++r) {
     float x = o[r];
     asm volatile("v_fma_f32 %0, %0, %1, %2" : "+v"(x) : "v"(k), "v"(z[r]));
     o[r] = x;
   }
+}
+// -infinity where token I is not seen (I >= seen)
+template <int I>
+__device__ __forceinline__ float hidden(float y, int32_t seen) {
+  asm volatile("v_cmp_lt_i32 vcc, %1, %2\n\ts_nop 1\n\tv_cndmask_b32 %0, %3, %0, vcc"
+               : "+v"(y) : "n"(I), "v"(seen), "v"(-INFINITY) : "vcc");
+  return y;
 }
 // -infinity where token 16 b + j is not seen (16 b + j >= seen)
 __device__ __forceinline__ void hide_in_place(f32x16 &x, int b, int32_t seen) {
@@ -367,6 +404,32 @@ __device__ __forceinline__ void products(f32x16 *x, const Tile<L> &tile, int fro
   }
 }
 
+constexpr float kLag = 3.0f, kRoom = 12.875f;   // see fast_tile
+// How an ordinary tile changes a row's state: mx is its largest score, most and least the
+// logarithms of its pages' value scales.
+struct Rise {
+  float m, g;
+  bool rise, near;
+  __device__ Rise(const State &st, float mx, float most, float least) {
+    const bool move = !(most - st.g <= kRoom + 0.025f && least - st.g >= 10.0f), none = st.top == -INFINITY;
+    rise = move || mx > st.m + kLag || none;
+    g = move ? most - kRoom : st.g;
+    m = fmaxf(st.m, mx);
+    near = (fabsf(m) < 32768.0f || m == -INFINITY) && (none || fabsf(g - st.g) <= 60.0f);
+  }
+  // returns the factor of the outputs
+  __device__ float apply(State &st) const {
+    const bool none = st.top == -INFINITY;
+    const float up = m == -INFINITY ? 0.0f : m - st.m, k = exp2_fast(-up), ko = none ? 0.0f : k * exp2_fast(st.g - g);
+    st.l *= k;
+    st.top = m == -INFINITY ? -INFINITY : fmaxf(st.top - up, g + kUnit);
+    st.m = m;
+    st.g = g;
+    st.settle();
+    return ko;
+  }
+};
+
 // A tile whose scales and scores are ordinary ones: weights go into the product with
 // their page's value scale, as 2^(t - m + log2(scale) - g), where g is held such that
 // the largest are 2^10 to 2^(15.9) (f16 has 11 bits from 2^-14 on), and come out of
@@ -377,7 +440,6 @@ __device__ __forceinline__ void products(f32x16 *x, const Tile<L> &tile, int fro
 // them), scores so far from 0 that a fused difference
 // would have a rounding of the score left over, values so far from the unit that moving
 // it could lose them.  (NaN fails.)
-constexpr float kLag = 3.0f, kRoom = 12.875f;
 template <typename L, int DT>
 __device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x16 (&x)[2], const Tile<L> &tile,
                                           const Scales &scales, float c) {
@@ -390,24 +452,14 @@ __device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x
     for (int j = 0; j < 8; ++j) most = fmaxf(most, x[b >> 1][8 * (b & 1) + j]);
     mx = fmaxf(mx, most * sc[b]);
   }
-  mx = max32(mx);
-  const float most = lane_of(scales.most, tile.at), least = lane_of(scales.least, tile.at);
-  const bool move = !(most - st.g <= kRoom + 0.025f && least - st.g >= 10.0f), none = st.top == -INFINITY;
-  const bool rise = move || mx > st.m + kLag || none;
-  const float g = move ? most - kRoom : st.g, m = fmaxf(st.m, mx);
   // (all of it before the outputs are touched: with ways out in between they are copied)
-  const bool near = (fabsf(m) < 32768.0f || m == -INFINITY) && (none || fabsf(g - st.g) <= 60.0f);
-  if ((scales.fine >> tile.at & 15u) != 15u || __any(rise && !near)) return false;
-  if (__any(rise)) {
-    const float up = m == -INFINITY ? 0.0f : m - st.m, k = exp2_fast(-up), ko = none ? 0.0f : k * exp2_fast(st.g - g);
-    st.l *= k;
-    st.top = m == -INFINITY ? -INFINITY : fmaxf(st.top - up, g + kUnit);
-    st.m = m;
-    st.g = g;
-    st.settle();
+  const Rise up(st, max32(mx), lane_of(scales.most, tile.at), lane_of(scales.least, tile.at));
+  if ((scales.fine >> tile.at & 15u) != 15u || __any(up.rise && !up.near)) return false;
+  if (__any(up.rise)) {
+    const float less = up.apply(st);
     results_there();
 #pragma unroll
-    for (int d = 0; d < DT; ++d) scale_in_place(o[d], ko);
+    for (int d = 0; d < DT; ++d) scale_in_place(o[d], less);
   }
   // the weights of the next 16 tokens between the products of these
   u32x4 p[2];
@@ -442,6 +494,29 @@ __device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x
   return true;
 }
 
+// A row's state with 16 tokens more, whose largest score is mx and whose page's value
+// scale v: the factors of its sum (less), of theirs (part), of its outputs (keep) and of
+// their product (f: with weights times 2^15).
+struct Block {
+  float m, g, top, less, part, keep, f;
+  __device__ Block(const State &st, float mx, const Scale &v, bool any) {
+    m = fmaxf(st.m, mx);
+    const float up = m - st.m, down = mx - m;
+    top = fmaxf(st.top - up, down + v.log);
+    g = st.g;
+    if (top > -kFloatMax && !(fabsf(top - kUnit - g) <= 30.0f)) g = top - kUnit;
+    less = exp2_fast(-up);
+    part = exp2_fast(down);
+    keep = any ? exp2_fast(st.g - g - up) : 1.0f;
+    f = any && v.part != 0.0f ? v.part * exp2_fast(down + v.whole - g - 15.0f) : 0.0f;
+  }
+  __device__ void apply(State &st) const {
+    st.m = m;
+    st.g = g;
+    st.top = top;
+  }
+};
+
 // Any tile: 16 tokens at a time, the weights relative to their own largest and their
 // product's part brought to the outputs' unit in 32 bits, the unit to the values'.  A
 // block that a row does not see has no influence on it, whatever its scales are.
@@ -473,18 +548,10 @@ __device__ __forceinline__ void slow_tile(State &st, f32x16 (&o)[DT], const f16v
         sum += p0 + p1;
         pw[j] = Elem<ENTRO_F16>::pack2(p0 * 32768.0f, p1 * 32768.0f);
       }
-      // the row's state with the block
-      const float m = fmaxf(st.m, mx), up = m - st.m, down = mx - m;
-      const float top = fmaxf(st.top - up, down + vs.log);
-      float g = st.g;
-      if (top > -kFloatMax && !(fabsf(top - kUnit - g) <= 30.0f)) g = top - kUnit;
-      const float keep = any ? exp2_fast(st.g - g - up) : 1.0f;
-      const float f = any && vs.part != 0.0f ? vs.part * exp2_fast(down + vs.whole - g - 15.0f) : 0.0f;
+      const Block b(st, mx, vs, any);
       if (any) {
-        st.l = st.l * exp2_fast(-up) + sum * exp2_fast(down);
-        st.m = m;
-        st.g = g;
-        st.top = top;
+        st.l = st.l * b.less + sum * b.part;
+        b.apply(st);
       }
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
@@ -494,15 +561,41 @@ __device__ __forceinline__ void slow_tile(State &st, f32x16 (&o)[DT], const f16v
         for (int i = 0; i < 16; ++i) z[i] = 0.0f;
         z = mfma(tile.value(d, blk), __builtin_bit_cast(f16v8, pw), z);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] = any ? z[i] * f : 0.0f;
+        for (int i = 0; i < 16; ++i) z[i] = any ? z[i] * b.f : 0.0f;
         results_there();
-        add_in_place(o[d], keep, z);
+        add_in_place(o[d], b.keep, z);
       }
       in_order();
     }
   }
   st.settle();
 }
+
+// Four dimensions of a row, of pieces of its tokens.
+struct Joined {
+  float m, l, g;   // of the pieces so far: as in State; g: -infinity where no value was added
+  f32x4 o;
+  // two of them, or one and a piece; factors from differences only
+  __device__ void add(float m1, float l1, float g1, f32x4 o1) {
+    if (m1 == -INFINITY && l1 == 0.0f) return;   // saw no token (a sum that is no number stays)
+    const float up = fmaxf(m, m1), d0 = m - up, d1 = m1 - up;
+    l = (m == -INFINITY ? 0.0f : l * exp2_fast(d0)) + l1 * exp2_fast(d1);
+    const float u0 = g == -INFINITY ? -INFINITY : g + d0, u1 = g1 + d1, unit = fmaxf(u0, u1);
+    if (unit != -INFINITY)   // (NaN passes)
+      o = o * (u0 == -INFINITY ? 0.0f : exp2_fast(u0 - unit)) + o1 * (u1 == -INFINITY ? 0.0f : exp2_fast(u1 - unit));
+    g = unit;
+    m = up;
+  }
+  template <entro_dtype T>
+  __device__ u32x2 result() const {
+    const float whole = floorf(fminf(fmaxf(g, -400.0f), 400.0f));
+    const float k = l == 0.0f || g == -INFINITY ? l * 0.0f : exp2_fast(g - whole) / l;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ldexpf(o[i] * k, (int)whole);
+    return (u32x2){Elem<T>::pack2(v[0], v[1]), Elem<T>::pack2(v[2], v[3])};
+  }
+};
 
 // ---------------------------------------------------------------------------
 // One workgroup takes pieces of blocks for one key/value head.  A block's rows are
@@ -528,19 +621,9 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = rfl(tid >> 6);
   const uint32_t page = 1u << a.page_log2;
   Place at(a, lane);
-  if (blockIdx.x == 0u && blockIdx.y == 0u && wave == 0u) {
-    Spans spans(a.cu, a.total_q, a.n_seq, lane);
-    for (uint32_t b0 = 0; b0 < a.n_seq; b0 += 64u) {
-      bool ok;
-      chunk_seq(a, spans, b0, &ok);
-      if (b0 + lane < a.n_seq && !ok) atomicOr(a.status + b0 + lane, ENTRO_F_LENGTH);
-    }
-  }
+  if (blockIdx.x == 0u && blockIdx.y == 0u && wave == 0u) flag_lengths(a, lane);
   const Shares sh = shares_of(a, at.count_all());
-  const uint32_t units = sh.work ? sh.n : 0u;
-  if (blockIdx.x == 0u && tid == 0u && a.total_q)   // (without rows there is no workspace)
-    for (uint32_t w = blockIdx.y; w < a.shares; w += gridDim.y)
-      if (w >= units) a.cuts[w] = (Cut){0u, 0u, 0u, 0u};
+  const uint32_t units = no_cuts(a, sh, tid);
   for (uint32_t head_part = blockIdx.x; head_part < a.n_kv * a.parts; head_part += gridDim.x)
     for (uint32_t w = blockIdx.y; w < units; w += gridDim.y) {
       const uint32_t kvh = head_part / a.parts, h0 = head_part % a.parts * a.heads;
@@ -550,15 +633,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
       uint64_t now = sh.begin(w);
       const uint64_t end = sh.begin(w + 1u);
       at.find(now);
-      if (head_part == 0u) {
-        const Seq s = at.here();
-        const Blocks blocks(a.block_log2, s);
-        const uint32_t token0 = at.block << a.block_log2;
-        Cut cut = {s.begin + token0, min(1u << a.block_log2, s.count - token0), 0u, 0u};
-        if (!cut_at(now, at.before) || cut_at(sh.begin(w - 1u), at.before)) cut.y = 0u;   // none, or not the block's first
-        if (cut.y) cut.z = sh.of(at.before + blocks.work(at.block) - 1u);
-        if (tid == 0u) a.cuts[w] = cut;
-      }
+      if (head_part == 0u && tid == 0u) a.cuts[w] = cut_of(a, at, sh, w);
       for (; now < end; at.next()) {
         const Seq s = at.here();
         const Blocks blocks(a.block_log2, s);
@@ -771,29 +846,307 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: 16, 32 or 64 in a workgroup.  A wavefront has 16 of them, and the wavefronts
+// of the same rows take turns at the tiles and are joined over LDS at the end of a piece.
+// Nothing of the cache passes through LDS: scores are K Q^T and outputs V^T P^T on
+// 16 x 16 x 32 matrix instructions with the rows as columns.  The first product's row
+// 4 g + r of its i-th part is token 16 g + 4 i + r of the tile: lane group g (16 lanes)
+// then holds 16 consecutive tokens of a row, of one page, just the 16 bytes of codes that
+// it reads of one dimension, and 64 bytes of a key or of a dimension are read side by side.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kFewWaves = 4;
+
+__device__ __forceinline__ f32x4 mfma16(f16v8 a, f16v8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ float max_of_row(float v) { return max32(max16(v)); }
+
+template <entro_dtype T, int D>
+__global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(ChunkArg a) {
+  constexpr int S64 = D / 64;            // 64-dimension parts of a key row read as 16 bytes a lane
+  constexpr bool S32 = (D % 64) != 0;    // and one of 32 read as 8
+  constexpr int KS = D / 32;             // matrix products over the dimensions
+  constexpr int DT = D / 16;             // 16-dimension parts of the output
+  constexpr uint32_t kRow = D + 4;       // of the results in LDS
+  float *red_o = reinterpret_cast<float *>(dyn_lds);                         // [kFewWaves][16][kRow]
+  f32x4 *red_s = reinterpret_cast<f32x4 *>(red_o + kFewWaves * 16u * kRow);  // [kFewWaves][16]
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = rfl(tid >> 6), n = lane & 15u, grp = lane >> 4;
+  const uint32_t page = 1u << a.page_log2, sets = a.rows / 16u, set = wave % sets, phases = kFewWaves / sets;
+  Place at(a, lane);
+  if (blockIdx.x == 0u && blockIdx.y == 0u && wave == 0u) flag_lengths(a, lane);
+  const Shares sh = shares_of(a, at.count_all());
+  const uint32_t units = no_cuts(a, sh, tid);
+  for (uint32_t head_part = blockIdx.x; head_part < a.n_kv * a.parts; head_part += gridDim.x)
+    for (uint32_t w = blockIdx.y; w < units; w += gridDim.y) {
+      const uint32_t kvh = head_part / a.parts, h0 = head_part % a.parts * a.heads;
+      const uint32_t heads = min(a.heads, a.group - h0), head0 = kvh * a.group + h0;
+      const uint32_t page_bytes = a.n_kv * page * D;   // from one page's codes to the next's, below 2^30
+      const int8_t *const kb = a.k_codes + (uint64_t)kvh * page * D, *const vb = a.v_codes + (uint64_t)kvh * page * D;
+      uint64_t now = sh.begin(w);
+      const uint64_t end = sh.begin(w + 1u);
+      at.find(now);
+      if (head_part == 0u) {
+        const Cut cut = cut_of(a, at, sh, w);
+        if (tid == 0u) a.cuts[w] = cut;
+      }
+      for (; now < end; at.next()) {
+        const Seq s = at.here();
+        const Blocks blocks(a.block_log2, s);
+        const uint32_t all_tiles = blocks.tiles(at.block);
+        const uint32_t t0 = cut_at(now, at.before), t1 = min(all_tiles, cut_at(end, at.before));
+        now = at.before + blocks.work(at.block);
+        if (t0 == t1) continue;
+        const int32_t *row = a.table + (uint64_t)at.seq * a.table_stride;
+        const uint32_t token0 = at.block << a.block_log2;
+        const uint32_t rows = min(1u << a.block_log2, s.count - token0) * heads;
+        // the lane's row (past the last, the last): the tokens that it sees, less the first
+        // of the lane's block, the query as f16 times 2^-e, the score's factor
+        const uint32_t own_row = min(16u * set + n, rows - 1u), token = token0 + own_row / heads, head = head0 + own_row % heads;
+        const int32_t sees = (int32_t)max((int64_t)0, blocks.ahead + token + 1);
+        const int32_t least = (int32_t)rfl((uint32_t)sees), limit = sees - 16 * (int32_t)grp;
+        f16v8 qf[KS];
+        float c;
+        {
+          u32x4 raw[KS];
+          const char *q = a.q + ((int64_t)s.begin + token) * a.q_t + (int64_t)head * a.q_h;
+#pragma unroll
+          for (int i = 0; i < S64; ++i) {
+            raw[2 * i] = *reinterpret_cast<const u32x4 *>(q + (64 * i + 16 * grp) * 2);
+            raw[2 * i + 1] = *reinterpret_cast<const u32x4 *>(q + (64 * i + 16 * grp + 8) * 2);
+          }
+          if (S32) raw[KS - 1] = *reinterpret_cast<const u32x4 *>(q + (64 * S64 + 8 * grp) * 2);
+          int e2 = 0;
+          if (T == ENTRO_BF16) {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+              for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(Elem<T>::lo(raw[i][e])), fabsf(Elem<T>::hi(raw[i][e]))));
+            top = max_of_row(top);
+            e2 = top == 0.0f ? 0 : (int)(__builtin_bit_cast(uint32_t, top) >> 23) - 127;   // bf16 denormals: -127
+          }
+          c = ldexpf(a.scale, e2);
+#pragma unroll
+          for (int i = 0; i < KS; ++i) {
+            u32x4 x;
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t y = T == ENTRO_F16 ? raw[i][e]
+                                                : Elem<ENTRO_F16>::pack2(ldexpf(Elem<T>::lo(raw[i][e]), -e2),
+                                                                         ldexpf(Elem<T>::hi(raw[i][e]), -e2));
+              x[e] = y ^ a.q_xor;
+            }
+            qf[i] = __builtin_bit_cast(f16v8, x);
+          }
+        }
+        const bool plain = __all(c >= 0x1p-60f);   // see fast_tile
+        f32x4 o[DT];
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[d] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+        State st = {-INFINITY, 0.0f, 0.0f, -INFINITY, 0.0f, 1.0f};
+
+        // This wavefront's tiles are first + phases k, k = 0 .. count - 1.  Four tiles' page
+        // numbers and scales at once, 16 blocks of 16 tokens in each 16 lanes, the page
+        // numbers two groups ahead and the scales one; keys one tile ahead.  (Past its last
+        // tile a wavefront fetches that one again: no branches.)  A block past the sequence's
+        // end, or of a page that does not exist, takes page 0.
+        bool bad = false;
+        const uint32_t first = t0 + wave / sets, count = t1 > first ? (t1 - first + phases - 1u) / phases : 0u;
+        const uint32_t last = count ? count - 1u : 0u;
+        const auto tile_of = [&](uint32_t k) { return first + min(k, last) * phases; };
+        const auto token_of = [&](uint32_t four) {
+          return tile_of(4u * four + (fresh(lane) >> 2 & 3u)) * kTile + (fresh(lane) & 3u) * 16u;
+        };
+        const auto page_at = [&](uint32_t four) {
+          return (uint32_t)row[min(token_of(four), max(s.len, 1u) - 1u) >> a.page_log2];
+        };
+        const auto page_ok = [&](uint32_t p, uint32_t four) {
+          const bool there = token_of(four) < s.len;
+          bad |= there && p >= a.n_pages;
+          return there && p < a.n_pages ? p : 0u;
+        };
+        const auto scale_at = [&](const float *scales, uint32_t p) { return scales[(uint64_t)p * a.n_kv + kvh]; };
+        u32x4 kq[4][S64], vq[DT];
+        u32x2 kq2[4];
+        const auto fetch_keys = [&](uint32_t k, uint32_t pages) {
+          const uint32_t p = (uint32_t)__shfl((int)pages, (int)((min(k, last) & 3u) * 4u + (n >> 2)));
+          const uint32_t in = ((tile_of(k) * kTile + (n >> 2) * 16u) & (page - 1u)) + (n & 3u);
+          const int8_t *from = kb + (uint64_t)p * page_bytes + in * D;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int e = 0; e < S64; ++e) kq[i][e] = *reinterpret_cast<const u32x4 *>(from + 4 * i * D + 64 * e + 16 * grp);
+            if (S32) kq2[i] = *reinterpret_cast<const u32x2 *>(from + 4 * i * D + 64 * S64 + 8 * grp);
+          }
+        };
+        const auto value_of = [&](uint32_t k, uint32_t pages, uint32_t d) {
+          const uint32_t p = (uint32_t)__shfl((int)pages, (int)((k & 3u) * 4u + grp));
+          const uint32_t in = (tile_of(k) * kTile + grp * 16u) & (page - 1u);
+          return reinterpret_cast<const u32x4 *>(vb + (uint64_t)p * page_bytes + (((16u * d + n) << a.page_log2) + in));
+        };
+        if (count) {
+          uint32_t pages = page_ok(page_at(0u), 0u);
+          fetch_keys(0u, pages);
+          float ks = scale_at(a.k_scales, pages), vs = scale_at(a.v_scales, pages);
+          uint32_t pages_next = page_ok(page_at(1u), 1u), pages_raw = page_at(2u);
+          for (uint32_t four = 0, k = 0; k < count; ++four) {
+            const Scales scales(ks, vs, token_of(four) >= s.len);
+            ks = scale_at(a.k_scales, pages_next);
+            vs = scale_at(a.v_scales, pages_next);
+            for (const uint32_t stop = min(count, 4u * four + 4u); k < stop; ++k) {
+#pragma unroll
+              for (int d = 0; d < DT; ++d) vq[d] = *value_of(k, pages, (uint32_t)d);
+              const uint32_t its = (k & 3u) * 4u;
+              float sc = c * __shfl(scales.k, (int)(its + grp));
+              float by = __shfl(scales.log, (int)(its + grp)), rcp = __shfl(scales.rcp, (int)(its + grp));
+              f32x4 x[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                x[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int e = 0; e < S64; ++e) {
+                  x[i] = mfma16(half8(kq[i][e].x, kq[i][e].y), qf[2 * e], x[i]);
+                  x[i] = mfma16(half8(kq[i][e].z, kq[i][e].w), qf[2 * e + 1], x[i]);
+                }
+                if (S32) x[i] = mfma16(half8(kq2[i].x, kq2[i].y), qf[KS - 1], x[i]);
+              }
+              fetch_keys(k + 1u, (k & 3u) == 3u ? pages_next : pages);
+              const int32_t seen = limit - (int32_t)(tile_of(k) * kTile);
+              if ((int32_t)(tile_of(k) * kTile + kTile) > least) {
+                results_there();
+#define ENTRO_HIDE(I)                                   \
+  x[I][0] = hidden<4 * I>(x[I][0], seen);               \
+  x[I][1] = hidden<4 * I + 1>(x[I][1], seen);           \
+  x[I][2] = hidden<4 * I + 2>(x[I][2], seen);           \
+  x[I][3] = hidden<4 * I + 3>(x[I][3], seen);
+                ENTRO_HIDE(0) ENTRO_HIDE(1) ENTRO_HIDE(2) ENTRO_HIDE(3)
+#undef ENTRO_HIDE
+              }
+              float mx = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[i][r]);
+              const Rise up(st, max_of_row(mx * sc), lane_of(scales.most, its), lane_of(scales.least, its));
+              if (!(plain && (scales.fine >> its & 15u) == 15u && !__any(up.rise && !up.near))) {
+                // as slow_tile, a block at a time: the others' lanes have weights of 0.  The
+                // outputs pass through LDS: such tiles take time, but no registers.
+                float *const own_o = red_o + (wave * 16u + n) * kRow + 4u * grp;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(own_o + 16 * d) = o[d];
+                float own = -kFloatMax, sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  for (int r = 0; r < 4; ++r) {
+                    x[i][r] = 4 * i + r < seen ? rounded(x[i][r], sc) : -INFINITY;
+                    own = fmaxf(own, x[i][r]);
+                  }
+                u32x4 pw[2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  for (int r = 0; r < 4; r += 2) {
+                    const float p0 = exp2_fast(x[i][r] - own), p1 = exp2_fast(x[i][r + 1] - own);
+                    sum += p0 + p1;
+                    pw[i >> 1][2 * (i & 1) + r / 2] = Elem<ENTRO_F16>::pack2(p0 * 32768.0f, p1 * 32768.0f);
+                  }
+#pragma unroll 1
+                for (uint32_t e = 0; e < 4u; ++e) {
+                  const Scale v(lane_of(scales.v, its + e));
+                  const bool mine = grp == e, any = max_of_row(mine && 0 < seen ? 1.0f : 0.0f) != 0.0f;
+                  const Block b(st, max_of_row(mine ? own : -kFloatMax), v, any);
+                  if (any) {
+                    st.l = st.l * b.less + (mine ? sum * b.part : 0.0f);
+                    b.apply(st);
+                  }
+                  u32x4 q[2];
+#pragma unroll
+                  for (int h = 0; h < 2; ++h)
+                    for (int i = 0; i < 4; ++i) q[h][i] = mine ? pw[h][i] : 0u;
+#pragma unroll 1
+                  for (uint32_t d = 0; d < (uint32_t)DT; ++d) {
+                    const u32x4 code = *value_of(k, pages, d);
+                    f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+                    z = mfma16(half8(code.x, code.y), __builtin_bit_cast(f16v8, q[0]), z);
+                    z = mfma16(half8(code.z, code.w), __builtin_bit_cast(f16v8, q[1]), z);
+                    f32x4 *const at_o = reinterpret_cast<f32x4 *>(own_o + 16u * d);
+                    f32x4 y = *at_o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = y[i] * b.keep + (any ? z[i] * b.f : 0.0f);
+                    *at_o = y;
+                  }
+                }
+                st.settle();
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d] = *reinterpret_cast<const f32x4 *>(own_o + 16 * d);
+                // and nothing of the tile is left for below
+                by = rcp = 0.0f;
+                sc = 1.0f;
+                for (int i = 0; i < 4; ++i) x[i] = (f32x4){-0x1p120f, -0x1p120f, -0x1p120f, -0x1p120f};
+              } else if (__any(up.rise)) {
+                const float less = up.apply(st);
+                results_there();
+#pragma unroll
+                for (int d = 0; d < DT; ++d) scale_in_place(o[d], less);
+              }
+              u32x4 p[2];
+              float sum = 0.0f;
+              const float off = by + st.off;
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                for (int r = 0; r < 4; r += 2) {
+                  const uint32_t y = Elem<ENTRO_F16>::pack2(exp2_fast(__builtin_fmaf(x[i][r], sc, off)),
+                                                            exp2_fast(__builtin_fmaf(x[i][r + 1], sc, off)));
+                  p[i >> 1][2 * (i & 1) + r / 2] = y;
+                  sum = Elem<ENTRO_F16>::add2(y, sum);
+                }
+              st.l = __builtin_fmaf(sum * rcp, st.unit, st.l);
+#pragma unroll
+              for (int d = 0; d < DT; ++d) {
+                o[d] = mfma16(half8(vq[d].x, vq[d].y), __builtin_bit_cast(f16v8, p[0]), o[d]);
+                o[d] = mfma16(half8(vq[d].z, vq[d].w), __builtin_bit_cast(f16v8, p[1]), o[d]);
+              }
+            }
+            pages = pages_next;
+            pages_next = page_ok(pages_raw, four + 2u);
+            pages_raw = page_at(four + 3u);
+          }
+        }
+        if (bad) atomicOr(a.status + at.seq, ENTRO_F_PAGE);
+        {
+          const uint32_t place = wave * 16u + n;
+          const float l = add32(add16(st.l));
+          if (grp == 0u) red_s[place] = (f32x4){st.m, l, st.top == -INFINITY ? -INFINITY : st.g, 0.0f};
+#pragma unroll
+          for (int d = 0; d < DT; ++d) *reinterpret_cast<f32x4 *>(red_o + place * kRow + 16 * d + 4 * grp) = o[d];
+        }
+        __syncthreads();
+        const uint64_t slot = (((uint64_t)head_part * a.shares + w) * 2u + (t0 == 0u)) * a.rows;
+        for (uint32_t i = tid; i < rows * (D / 4u); i += 64u * kFewWaves) {
+          const uint32_t r = i / (D / 4u), d = i % (D / 4u) * 4u;
+          Joined j = {-INFINITY, 0.0f, -INFINITY, {0.0f, 0.0f, 0.0f, 0.0f}};
+          for (uint32_t place = r; place < 16u * kFewWaves; place += 16u * sets) {
+            const f32x4 q = red_s[place];
+            j.add(q.x, q.y, q.z, *reinterpret_cast<const f32x4 *>(red_o + place * kRow + d));
+          }
+          if (t1 - t0 == all_tiles) {
+            *reinterpret_cast<u32x2 *>(a.out + ((int64_t)s.begin + token0 + r / heads) * a.o_t + (int64_t)(head0 + r % heads) * a.o_h +
+                                       d * 2u) = j.result<T>();
+          } else {
+            if (d == 0u) a.part_s[slot + r] = (f32x4){j.m, j.l, j.g, 0.0f};
+            *reinterpret_cast<f32x4 *>(a.part_o + (slot + r) * D + d) = j.o;
+          }
+        }
+        __syncthreads();   // red_o and red_s are written again
+      }
+    }
+}
+
 // Joins the pieces of the blocks that were cut: kJoinSlots slots of D / 4 threads, four
 // dimensions each, for the first cut in a block.  A slot takes whole rows; where there
 // are many pieces the slots take every kJoinSlots-th piece of one row and are joined
 // over LDS.  Four pieces' reads at once; the order is the same in every call.
 constexpr uint32_t kJoinSlots = 8;
-struct Joined {
-  float m, l, g;   // of the pieces so far: as in State; g: -infinity where no value was added
-  f32x4 o;
-  // two of them, or one and a piece; factors from differences only
-  __device__ void add(float m1, float l1, float g1, f32x4 o1) {
-    if (m1 == -INFINITY && l1 == 0.0f) return;   // saw no token (a sum that is no number stays)
-    const float up = fmaxf(m, m1), d0 = m - up, d1 = m1 - up;
-    l = (m == -INFINITY ? 0.0f : l * exp2_fast(d0)) + l1 * exp2_fast(d1);
-    const float u0 = g == -INFINITY ? -INFINITY : g + d0, u1 = g1 + d1, unit = fmaxf(u0, u1);
-    if (unit != -INFINITY)   // (NaN passes)
-      o = o * (u0 == -INFINITY ? 0.0f : exp2_fast(u0 - unit)) + o1 * (u1 == -INFINITY ? 0.0f : exp2_fast(u1 - unit));
-    g = unit;
-    m = up;
-  }
-};
-template <entro_dtype T, int D, int W>
+template <entro_dtype T, int D>
 __global__ __launch_bounds__(kJoinSlots * D / 4) void attn_chunk_join_kernel(ChunkArg a) {
-  constexpr uint32_t kRows = 32 * W, kGroups = kRows / kJoinSlots;
+  const uint32_t kRows = a.rows, kGroups = kRows / kJoinSlots;
   __shared__ Joined red[kJoinSlots][D / 4];
   const uint32_t slot = threadIdx.x / (D / 4u), dq = threadIdx.x % (D / 4u);
   for (uint32_t w = 1u + blockIdx.y; w < a.shares; w += gridDim.y) {
@@ -834,13 +1187,8 @@ __global__ __launch_bounds__(kJoinSlots * D / 4) void attn_chunk_join_kernel(Chu
         } else if (r0 + slot >= rows) {
           continue;
         }
-        const float whole = floorf(fminf(fmaxf(j.g, -400.0f), 400.0f));
-        const float k = j.l == 0.0f || j.g == -INFINITY ? j.l * 0.0f : exp2_fast(j.g - whole) / j.l;
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = ldexpf(j.o[i] * k, (int)whole);
         *reinterpret_cast<u32x2 *>(a.out + ((int64_t)cut.x + r / heads) * a.o_t + (int64_t)(head0 + r % heads) * a.o_h + dq * 8u) =
-            (u32x2){Elem<T>::pack2(v[0], v[1]), Elem<T>::pack2(v[2], v[3])};
+            j.result<T>();
       }
     }
   }
@@ -852,28 +1200,36 @@ __global__ __launch_bounds__(kJoinSlots * D / 4) void attn_chunk_join_kernel(Chu
 
 // How a call is laid out.
 struct Plan {
-  uint32_t waves, heads, parts, block_log2, shares;
-  uint64_t rows() const { return 32u * waves; }
+  uint32_t waves;   // 0: few rows
+  uint32_t rows, heads, parts, block_log2, shares;
 };
 static Plan plan_of(uint32_t n_seq, uint32_t total_q, uint32_t n_heads, uint32_t n_kv, uint32_t head_dim) {
   Plan p{};
   const uint32_t group = n_heads / n_kv;
-  p.waves = (uint64_t)total_q * group > 128ull * n_seq ? 8u : 4u;
-  p.heads = std::min<uint32_t>(group, (uint32_t)p.rows());
+  const uint64_t rows = (uint64_t)total_q * group;
+  p.waves = rows > 128ull * n_seq ? 8u : rows > 64ull * n_seq ? 4u : 0u;
+  p.rows = p.waves ? 32u * p.waves : rows > 32ull * n_seq ? 64u : rows > 16ull * n_seq ? 32u : 16u;
+  p.heads = std::min(group, p.rows);
   p.parts = (group + p.heads - 1u) / p.heads;
-  while ((2u << p.block_log2) * p.heads <= p.rows()) ++p.block_log2;
-  p.shares = std::max(1u, (p.waves == 8u ? 256u : head_dim == 64u ? 768u : 512u) / (n_kv * p.parts));
+  while ((2u << p.block_log2) * p.heads <= p.rows) ++p.block_log2;
+  p.shares = std::max(1u, (p.waves == 8u ? 256u : p.waves == 4u && head_dim == 64u ? 768u : 512u) / (n_kv * p.parts));
   return p;
 }
 
-template <entro_dtype T, int D, int W>
-static entro_status launch_chunk(const ChunkArg &a, hipStream_t s) {
-  const uint32_t lds = Lds<D, W>::bytes, heads = a.n_kv * a.parts;
+template <entro_dtype T, int D>
+static entro_status launch_chunk(const ChunkArg &a, uint32_t waves, hipStream_t s) {
+  const uint32_t heads = a.n_kv * a.parts;
+  const dim3 grid = grid2(heads, a.shares);
   (void)hipGetLastError();
-  hipLaunchKernelGGL((attn_chunk_kernel<T, D, W>), grid2(heads, a.shares), dim3(64 * W), lds, s, a);
+  if (waves == 8u)
+    hipLaunchKernelGGL((attn_chunk_kernel<T, D, 8>), grid, dim3(512), (Lds<D, 8>::bytes), s, a);
+  else if (waves == 4u)
+    hipLaunchKernelGGL((attn_chunk_kernel<T, D, 4>), grid, dim3(256), (Lds<D, 4>::bytes), s, a);
+  else
+    hipLaunchKernelGGL((attn_few_kernel<T, D>), grid, dim3(64 * kFewWaves), kFewWaves * 16u * (D + 8u) * 4u, s, a);
   if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
   if (a.shares > 1u && a.total_q) {
-    hipLaunchKernelGGL((attn_chunk_join_kernel<T, D, W>), grid2((uint64_t)heads * (32u * W / kJoinSlots), a.shares - 1u),
+    hipLaunchKernelGGL((attn_chunk_join_kernel<T, D>), grid2((uint64_t)heads * (a.rows / kJoinSlots), a.shares - 1u),
                        dim3(kJoinSlots * D / 4), 0, s, a);
     if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
   }
@@ -889,7 +1245,7 @@ extern "C" uint64_t entro_attn_chunk_work_bytes(uint32_t n_seq, uint32_t total_q
   if (n_seq == 0 || total_q == 0 || total_q > 0x7FFFFFFFu || check_heads(n_heads, n_kv_heads, head_dim, ENTRO_BF16) != ENTRO_OK)
     return 0;
   const Plan p = plan_of(n_seq, total_q, n_heads, n_kv_heads, head_dim);
-  return (uint64_t)n_kv_heads * p.parts * p.shares * 2u * p.rows() * (head_dim + 4u) * 4u + 16u * p.shares;
+  return (uint64_t)n_kv_heads * p.parts * p.shares * 2u * p.rows * (head_dim + 4u) * 4u + 16u * p.shares;
 }
 
 extern "C" entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv_table *t, const entro_attn_chunk_args *a,
@@ -935,21 +1291,18 @@ extern "C" entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv
   k.heads = p.heads;
   k.parts = p.parts;
   k.block_log2 = p.block_log2;
+  k.rows = p.rows;
   k.shares = p.shares;
   k.scale = std::fabs(a->scale) * kLog2e;
   k.q_xor = std::signbit(a->scale) ? 0x80008000u : 0u;
   k.cuts = static_cast<u32x4 *>(a->d_work);
   k.part_s = reinterpret_cast<f32x4 *>(k.cuts + p.shares);
-  k.part_o = reinterpret_cast<float *>(k.part_s + (uint64_t)k.n_kv * k.parts * k.shares * 2u * p.rows());
+  k.part_o = reinterpret_cast<float *>(k.part_s + (uint64_t)k.n_kv * k.parts * k.shares * 2u * p.rows);
   k.status = d_status;
-  const auto waves = [&](auto type, auto dim) {
-    return p.waves == 8u ? launch_chunk<decltype(type)::value, decltype(dim)::value, 8>(k, stream)
-                         : launch_chunk<decltype(type)::value, decltype(dim)::value, 4>(k, stream);
-  };
   const auto dims = [&](auto type) {
-    return c->head_dim == 64u   ? waves(type, std::integral_constant<int, 64>{})
-           : c->head_dim == 96u ? waves(type, std::integral_constant<int, 96>{})
-                                : waves(type, std::integral_constant<int, 128>{});
+    return c->head_dim == 64u   ? launch_chunk<decltype(type)::value, 64>(k, p.waves, stream)
+           : c->head_dim == 96u ? launch_chunk<decltype(type)::value, 96>(k, p.waves, stream)
+                                : launch_chunk<decltype(type)::value, 128>(k, p.waves, stream);
   };
   return a->dtype == ENTRO_BF16 ? dims(std::integral_constant<entro_dtype, ENTRO_BF16>{})
                                 : dims(std::integral_constant<entro_dtype, ENTRO_F16>{});
