@@ -8,6 +8,8 @@
 
 namespace entro {
 
+__device__ __forceinline__ void in_order() { __builtin_amdgcn_sched_barrier(0); }
+
 struct RotArg {
   const float *freqs;
   uint32_t axes[4];
@@ -18,12 +20,13 @@ struct RotArg {
   int64_t pos_stride;
 };
 
-// Input element types: the operand's bytes, eight of them as floats, and the
-// magnitude bits from which a value is infinite or NaN.
+// Input element types: eight operands' bits, and each as a float (after anew, computed
+// again: floats from before are not kept in registers).
 template <entro_dtype T>
 struct In {
   static constexpr int kSize = 2;
   typedef u32x4 raw;
+  __device__ static void anew(raw &r) { asm volatile("" : "+v"(r)); }
   __device__ static raw load(const char *p) { return *reinterpret_cast<const u32x4 *>(p); }
   __device__ static float get(const raw &r, int i) {
     return i & 1 ? Elem<T>::hi(r[i >> 1]) : Elem<T>::lo(r[i >> 1]);
@@ -35,6 +38,7 @@ struct In<ENTRO_F32> {
   struct raw {
     u32x4 a, b;
   };
+  __device__ static void anew(raw &r) { asm volatile("" : "+v"(r.a), "+v"(r.b)); }
   __device__ static raw load(const char *p) {
     return {*reinterpret_cast<const u32x4 *>(p), *reinterpret_cast<const u32x4 *>(p + 16)};
   }
@@ -88,6 +92,7 @@ __device__ __forceinline__ void turn_at(Turn &t, const RotArg &r, uint32_t u, in
     const float y = (float)(x - __builtin_rint(x));
     t.c[j] = __builtin_amdgcn_cosf(y) * r.gain;
     t.s[j] = __builtin_amdgcn_sinf(y) * r.gain;
+    if (j % 2) in_order();   // (eight at once take registers for eight products of 64 bits)
   }
 }
 
@@ -110,18 +115,17 @@ __device__ __forceinline__ void turned16(float *x, const typename In<T>::raw &p0
   }
 }
 
-// Rows of queries and keys of up to kHeadsAhead heads at a time, a thread's own
-// unit and token: cosine and sine are taken once for all its heads.
+// Rows of queries and keys, a few heads at a time, a thread's own unit and token: cosine and sine are taken once for all its heads.
 struct RowsArg {
   const char *x[2];         // queries, keys
   char *out[2];
   int64_t x_t[2], x_h[2], o_t[2], o_h[2];   // bytes
   uint32_t heads[2];
 };
-constexpr uint32_t kHeadsAhead = 4;
 template <entro_dtype T, entro_dtype O, bool INTER>
 __device__ __forceinline__ void turn_rows(const RowsArg &a, const RotArg &r, uint32_t u, int64_t row, uint32_t place,
                                           uint32_t head0, uint32_t step) {
+  constexpr uint32_t kHeadsAhead = 8 / In<T>::kSize;   // heads whose loads go out together
   const Unit un = unit_of<INTER>(r, u);
   Turn t;
   if (un.turned) turn_at(t, r, u, row, place);
@@ -250,6 +254,7 @@ __device__ __forceinline__ void append_page(const AppendArg &arg, const KvItem &
       turn_at(t, arg.rot, u, it.first + r, it.place + r);
     }
     turned16<T, INTER>(kx[i], k0[i], k1[i], t, un.turned);
+    in_order();
 #pragma unroll
     for (int j = 0; j < 16; ++j) k_top = max(k_top, bits_of(kx[i][j]));
   }
@@ -257,6 +262,8 @@ __device__ __forceinline__ void append_page(const AppendArg &arg, const KvItem &
   for (int i = 0; i < 4; ++i)
     for (int j = 0; j < 8; ++j) v_top = max(v_top, bits_of(In<T>::get(vx[i], j)));
   wg_max2(k_top, v_top, red);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) In<T>::anew(vx[i]);
   if (max(k_top, v_top) >= 0x7F800000u) {   // the same in every thread
     k_top = v_top = 0;
 #pragma unroll
@@ -266,6 +273,8 @@ __device__ __forceinline__ void append_page(const AppendArg &arg, const KvItem &
     for (int i = 0; i < 4; ++i)
       for (int j = 0; j < 8; ++j) v_top = max(v_top, finite_bits(In<T>::get(vx[i], j)));
     wg_max2(k_top, v_top, red);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) In<T>::anew(vx[i]);
   }
   const Grow kg = grow(k_before, __builtin_bit_cast(float, k_top)), vg = grow(v_before, __builtin_bit_cast(float, v_top));
   if (tid == 0u) {
@@ -368,20 +377,22 @@ __device__ __forceinline__ void append_queries(const AppendArg &arg, uint32_t pa
 }
 
 template <entro_dtype T, entro_dtype O, int D, bool INTER>
-__global__ __launch_bounds__(512, 4) void kv_append_kernel(AppendArg arg, uint32_t page) {
+__global__ __launch_bounds__(512, T == ENTRO_F32 ? 2 : 4) void kv_append_kernel(AppendArg arg, uint32_t page) {
   const KvArg &a = arg.kv;
   const uint32_t lane = threadIdx.x & 63u;
   if (blockIdx.x == 0u && blockIdx.y == 0u) kv_check(a, page);
-  // rows of the grid: the heads' pages, then the queries' items, as many a row as
-  // there are pages
+  // rows of the grid: the heads' pages and the queries' items, as many a row as there
+  // are pages, the heads spread evenly among them: pages wait (for their largest values,
+  // for their turn through LDS) while queries stream
   const uint64_t rows = a.n_kv + (arg.q_items + a.items - 1u) / a.items;
   for (uint64_t y = blockIdx.y; y < rows; y += gridDim.y)
     for (uint64_t x = blockIdx.x; x < a.items; x += gridDim.x) {
-      if (y < a.n_kv) {
-        const KvItem it = kv_item(a, page, (uint32_t)x, (uint32_t)y, lane);
+      const uint64_t head = y * a.n_kv / rows;   // heads before row y
+      if ((y + 1u) * a.n_kv / rows != head) {
+        const KvItem it = kv_item(a, page, (uint32_t)x, (uint32_t)head, lane);
         if (it.any) append_page<T, D, INTER>(arg, it, page);
       } else {
-        const uint64_t item = (y - a.n_kv) * a.items + x;
+        const uint64_t item = (y - head) * a.items + x;
         if (item < arg.q_items) append_queries<T, O, D, INTER>(arg, page, (uint32_t)item, lane);
       }
     }
