@@ -28,6 +28,7 @@ struct ChunkArg {
   uint32_t heads, parts;        // query heads of a workgroup, workgroups per key/value head for all of them
   uint32_t block_log2;          // tokens of a workgroup
   uint32_t rows;                // rows (queries of a head) of a workgroup, at most
+  uint32_t join_groups;         // workgroups that join a block's pieces
   uint32_t shares;              // that the tiles of a key/value head are split into at most
   float scale;                  // magnitude, times log2(e)
   uint32_t q_xor;               // on a pair of q: the scale's sign
@@ -633,7 +634,10 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
       uint64_t now = sh.begin(w);
       const uint64_t end = sh.begin(w + 1u);
       at.find(now);
-      if (head_part == 0u && tid == 0u) a.cuts[w] = cut_of(a, at, sh, w);
+      if (head_part == 0u) {
+        const Cut cut = cut_of(a, at, sh, w);
+        if (tid == 0u) a.cuts[w] = cut;
+      }
       for (; now < end; at.next()) {
         const Seq s = at.here();
         const Blocks blocks(a.block_log2, s);
@@ -847,8 +851,8 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: 16, 32 or 64 in a workgroup.  A wavefront has 16 of them, and the wavefronts
-// of the same rows take turns at the tiles and are joined over LDS at the end of a piece.
+// Few rows: at most 64 in a block.  A wavefront has 16 of them, and where there are no more
+// than 32 or 16, the wavefronts of the same rows take turns at the tiles and are joined over LDS at the end of a piece.
 // Nothing of the cache passes through LDS: scores are K Q^T and outputs V^T P^T on
 // 16 x 16 x 32 matrix instructions with the rows as columns.  The first product's row
 // 4 g + r of its i-th part is token 16 g + 4 i + r of the tile: lane group g (16 lanes)
@@ -872,7 +876,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(ChunkArg a)
   float *red_o = reinterpret_cast<float *>(dyn_lds);                         // [kFewWaves][16][kRow]
   f32x4 *red_s = reinterpret_cast<f32x4 *>(red_o + kFewWaves * 16u * kRow);  // [kFewWaves][16]
   const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = rfl(tid >> 6), n = lane & 15u, grp = lane >> 4;
-  const uint32_t page = 1u << a.page_log2, sets = a.rows / 16u, set = wave % sets, phases = kFewWaves / sets;
+  const uint32_t page = 1u << a.page_log2;
   Place at(a, lane);
   if (blockIdx.x == 0u && blockIdx.y == 0u && wave == 0u) flag_lengths(a, lane);
   const Shares sh = shares_of(a, at.count_all());
@@ -900,6 +904,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(ChunkArg a)
         const int32_t *row = a.table + (uint64_t)at.seq * a.table_stride;
         const uint32_t token0 = at.block << a.block_log2;
         const uint32_t rows = min(1u << a.block_log2, s.count - token0) * heads;
+        const uint32_t sets = rows <= 16u ? 1u : rows <= 32u ? 2u : 4u, set = wave & (sets - 1u);   // of 16 rows
+        const uint32_t phases = kFewWaves / sets;
         // the lane's row (past the last, the last): the tokens that it sees, less the first
         // of the lane's block, the query as f16 times 2^-e, the score's factor
         const uint32_t own_row = min(16u * set + n, rows - 1u), token = token0 + own_row / heads, head = head0 + own_row % heads;
@@ -950,7 +956,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(ChunkArg a)
         // tile a wavefront fetches that one again: no branches.)  A block past the sequence's
         // end, or of a page that does not exist, takes page 0.
         bool bad = false;
-        const uint32_t first = t0 + wave / sets, count = t1 > first ? (t1 - first + phases - 1u) / phases : 0u;
+        const uint32_t first = t0 + (wave - set) / sets, count = t1 > first ? (t1 - first + phases - 1u) / phases : 0u;
         const uint32_t last = count ? count - 1u : 0u;
         const auto tile_of = [&](uint32_t k) { return first + min(k, last) * phases; };
         const auto token_of = [&](uint32_t four) {
@@ -1146,7 +1152,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(ChunkArg a)
 constexpr uint32_t kJoinSlots = 8;
 template <entro_dtype T, int D>
 __global__ __launch_bounds__(kJoinSlots * D / 4) void attn_chunk_join_kernel(ChunkArg a) {
-  const uint32_t kRows = a.rows, kGroups = kRows / kJoinSlots;
+  const uint32_t kRows = a.rows, kGroups = a.join_groups;
   __shared__ Joined red[kJoinSlots][D / 4];
   const uint32_t slot = threadIdx.x / (D / 4u), dq = threadIdx.x % (D / 4u);
   for (uint32_t w = 1u + blockIdx.y; w < a.shares; w += gridDim.y) {
@@ -1207,7 +1213,7 @@ static Plan plan_of(uint32_t n_seq, uint32_t total_q, uint32_t n_heads, uint32_t
   Plan p{};
   const uint32_t group = n_heads / n_kv;
   const uint64_t rows = (uint64_t)total_q * group;
-  p.waves = rows > 128ull * n_seq ? 8u : rows > 64ull * n_seq ? 4u : 0u;
+  p.waves = rows > 128ull * n_seq ? 8u : rows > 48ull * n_seq ? 4u : 0u;
   p.rows = p.waves ? 32u * p.waves : rows > 32ull * n_seq ? 64u : rows > 16ull * n_seq ? 32u : 16u;
   p.heads = std::min(group, p.rows);
   p.parts = (group + p.heads - 1u) / p.heads;
@@ -1229,7 +1235,7 @@ static entro_status launch_chunk(const ChunkArg &a, uint32_t waves, hipStream_t 
     hipLaunchKernelGGL((attn_few_kernel<T, D>), grid, dim3(64 * kFewWaves), kFewWaves * 16u * (D + 8u) * 4u, s, a);
   if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
   if (a.shares > 1u && a.total_q) {
-    hipLaunchKernelGGL((attn_chunk_join_kernel<T, D>), grid2((uint64_t)heads * (a.rows / kJoinSlots), a.shares - 1u),
+    hipLaunchKernelGGL((attn_chunk_join_kernel<T, D>), grid2((uint64_t)heads * a.join_groups, a.shares - 1u),
                        dim3(kJoinSlots * D / 4), 0, s, a);
     if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
   }
@@ -1292,6 +1298,7 @@ extern "C" entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv
   k.parts = p.parts;
   k.block_log2 = p.block_log2;
   k.rows = p.rows;
+  k.join_groups = std::max(p.rows / kJoinSlots, p.shares >= 32u * t->n_seq ? 16u : 0u);
   k.shares = p.shares;
   k.scale = std::fabs(a->scale) * kLog2e;
   k.q_xor = std::signbit(a->scale) ? 0x80008000u : 0u;
