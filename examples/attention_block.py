@@ -5,11 +5,13 @@ token by token.
 
 The q, k, v and o matrices are quantized to 4 bits, Huffman-coded and kept
 coded on the GPU.  A piece of the prompt goes through the fused decode + GEMM,
-its keys and values into the 8-bit cache and its attention through
-``attn_prompt`` (the second piece reads the first one's keys and values back
-from the cache); a new token goes through the fused decode + GEMV, the cache
-and ``attn_cache``.  Outputs are compared with the same block in float32 on the
-decoded weights without a cache: what differs is the cache's 8 bits.
+a new token through the fused decode + GEMV.  The first piece's queries and keys
+are turned by their positions (``rope``) and attend among themselves
+(``attn_prompt``) before the 8-bit cache takes keys and values; later pieces and
+tokens are turned and stored in one call (``kv_append``) and attend over the
+cache (``attn_chunk``, ``attn_cache``).  Outputs are compared with the same block
+in float32 on the decoded weights without a cache: what differs is the cache's
+8 bits.
 """
 from __future__ import annotations
 
@@ -68,7 +70,7 @@ def product(matrices, x):
 
 
 def rotate(x, first: int, base: float = 10000.0):
-    """Rotary position embedding of x [tokens][heads][dim] at positions first on."""
+    """Rotary position embedding of x [tokens][heads][dim] at positions first on, in torch."""
     import torch
 
     half = x.shape[2] // 2
@@ -93,6 +95,8 @@ class Block:
         self.cache = ent.KVCache.empty(pages, kv_heads, dim, page)
         self.table = torch.randperm(pages, device="cuda").to(torch.int32)[None].contiguous()
         self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        freqs = 10000.0 ** (-torch.arange(dim // 2, dtype=torch.float64) / (dim // 2))
+        self.rotary = ent.Rotary(freqs.float().cuda())
         self.held = 0
 
     def _ints(self, *v):
@@ -107,19 +111,21 @@ class Block:
 
         n, first = x.shape[0], self.held
         q, k, v = product((self.q, self.k, self.v), x)
-        q = rotate(q.view(n, self.heads, self.dim), first).to(torch.bfloat16)
-        k = rotate(k.view(n, self.kv_heads, self.dim), first).to(torch.bfloat16)
-        v = v.view(n, self.kv_heads, self.dim).to(torch.bfloat16)
-        if n > 1:
-            # the tokens in front from the cache, then this piece's own
-            kk, vv = (torch.empty(first + n, self.kv_heads, self.dim, dtype=torch.bfloat16, device="cuda") for _ in range(2))
-            ent.kv_load(self.cache, self.table, self._ints(0), self._ints(0, first), first, self.status,
-                        out=(kk[:first], vv[:first]))
-            kk[first:], vv[first:] = k, v
-            y = ent.attn_prompt(q, kk, vv, self._ints(0, n), self._ints(0, first + n), self.status)
-        ent.kv_store(self.cache, k, v, self.table, self._ints(first), self._ints(0, n), self.status)
-        if n == 1:
-            y = ent.attn_cache(q, self.cache, self.table, self._ints(first + 1), self.status)
+        # float32 from the products, bf16 for attention
+        q, k, v = q.view(n, self.heads, self.dim), k.view(n, self.kv_heads, self.dim), v.view(n, self.kv_heads, self.dim)
+        if first == 0 and n > 1:
+            # nothing in front: attention over the piece itself, in 16 bits
+            at = torch.arange(n, dtype=torch.int32, device="cuda")
+            q, k = ent.rope(self.rotary, q, k, at, dtype=torch.bfloat16)
+            v = v.to(torch.bfloat16)
+            y = ent.attn_prompt(q, k, v, self._ints(0, n), self._ints(0, n), self.status)
+            ent.kv_store(self.cache, k, v, self.table, self._ints(0), self._ints(0, n), self.status)
+        else:
+            q = ent.kv_append(self.cache, self.rotary, k, v, self.table, self._ints(first), self._ints(0, n), self.status,
+                              q=q, dtype=torch.bfloat16)
+            lens = self._ints(first + n)
+            y = (ent.attn_cache(q, self.cache, self.table, lens, self.status) if n == 1 else
+                 ent.attn_chunk(q, self.cache, self.table, lens, self._ints(0, n), self.status))
         self.held = first + n
         return product((self.o,), y.view(n, self.heads * self.dim))[0]
 
