@@ -1,5 +1,15 @@
 // HIP kernels (gfx950) and entry points of the attention of chunks over the 8-bit
 // cache: entro_attn_chunk.  Layout and definition are in entro_attn.h.
+//
+// One pass over a block's tiles with a running maximum and sum; the work of all blocks
+// is cut into equal shares, one workgroup each, and a second kernel joins the pieces of
+// blocks that were cut.  Two first kernels: attn_chunk_kernel for many rows, by way of
+// LDS, and attn_few_kernel for few.
+//
+// Measured on an MI355X (copy 4.8 TB/s, 16384^3 f16 product 1300 TFLOP/s): 2048 tokens
+// behind 30720, 32 / 8 heads of 128, bf16: 1.10 ms, 969 TFLOP/s; 61 tokens behind 40003,
+// 64 / 8 heads of 128, f16: 115 us; 24 sequences of up to 7 tokens behind up to 12000,
+// 32 / 8 heads of 128: 56 us; 5 tokens behind 85, 32 heads of 64: 9.2 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -9,7 +19,7 @@
 namespace entro {
 
 constexpr uint32_t kTile = 64;          // tokens of a step
-constexpr uint32_t kShareTiles = 6;     // least work of a workgroup's share, in tiles
+constexpr uint32_t kShareTiles = 6;     // least work of a workgroup's share, in tiles: less is a join that costs more
 constexpr float kFloatMax = 3.40282347e38f;
 
 struct ChunkArg {
@@ -346,7 +356,7 @@ __device__ __forceinline__ f32x16 mfma(f16v8 a, f16v8 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-template <int D, int W>
+template <int D>
 struct Lds {
   static constexpr uint32_t kRow = D * 2 + 16;          // bytes of a key's row and
   static constexpr uint32_t vRow = kTile * 2 + 16;      // of a dimension's: rows begin four banks further
@@ -610,10 +620,23 @@ struct Joined {
 // where they are, are the second product's operand: row 16 c + 8 i + 4 h + j is token
 // 16 c + 8 h + 4 i + j.  A lane then has eight tokens of each 16, which are of one
 // page: its scales are the same in the whole wavefront.
+//
+// Codes are exact in f16, and so are a bf16 query's elements down to 2^-17 of its largest
+// (they go in times the power of two that makes that 1 to 2; smaller ones are off by 2^-25
+// of it).  What is rounded to fewer than 32 bits is the weights: f16, half a step 2^-12, as
+// the matrix instruction takes them; fast_tile's sum is of the rounded ones.
+//
+// Bound: with many rows the matrix instructions and the softmax's vector instructions
+// between them share the issue slots (four wavefronts of a SIMD pair cannot hide all of
+// it: 969 of 1300 TFLOP/s); with one block per sequence the way of a tile through
+// registers and LDS, 0.65 us a tile and workgroup.  256 rows in a workgroup (W = 8)
+// halve that way's cost per row, 128 (W = 4) waste less where sequences have fewer:
+// 2048 tokens behind 30720, 1141 us with W = 8 and 1245 with W = 4; 61 behind 40003 with
+// 8 heads sharing, 77 and 84; 24 of up to 60 tokens with 4 sharing, 77 and 60.
 // ---------------------------------------------------------------------------
 template <entro_dtype T, int D, int W>
 __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
-  typedef Lds<D, W> L;
+  typedef Lds<D> L;
   constexpr int KS = D / 16;                       // products over the dimensions
   constexpr int DT = D / 32;                       // 32-dimension parts of the output
   constexpr int PT = 8 / W;                        // 16-byte pieces of a tile's keys, and of its values, for a thread
@@ -858,6 +881,11 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
 // 4 g + r of its i-th part is token 16 g + 4 i + r of the tile: lane group g (16 lanes)
 // then holds 16 consecutive tokens of a row, of one page, just the 16 bytes of codes that
 // it reads of one dimension, and 64 bytes of a key or of a dimension are read side by side.
+// (With 32 x 32 x 16 products a key gives 32 bytes a read: 24 sequences of up to 7 tokens,
+// 61 us instead of 50.)
+//
+// Bound: the wait for a tile's codes; a wavefront has 16 KB on the way, and the queue of
+// a CU's eight is 4 TB/s of the 6.4 that reads alone reach.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kFewWaves = 4;
 
@@ -1148,7 +1176,8 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(ChunkArg a)
 // Joins the pieces of the blocks that were cut: kJoinSlots slots of D / 4 threads, four
 // dimensions each, for the first cut in a block.  A slot takes whole rows; where there
 // are many pieces the slots take every kJoinSlots-th piece of one row and are joined
-// over LDS.  Four pieces' reads at once; the order is the same in every call.
+// over LDS.  Four pieces' reads at once; the order is the same in every call.  Its time
+// is that of its waits: 2 to 15 us.
 constexpr uint32_t kJoinSlots = 8;
 template <entro_dtype T, int D>
 __global__ __launch_bounds__(kJoinSlots * D / 4) void attn_chunk_join_kernel(ChunkArg a) {
@@ -1213,11 +1242,17 @@ static Plan plan_of(uint32_t n_seq, uint32_t total_q, uint32_t n_heads, uint32_t
   Plan p{};
   const uint32_t group = n_heads / n_kv;
   const uint64_t rows = (uint64_t)total_q * group;
+  // By the rows of a sequence on average (the lengths are on the device).  Up to 48 the
+  // kernel for few rows: 24 sequences of up to 16 tokens behind up to 6000, 32 / 8 heads
+  // of 128 (34 rows on average), 38.6 us instead of 44.9; 4 tokens behind 40000 30.6
+  // instead of 36.5.  Above that its blocks are too small: 16 tokens behind 40000 (64
+  // rows), 66.6 us instead of 59.4.
   p.waves = rows > 128ull * n_seq ? 8u : rows > 48ull * n_seq ? 4u : 0u;
   p.rows = p.waves ? 32u * p.waves : rows > 32ull * n_seq ? 64u : rows > 16ull * n_seq ? 32u : 16u;
   p.heads = std::min(group, p.rows);
   p.parts = (group + p.heads - 1u) / p.heads;
   while ((2u << p.block_log2) * p.heads <= p.rows) ++p.block_log2;
+  // as many workgroups as the GPU holds at once: 1, 2 or (heads of 64) 3 a CU
   p.shares = std::max(1u, (p.waves == 8u ? 256u : p.waves == 4u && head_dim == 64u ? 768u : 512u) / (n_kv * p.parts));
   return p;
 }
@@ -1228,9 +1263,9 @@ static entro_status launch_chunk(const ChunkArg &a, uint32_t waves, hipStream_t 
   const dim3 grid = grid2(heads, a.shares);
   (void)hipGetLastError();
   if (waves == 8u)
-    hipLaunchKernelGGL((attn_chunk_kernel<T, D, 8>), grid, dim3(512), (Lds<D, 8>::bytes), s, a);
+    hipLaunchKernelGGL((attn_chunk_kernel<T, D, 8>), grid, dim3(512), Lds<D>::bytes, s, a);
   else if (waves == 4u)
-    hipLaunchKernelGGL((attn_chunk_kernel<T, D, 4>), grid, dim3(256), (Lds<D, 4>::bytes), s, a);
+    hipLaunchKernelGGL((attn_chunk_kernel<T, D, 4>), grid, dim3(256), Lds<D>::bytes, s, a);
   else
     hipLaunchKernelGGL((attn_few_kernel<T, D>), grid, dim3(64 * kFewWaves), kFewWaves * 16u * (D + 8u) * 4u, s, a);
   if (hipGetLastError() != hipSuccess) return ENTRO_E_HIP;
@@ -1251,6 +1286,7 @@ extern "C" uint64_t entro_attn_chunk_work_bytes(uint32_t n_seq, uint32_t total_q
   if (n_seq == 0 || total_q == 0 || total_q > 0x7FFFFFFFu || check_heads(n_heads, n_kv_heads, head_dim, ENTRO_BF16) != ENTRO_OK)
     return 0;
   const Plan p = plan_of(n_seq, total_q, n_heads, n_kv_heads, head_dim);
+  if (p.shares == 1u) return 16u;   // (no block is cut)
   return (uint64_t)n_kv_heads * p.parts * p.shares * 2u * p.rows * (head_dim + 4u) * 4u + 16u * p.shares;
 }
 
@@ -1298,6 +1334,9 @@ extern "C" entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv
   k.parts = p.parts;
   k.block_log2 = p.block_log2;
   k.rows = p.rows;
+  // (more for a sequence with many pieces: 4 tokens behind 40000, 30.6 us instead of 52.6;
+  // where there are few, the workgroups without rows cost: 24 of up to 7 tokens, 11 us
+  // instead of 6)
   k.join_groups = std::max(p.rows / kJoinSlots, p.shares >= 32u * t->n_seq ? 16u : 0u);
   k.shares = p.shares;
   k.scale = std::fabs(a->scale) * kLog2e;
