@@ -499,3 +499,11 @@ def test_prompt_in_pieces(ent, dtype):
             assert np.linalg.norm(out[i] - want) <= 0.03 * np.linalg.norm(want)
         held = lens
     assert not status.any()
+
+
+@pytest.mark.parametrize("new,lens", [([3, 1, 0, 16], [400, 70, 5, 16]), ([60, 33], [300, 33]), ([140], [141])], ids=str)
+def test_chunk_more_heads_than_workgroups_at_once(ent, new, lens):
+    """So many key/value heads that no block is cut: the workspace is nominal."""
+    say(f"chunk of 520 key/value heads {new} {lens}")
+    assert ent.attn_chunk_work_bytes(len(new), sum(new), 520, 520, 64) == 16
+    run(ent, (520, 520, 64), "bf16", 16, new, lens)
