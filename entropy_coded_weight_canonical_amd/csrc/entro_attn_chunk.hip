@@ -415,7 +415,7 @@ __device__ __forceinline__ void products(f32x16 *x, const Tile<L> &tile, int fro
   }
 }
 
-constexpr float kLag = 3.0f, kRoom = 12.875f;   // see fast_tile
+constexpr float kLag = 3.0f, kRoom = 12.875f, kNear = 2048.0f;   // see fast_tile
 // How an ordinary tile changes a row's state: mx is its largest score, most and least the
 // logarithms of its pages' value scales.
 struct Rise {
@@ -426,7 +426,7 @@ struct Rise {
     rise = move || mx > st.m + kLag || none;
     g = move ? most - kRoom : st.g;
     m = fmaxf(st.m, mx);
-    near = (fabsf(m) < 32768.0f || m == -INFINITY) && (none || fabsf(g - st.g) <= 60.0f);
+    near = (fabsf(m) < kNear || m == -INFINITY) && (none || fabsf(g - st.g) <= 60.0f);
   }
   // returns the factor of the outputs
   __device__ float apply(State &st) const {
@@ -448,9 +448,10 @@ struct Rise {
 // that is one pass over the outputs.  False, and nothing done, for tiles that are not
 // ordinary: values' scales more than a factor of 2^kSpread from one another or near the
 // ends of the range, keys' not finite or close to 0 (a hidden score is -infinity times
-// them), scores so far from 0 that a fused difference
-// would have a rounding of the score left over, values so far from the unit that moving
-// it could lose them.  (NaN fails.)
+// them), scores so far from 0 (2^11: m + g is off by 2^-14) that a fused difference
+// would have a rounding of the score left over (in a tile that does not raise m, too: m
+// may have been raised by one that was not ordinary), values so far from the unit that
+// moving it could lose them.  (NaN fails.)
 template <typename L, int DT>
 __device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x16 (&x)[2], const Tile<L> &tile,
                                           const Scales &scales, float c) {
@@ -465,7 +466,7 @@ __device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x
   }
   // (all of it before the outputs are touched: with ways out in between they are copied)
   const Rise up(st, max32(mx), lane_of(scales.most, tile.at), lane_of(scales.least, tile.at));
-  if ((scales.fine >> tile.at & 15u) != 15u || __any(up.rise && !up.near)) return false;
+  if ((scales.fine >> tile.at & 15u) != 15u || __any(!up.near)) return false;
   if (__any(up.rise)) {
     const float less = up.apply(st);
     results_there();
@@ -1060,7 +1061,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(ChunkArg a)
               for (int i = 0; i < 4; ++i)
                 for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[i][r]);
               const Rise up(st, max_of_row(mx * sc), lane_of(scales.most, its), lane_of(scales.least, its));
-              if (!(plain && (scales.fine >> its & 15u) == 15u && !__any(up.rise && !up.near))) {
+              if (!(plain && (scales.fine >> its & 15u) == 15u && !__any(!up.near))) {
                 // as slow_tile, a block at a time: the others' lanes have weights of 0.  The
                 // outputs pass through LDS: such tiles take time, but no registers.
                 float *const own_o = red_o + (wave * 16u + n) * kRow + 4u * grp;
