@@ -265,8 +265,9 @@ __device__ __forceinline__ Cut cut_of(const ChunkArg &a, const Place &at, const 
 // What is known of a row (one query of one head) beside its outputs, in powers of
 // two: the largest score m, the weights' sum l relative to 2^m, and the exponent g
 // of the outputs' unit, relative to 2^m too.  top: the largest exponent, less m, with
-// which values have been added (their scale's times their weight's); the unit stays
-// near it, so that outputs keep their bits whatever the pages' scales are.
+// which values have been added (their scale's times their weight's; in an ordinary
+// tile, to 2^kSpread); the unit stays within kApart of kUnit below it, so that outputs
+// keep their bits whatever the pages' scales are, one after another.
 struct State {
   float m, l, g, top;
   // of the weights: -g - m (m: 0 where nothing was seen), and 2^g
@@ -277,6 +278,7 @@ struct State {
   }
 };
 constexpr float kUnit = 11.5f;   // the unit lies by about as much below top
+constexpr float kApart = 30.0f;  // (2^31 values then sum up to 2^83)
 constexpr float kSpread = 2.75f; // and a tile's scales that are ordinary by as much from one another at most
 
 // log2 of a page's value scale (below 2^-126: 0)
@@ -415,31 +417,36 @@ __device__ __forceinline__ void products(f32x16 *x, const Tile<L> &tile, int fro
   }
 }
 
-constexpr float kLag = 3.0f, kRoom = 12.875f, kNear = 2048.0f;   // see fast_tile
-// How an ordinary tile changes a row's state: mx is its largest score, most and least the
-// logarithms of its pages' value scales.
+constexpr float kLag = 3.0f, kRoom = 12.875f, kNear = 2048.0f, kUnder = 8.0f;   // see fast_tile
+// How an ordinary tile changes a row's state: mx is its largest score (-infinity: the row
+// sees nothing of it, and nothing changes), most and least the logarithms of its pages'
+// value scales.
 struct Rise {
-  float m, g;
+  float m, g, up;
   bool rise, near;
   __device__ Rise(const State &st, float mx, float most, float least) {
-    const bool move = !(most - st.g <= kRoom + 0.025f && least - st.g >= 10.0f), none = st.top == -INFINITY;
-    rise = move || mx > st.m + kLag || none;
+    const bool seen = mx > -INFINITY;
+    const bool move = seen && !(most - st.g <= kRoom + 0.025f && least - st.g >= 10.0f);
+    rise = move || mx > st.m + kLag;
     g = move ? most - kRoom : st.g;
     m = fmaxf(st.m, mx);
-    near = (fabsf(m) < kNear || m == -INFINITY) && (none || fabsf(g - st.g) <= 60.0f);
+    up = m == st.m ? 0.0f : m - st.m;
+    const float over = fmaxf(st.top - up, mx - m + most) - kUnit - g;
+    near = !seen || (fabsf(m) < kNear && over <= kApart && over >= -kUnder);
   }
   // returns the factor of the outputs
   __device__ float apply(State &st) const {
-    const bool none = st.top == -INFINITY;
-    const float up = m == -INFINITY ? 0.0f : m - st.m, k = exp2_fast(-up), ko = none ? 0.0f : k * exp2_fast(st.g - g);
-    st.l *= k;
-    st.top = m == -INFINITY ? -INFINITY : fmaxf(st.top - up, g + kUnit);
+    const float k = st.top == -INFINITY ? 0.0f : exp2_fast(st.g - g - up);   // (no value added yet: any unit)
+    st.l *= exp2_fast(-up);
+    st.top -= up;
     st.m = m;
     st.g = g;
     st.settle();
-    return ko;
+    return k;
   }
 };
+// The top with an ordinary tile's values, once the state has risen where it does.
+__device__ __forceinline__ float with_tile(const State &st, float mx, float most) { return fmaxf(st.top, mx - st.m + most); }
 
 // A tile whose scales and scores are ordinary ones: weights go into the product with
 // their page's value scale, as 2^(t - m + log2(scale) - g), where g is held such that
@@ -450,8 +457,10 @@ struct Rise {
 // ends of the range, keys' not finite or close to 0 (a hidden score is -infinity times
 // them), scores so far from 0 (2^11: m + g is off by 2^-14) that a fused difference
 // would have a rounding of the score left over (in a tile that does not raise m, too: m
-// may have been raised by one that was not ordinary), values so far from the unit that
-// moving it could lose them.  (NaN fails.)
+// may have been raised by one that was not ordinary), a unit for the tile's values that
+// lies far from the top's: kApart below it, moved tile after tile, the outputs would run
+// out of their range; kUnder above it, large values' weights would be f16's smallest.
+// (NaN fails.)
 template <typename L, int DT>
 __device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x16 (&x)[2], const Tile<L> &tile,
                                           const Scales &scales, float c) {
@@ -465,7 +474,9 @@ __device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x
     mx = fmaxf(mx, most * sc[b]);
   }
   // (all of it before the outputs are touched: with ways out in between they are copied)
-  const Rise up(st, max32(mx), lane_of(scales.most, tile.at), lane_of(scales.least, tile.at));
+  mx = max32(mx);
+  const float most = lane_of(scales.most, tile.at);
+  const Rise up(st, mx, most, lane_of(scales.least, tile.at));
   if ((scales.fine >> tile.at & 15u) != 15u || __any(!up.near)) return false;
   if (__any(up.rise)) {
     const float less = up.apply(st);
@@ -473,6 +484,7 @@ __device__ __forceinline__ bool fast_tile(State &st, f32x16 (&o)[DT], const f32x
 #pragma unroll
     for (int d = 0; d < DT; ++d) scale_in_place(o[d], less);
   }
+  st.top = with_tile(st, mx, most);
   // the weights of the next 16 tokens between the products of these
   u32x4 p[2];
   float part = 0.0f, sum = 0.0f;
@@ -516,7 +528,7 @@ struct Block {
     const float up = m - st.m, down = mx - m;
     top = fmaxf(st.top - up, down + v.log);
     g = st.g;
-    if (top > -kFloatMax && !(fabsf(top - kUnit - g) <= 30.0f)) g = top - kUnit;
+    if (top > -kFloatMax && !(fabsf(top - kUnit - g) <= kApart)) g = top - kUnit;
     less = exp2_fast(-up);
     part = exp2_fast(down);
     keep = any ? exp2_fast(st.g - g - up) : 1.0f;
@@ -1060,7 +1072,9 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(ChunkArg a)
 #pragma unroll
               for (int i = 0; i < 4; ++i)
                 for (int r = 0; r < 4; ++r) mx = fmaxf(mx, x[i][r]);
-              const Rise up(st, max_of_row(mx * sc), lane_of(scales.most, its), lane_of(scales.least, its));
+              mx = max_of_row(mx * sc);
+              const float most = lane_of(scales.most, its);
+              const Rise up(st, mx, most, lane_of(scales.least, its));
               if (!(plain && (scales.fine >> its & 15u) == 15u && !__any(!up.near))) {
                 // as slow_tile, a block at a time: the others' lanes have weights of 0.  The
                 // outputs pass through LDS: such tiles take time, but no registers.
@@ -1115,11 +1129,14 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(ChunkArg a)
                 by = rcp = 0.0f;
                 sc = 1.0f;
                 for (int i = 0; i < 4; ++i) x[i] = (f32x4){-0x1p120f, -0x1p120f, -0x1p120f, -0x1p120f};
-              } else if (__any(up.rise)) {
-                const float less = up.apply(st);
-                results_there();
+              } else {
+                if (__any(up.rise)) {
+                  const float less = up.apply(st);
+                  results_there();
 #pragma unroll
-                for (int d = 0; d < DT; ++d) scale_in_place(o[d], less);
+                  for (int d = 0; d < DT; ++d) scale_in_place(o[d], less);
+                }
+                st.top = with_tile(st, mx, most);
               }
               u32x4 p[2];
               float sum = 0.0f;
