@@ -841,7 +841,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
               for (int j = kSteps * i / (2 * KS); j < kSteps * (i + 1) / (2 * KS); ++j) ahead(j);
             });
             const int32_t seen = limit - (int32_t)(t * kTile);
-            if ((int32_t)(t * kTile + kTile) > least) {
+            if (least - (int32_t)(t * kTile) < (int32_t)kTile) {   // (t kTile + kTile may be 2^31)
               results_there();
 #pragma unroll
               for (int b = 0; b < 4; ++b) hide_in_place(x[b >> 1], b, seen);
@@ -1058,7 +1058,7 @@ __global__ __launch_bounds__(64 * kFewWaves, 2) void attn_few_kernel(ChunkArg a)
               }
               fetch_keys(k + 1u, (k & 3u) == 3u ? pages_next : pages);
               const int32_t seen = limit - (int32_t)(tile_of(k) * kTile);
-              if ((int32_t)(tile_of(k) * kTile + kTile) > least) {
+              if (least - (int32_t)(tile_of(k) * kTile) < (int32_t)kTile) {   // (the tile may end at 2^31)
                 results_there();
 #define ENTRO_HIDE(I)                                   \
   x[I][0] = hidden<4 * I>(x[I][0], seen);               \
