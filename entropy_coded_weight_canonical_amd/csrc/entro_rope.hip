@@ -74,9 +74,14 @@ __device__ __forceinline__ Unit unit_of(const RotArg &r, uint32_t u) {
   return {16u * u, 16u * u + 8u, turned};
 }
 
-// Cosine and sine of a unit's eight pairs at one token.  position * freqs is exact
-// in 64 bits for positions below 2^29; the angle in turns is brought to -1/2 .. 1/2
-// there, where 32 bits hold it to 2^-26, which is what the cosine instruction takes.
+// Cosine and sine of a unit's eight pairs at one token.  Whole turns are taken out of
+// position * (freqs / (2 pi)) in 64 bits by a fused product, so that the rest, -1/2 ..
+// 1/2, is off by no more than the factor is: 1.56 * 2^-53 of the angle, 2^-53 for its
+// rounding and 0.56 * 2^-53 for that of 1 / (2 pi).  (With the factor as two 64-bit
+// numbers it would be off by 2^-52 of a turn wherever, and rope_kernel take 4 % more where
+// a thread has one head: 64-bit angles have the former error in any case.)  The cosine
+// instruction takes the rest in 32 bits, off by 2^-26 of a turn (2^-23.3 as an angle), and
+// is off by 2^-22.9 itself (over all 32-bit numbers of the range): together below 2^-22.
 struct Turn {
   float c[8], s[8];
 };
@@ -96,8 +101,8 @@ __device__ __forceinline__ void turn_at(Turn &t, const RotArg &r, uint32_t u, in
       const uint32_t a = (bits >> (2 * j)) & 3u;
       at = a == 0u ? p[0] : a == 1u ? p[1] : a == 2u ? p[2] : p[3];
     }
-    const double x = (double)at * (double)(j < 4 ? f0[j & 3] : f1[j & 3]) * kTurn;
-    const float y = (float)(x - __builtin_rint(x));
+    const double by = (double)(j < 4 ? f0[j & 3] : f1[j & 3]) * kTurn, way = (double)at;
+    const float y = (float)__builtin_fma(way, by, -__builtin_rint(way * by));
     t.c[j] = __builtin_amdgcn_cosf(y) * r.gain;
     t.s[j] = __builtin_amdgcn_sinf(y) * r.gain;
     if (j % 2) in_order();   // (eight at once take registers for eight products of 64 bits)

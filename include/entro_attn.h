@@ -226,8 +226,8 @@ entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv_table *t, 
  * Further elements are left as they are.  A token has a position on each of n_axes
  * axes (1 for text; time, height and width of an image's or video's patches, for
  * one) and each pair belongs to one of them.  Positions are any 32-bit integers:
- * angles are computed in 64 bits and brought to one turn there, cosine and sine are
- * then taken in 32 bits (off by at most 2^-21). */
+ * angles are brought to one turn in 64 bits, cosine and sine are then taken in 32 bits.
+ * They are off by at most 2^-22 + 2^-52 |position * d_freqs[i]|. */
 typedef struct {
   const float *d_freqs;    /* [pairs] radians per position */
   uint32_t pairs;          /* a multiple of 8, at most head_dim / 2 */
