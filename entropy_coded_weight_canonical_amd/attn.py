@@ -13,7 +13,8 @@ its tensors; their memory is kept until a torch stream has used them (on a raw
 handle that, too, is the caller's).  ``status`` is an int32 tensor with one entry per sequence,
 zeroed by the caller, in which faults found in the data are OR-ed
 (``FLAGS["length"]``, ``FLAGS["page"]``).  There is no backward pass: operands that
-require a gradient are refused outside ``torch.no_grad()``.
+require a gradient are refused outside ``torch.no_grad()``, and ones that carry a
+forward-mode tangent wherever forward mode is on.
 """
 from __future__ import annotations
 

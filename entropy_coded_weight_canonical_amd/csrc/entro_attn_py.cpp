@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/AutogradState.h>
 #include <c10/core/DeviceGuard.h>
 #include <c10/core/GradMode.h>
 #include <torch/csrc/Exceptions.h>
@@ -55,13 +56,16 @@ const at::Tensor &tensor(PyObject *o, const char *what) {
 
 // All tensors of a call are on the device of the first one that is named (the
 // call's, which the kernels run on), and none is one that a gradient is recorded
-// for: there is no backward pass.  Looked at before anything is read or made.
+// for or that carries a tangent: there is no derivative, backward or forward.  Looked at
+// before anything is read or made.
 struct Together {
   const at::Device device;
   const Together &operator()(const char *what, const at::Tensor &x) const {
     if (x.device() != device) refuse(what, ": on device ", x.device(), ", the call is on ", device);
     if (x.requires_grad() && c10::GradMode::is_enabled())
       refuse(what, ": requires a gradient, and there is no backward pass; call under torch.no_grad() or detach it");
+    if (x._fw_grad(/*level=*/0).defined() && c10::AutogradState::get_tls_state().get_fw_grad_mode())
+      refuse(what, ": carries a tangent, and there is no forward-mode derivative; unpack it first");
     return *this;
   }
 };
