@@ -334,8 +334,8 @@ def attn_chunk(q, cache: KVCache, table, lens, cu_q, status, scale=None, out=Non
     ``cu_q``, ``lens`` the tokens of each sequence in the cache, its chunk's (the
     last of them) among them.  ``work``: a contiguous tensor of at least
     ``attn_chunk_work_bytes`` bytes that no call on another stream uses meanwhile
-    (made for the call by default).  Returns ``out`` [rows][heads][dim] (rows of no
-    sequence are left as they are)."""
+    (made for the call by default).  Returns ``out`` [rows][heads][dim], which must
+    not overlap ``q`` (rows of no sequence are left as they are)."""
     e = _ext or _load_ext()
     if stream is not None:
         return _on(stream, e.attn_chunk, q, cache, table, lens, cu_q, status, scale, out, work)

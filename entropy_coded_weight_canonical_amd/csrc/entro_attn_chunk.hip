@@ -1275,6 +1275,16 @@ static Plan plan_of(uint32_t n_seq, uint32_t total_q, uint32_t n_heads, uint32_t
   return p;
 }
 
+// Whether outputs lie where queries do, which workgroups that share a block still read:
+// where both begin at the same place, or both are without gaps.  (Slices of one tensor
+// may lie between one another.)
+static bool same_place(const entro_rows &q, const entro_rows &out, uint32_t rows, uint32_t n_heads, uint32_t dim) {
+  if (rows == 0) return false;
+  const auto dense = [&](const entro_rows &x) { return x.stride_h == dim && x.stride_t == (int64_t)n_heads * dim; };
+  const uintptr_t a = reinterpret_cast<uintptr_t>(q.d), b = reinterpret_cast<uintptr_t>(out.d);
+  return a == b || (dense(q) && dense(out) && std::max(a, b) - std::min(a, b) < 2ull * rows * n_heads * dim);
+}
+
 template <entro_dtype T, int D>
 static entro_status launch_chunk(const ChunkArg &a, uint32_t waves, hipStream_t s) {
   const uint32_t heads = a.n_kv * a.parts;
@@ -1322,6 +1332,7 @@ extern "C" entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv
     st = check_rows(*r, a->total_q);
     if (st != ENTRO_OK) return st;
   }
+  if (same_place(a->q, a->out, a->total_q, a->n_heads, c->head_dim)) return ENTRO_E_INVAL;
   const uint64_t need = entro_attn_chunk_work_bytes(t->n_seq, a->total_q, a->n_heads, c->n_kv_heads, c->head_dim);
   if (need && (!a->d_work || (reinterpret_cast<uintptr_t>(a->d_work) & 15u) || a->work_bytes < need)) return ENTRO_E_INVAL;
   const Plan p = plan_of(t->n_seq, a->total_q, a->n_heads, c->n_kv_heads, c->head_dim);

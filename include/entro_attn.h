@@ -216,7 +216,9 @@ uint64_t entro_attn_chunk_work_bytes(uint32_t n_seq, uint32_t total_q, uint32_t 
  * power of two per query and head (exact but for values below 2^-17 of the row's
  * largest, which are rounded at 2^-25 of it), the weights in f16 for the product
  * with the values, everything else in 32 bits.  The result does not depend on
- * timing.  Row strides up to 2^31 - 1 elements; at most 2^31 - 1 rows. */
+ * timing.  Row strides up to 2^31 - 1 elements; at most 2^31 - 1 rows.  out must not
+ * overlap the inputs (ENTRO_E_INVAL where it begins where q does, or where both are
+ * without gaps; slices of one tensor that lie between one another are the caller's). */
 entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv_table *t, const entro_attn_chunk_args *a,
                               uint32_t *d_status, hipStream_t stream);
 
