@@ -1,6 +1,8 @@
 """GPU tests of the attention of chunks where the values' scales move by up to 2^59
 from one tile of 64 tokens to the next, each tile's being equal, so that the outputs'
 unit would follow them step by step; bounds as in test_gpu_attn_chunk_far.py."""
+import random
+
 import pytest
 
 from tests.test_gpu_attn import ints, say
@@ -70,6 +72,37 @@ def test_large_values_of_low_scores(ent, kernel, behind, log):
         attend(ent, "bf16", 64, kernel, codes, scales, 0.25)
     if kernel != "turns":
         attend(ent, "f16", 64, kernel, [behind, 0, 0, 0], [2.0 ** (x - log) for x in (0, log, log, 0)], 0.25)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_scales_and_scores_at_random(ent, kernel):
+    """Tiles' scales and scores drawn over wide ranges, apart and together."""
+    say(f"chunk: scales and scores at random, {kernel}")
+    rng = random.Random(5)
+    for i in range(30):
+        tiles = KERNELS[kernel][1] + (0 if kernel == "turns" else rng.randint(0, 4))
+        wide = rng.choice((3, 12, 40, 90))
+        far = rng.choice((0, 1, 8, 60))
+        logs = [rng.uniform(-wide, wide) for _ in range(tiles)]
+        if rng.random() < 0.3:
+            logs = sorted(logs, reverse=rng.random() < 0.5)
+        keys = [rng.randint(-far, far) for _ in range(tiles)]
+        if rng.random() < 0.3:      # the scores make up for the scales
+            keys = [round(max(-127, min(127, far / 16 - x))) for x in logs]
+        attend(ent, "bf16", 64, kernel, keys, [2.0 ** x for x in logs], rng.choice((0.25, 0.1733)), less=rng.randint(0, 63))
+
+
+@pytest.mark.parametrize("kernel", ["few", "four", "eight"])
+def test_pieces_at_random(ent, kernel):
+    """The same over sequences that are cut into pieces, with scores up to 2^30."""
+    say(f"chunk: pieces of scales and scores at random, {kernel}")
+    rng = random.Random(6)
+    for i in range(16):
+        tiles = rng.randint(14, 50)
+        wide, far, scale = rng.choice((3, 12, 40, 90)), rng.choice((0, 1, 8, 60)), rng.choice((0.25, 0.1733, 2.0 ** 9, 2.0 ** 22))
+        logs = [rng.uniform(-wide, wide) for _ in range(tiles)]
+        keys = [rng.randint(-far, far) for _ in range(tiles)]
+        attend(ent, "bf16", 64, kernel, keys, [2.0 ** x for x in logs], scale, less=rng.randint(0, 63))
 
 
 @pytest.mark.parametrize("new,heads", [(20, (2, 1)), (24, (1, 1)), (30, (2, 1)), (80, (2, 1)), (130, (1, 1))], ids=str)
