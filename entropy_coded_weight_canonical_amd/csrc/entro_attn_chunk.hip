@@ -7,9 +7,10 @@
 // LDS, and attn_few_kernel for few.
 //
 // Measured on an MI355X (copy 4.8 TB/s, 16384^3 f16 product 1300 TFLOP/s): 2048 tokens
-// behind 30720, 32 / 8 heads of 128, bf16: 1.10 ms, 969 TFLOP/s; 61 tokens behind 40003,
-// 64 / 8 heads of 128, f16: 115 us; 24 sequences of up to 7 tokens behind up to 12000,
-// 32 / 8 heads of 128: 56 us; 5 tokens behind 85, 32 heads of 64: 9.2 us.
+// behind 30720, 32 / 8 heads of 128, bf16: 1.09 to 1.19 ms, 900 to 975 TFLOP/s as the card's
+// clock goes; 61 tokens behind 40003, 64 / 8 heads of 128, f16: 115 us; 24 sequences of up to
+// 7 tokens behind up to 12000, 32 / 8 heads of 128: 56 us; 5 tokens behind 85, 32 heads of 64:
+// 9.2 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -34,7 +35,7 @@ struct ChunkArg {
   int64_t q_t, q_h, o_t, o_h;   // bytes
   const int32_t *cu, *lens;
   uint32_t total_q;
-  uint32_t n_heads, group;      // group: query heads per key/value head
+  uint32_t group;               // query heads per key/value head
   uint32_t heads, parts;        // query heads of a workgroup, workgroups per key/value head for all of them
   uint32_t block_log2;          // tokens of a workgroup
   uint32_t rows;                // rows (queries of a head) of a workgroup, at most
@@ -639,13 +640,14 @@ struct Joined {
 // of it).  What is rounded to fewer than 32 bits is the weights: f16, half a step 2^-12, as
 // the matrix instruction takes them; fast_tile's sum is of the rounded ones.
 //
-// Bound: with many rows the matrix instructions and the softmax's vector instructions
-// between them share the issue slots (four wavefronts of a SIMD pair cannot hide all of
-// it: 969 of 1300 TFLOP/s); with one block per sequence the way of a tile through
-// registers and LDS, 0.65 us a tile and workgroup.  256 rows in a workgroup (W = 8)
-// halve that way's cost per row, 128 (W = 4) waste less where sequences have fewer:
-// 2048 tokens behind 30720, 1141 us with W = 8 and 1245 with W = 4; 61 behind 40003 with
-// 8 heads sharing, 77 and 84; 24 of up to 60 tokens with 4 sharing, 77 and 60.
+// Bound: the waits of a wavefront for its own steps (scores, softmax, outputs, one after
+// another), of which two wavefronts a SIMD hide a part: with many rows matrix instructions
+// are at work in 41% of the cycles and vector instructions in 49%, side by side where the
+// wavefronts' steps differ (900 to 975 of 1300 TFLOP/s); with 64 dimensions 14% and 40%.
+// With one block per sequence the way of a tile through registers and LDS, 0.65 us a tile
+// and workgroup.  256 rows in a workgroup (W = 8) halve that way's cost per row, 128
+// (W = 4) waste less where sequences have fewer: 2048 tokens behind 30720, 1141 us with
+// W = 8 and 1245 with W = 4; plan_of has others.
 // ---------------------------------------------------------------------------
 template <entro_dtype T, int D, int W>
 __global__ __launch_bounds__(64 * W, 2) void attn_chunk_kernel(ChunkArg a) {
@@ -1264,7 +1266,16 @@ static Plan plan_of(uint32_t n_seq, uint32_t total_q, uint32_t n_heads, uint32_t
   // kernel for few rows: 24 sequences of up to 16 tokens behind up to 6000, 32 / 8 heads
   // of 128 (34 rows on average), 38.6 us instead of 44.9; 4 tokens behind 40000 30.6
   // instead of 36.5.  Above that its blocks are too small: 16 tokens behind 40000 (64
-  // rows), 66.6 us instead of 59.4.
+  // rows), 66.6 us instead of 59.4.  (By heads of 64, 64 sequences of 40 rows behind 2000,
+  // 32 heads, 248 us and 256 with blocks of 128 rows, of 64 rows 252 and 257; 96, 314 and
+  // 316, then 334 and 325; of 128, 32 / 8 heads, the few rows' kernel is behind from some
+  // 32 rows on: of 24 rows 61 and 72, of 40 107 and 88.)
+  // Above 128 blocks of 256 rows.  The same sequences with 128 rows, blocks of 256 and of
+  // 128: 428 and 319 us with heads of 64, 493 and 389 of 96, 137 and 105 of 128; with 160
+  // rows 506 and 482, 575 and 629, 157 and 168; 16 with 1024 rows 632 and 638, 741 and 838,
+  // 186 and 213.  Where lengths spread over a factor of 32 the average stands for few of
+  // them, and blocks of 128 take less up to some 400 rows: 411 and 330 (182 rows on
+  // average), 596 and 566 (210), 177 and 161 (223).
   p.waves = rows > 128ull * n_seq ? 8u : rows > 48ull * n_seq ? 4u : 0u;
   p.rows = p.waves ? 32u * p.waves : rows > 32ull * n_seq ? 64u : rows > 16ull * n_seq ? 32u : 16u;
   p.heads = std::min(group, p.rows);
@@ -1357,7 +1368,6 @@ extern "C" entro_status entro_attn_chunk(const entro_kv_cache *c, const entro_kv
   k.cu = a->d_cu_q;
   k.lens = a->d_lens;
   k.total_q = a->total_q;
-  k.n_heads = a->n_heads;
   k.group = a->n_heads / c->n_kv_heads;
   k.heads = p.heads;
   k.parts = p.parts;

@@ -12,7 +12,7 @@ namespace entro {
 struct KvSide {
   int8_t *codes;
   float *scales;
-  char *x;                     // 16-bit rows (written by the load)
+  char *x;                     // rows of the call's type (written by the load)
   int64_t stride_t, stride_h;  // bytes
 };
 struct KvArg {
@@ -55,9 +55,10 @@ __device__ __forceinline__ void kv_check(const KvArg &a, uint32_t page) {
 }
 
 // What a workgroup does: one page (the sequences' pages that take part are
-// numbered one after another) for one head, keys and values.  Neighbouring workgroups
-// take the pages of one head: with the heads of one page side by side, reading
-// 58371 tokens back took 98 us instead of 74.
+// numbered one after another) for one head, keys and values.  In the store and the load
+// neighbouring workgroups take the pages of one head: with the heads of one page side by
+// side, reading 58371 tokens back took 98 us instead of 74.  (The append, which has
+// queries between them, takes the heads of one page: see kv_append_kernel.)
 struct KvItem {
   bool any;            // whether there is an item, and a page
   uint32_t head;

@@ -28,8 +28,8 @@
  *   key codes    int8 [page][kv head][row][dim]
  *   value codes  int8 [page][kv head][dim][row]
  *   scales       float [page][kv head], one array for keys, one for values
- * and the value of a code is code * scale; scales are 0 or more (entro_attn_cache
- * takes value scales below 2^-126 as 0).  Values are held with a row's
+ * and the value of a code is code * scale; scales are 0 or more (entro_attn_cache and
+ * entro_attn_chunk take value scales below 2^-126 as 0).  Values are held with a row's
  * tokens side by side because the product with the attention weights runs
  * along the tokens.  A page belongs to one sequence while it is written;
  * pages that are only read may be shared.
